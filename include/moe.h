@@ -397,6 +397,91 @@ moe_status moe_ffn_dgrad1_mx(const moe_shape* s, const uint8_t* dabq_rows, const
                              void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Around the expert layer: what a learned router trains on, and the norms of the block that
+ * the layer sits in.
+ * --------------------------------------------------------------------------------------- */
+
+/* Balance loss, router z-loss and per-expert counts of a batch's routing.
+ * A token t is kept unless mask[t] is 0 (a padded batch; mask NULL keeps all) or none of its
+ * scores is above -inf; a token left out enters nothing, whatever its scores hold (inf, NaN).
+ * Over the N kept tokens, with p = softmax(logits[t]) over all E experts:
+ *   counts[e] = c_e, how often topk_idx of a kept token names expert e;  counts[E] = N
+ *   prob_mean[e] = mean p_e;  lse[t] = log sum_e exp(logits[t, e]) (-inf for a token left out)
+ *   loss[0] = E / (k N) sum_e c_e prob_mean[e]  (1 when choices and probabilities are even)
+ *   loss[1] = mean lse[t]^2
+ * N = 0 gives zero losses and means.  Scores may be -inf (an expert out of use: p = 0).  Ids
+ * outside [0, E) are clamped.  logits [T, E] float, topk_idx [T, k], mask [T] u8 or NULL; lse [T]
+ * float, counts [E + 1] int32, prob_mean [E] and loss [2] float written.  Sums over tokens are
+ * float inside a workgroup and double across workgroups. */
+moe_status moe_balance_fwd(const moe_shape* s, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                           float* lse, int32_t* counts, float* prob_mean, float* loss, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* Gradient of dloss[0] loss[0] + dloss[1] loss[1] w.r.t. the scores (counts have none), with the
+ * gates' gradient in the same pass:
+ *   dlogits[t, e] = p_e (dloss[0] E / (k N) (c_e / N - sum_e' p_e' c_e' / N) + 2 dloss[1] lse[t] / N)
+ *                   + (e chosen by t: g_e (dgates_e - sum_j g_j dgates_j), as moe_route_bwd)
+ * dgates, gates, topk_idx [T, k]: all three, or dgates NULL for the losses' gradient alone.  A
+ * token left out (lse -inf) keeps its gates' gradient.  dlogits [T, E] float written in full; with
+ * dloss zero it equals moe_route_bwd's.  dloss [2] float, on the device.
+ * Ranks of a data-parallel job that add up counts (all E + 1 of them) between the two calls get
+ * the gradient of the losses over all their tokens.  These gradients are not zero outside a
+ * token's chosen experts: the router's input gradient then needs moe_router_bwd's dx_r
+ * (moe_permute_bwd_router reads the chosen experts only). */
+moe_status moe_balance_bwd(const moe_shape* s, const float* logits, const float* lse, const int32_t* counts,
+                           const float* dloss, const float* dgates, const float* gates, const int32_t* topk_idx,
+                           float* dlogits, void* stream);
+
+/* Norms before and after a block, with the block's gate and residual scale.
+ * r(z) = 1 / sqrt(mean(z^2) + eps) over a row of d, a = res_scale, g = gate[t] (1 if gate is NULL):
+ *   v[t]  = x[t] + a g (y[t] r(y[t]) w_post)     x [T, d], y [T, d] the block's output
+ *   xn[t] = v[t] r(v[t]) w_pre                   the input of what follows
+ * y NULL: no block ends here, v is x and is not written (a norm before a block alone).  w_post
+ * NULL: y enters without a norm.  w_pre NULL: no norm follows, xn and rstd_pre stay NULL.  A gate
+ * of exactly 0 drops the branch whatever y holds.  x, y, w_post [d], w_pre [d], v, xn act; gate
+ * [T] float; rstd_post, rstd_pre [T] float: r(y) and r(v) for the backward (with w_post, w_pre).
+ * v may be x (in place).  Each stored row is rounded once; xn is taken from the unrounded v.
+ * Needs d <= 16384, eps > 0 and finite res_scale; a pointer that the call has no use for (xn
+ * without w_pre, gate without y, ...) is MOE_EINVAL. */
+moe_status moe_block_norm_fwd(const moe_shape* s, const void* x, const void* y, const float* gate,
+                              const void* w_post, const void* w_pre, float res_scale, float eps, void* v, void* xn,
+                              float* rstd_post, float* rstd_pre, void* stream);
+
+/* Backward of moe_block_norm_fwd.  dv [T, d] act (may be NULL with w_pre) and dxn [T, d] (with
+ * w_pre): gradients of v and xn.  v: the stored one (x where y is NULL).  With vh = v rstd_pre,
+ * yh = y rstd_post and D the gradient of v from both of its uses,
+ *   D = dv + rstd_pre (w_pre dxn - vh mean(vh w_pre dxn));  dx = D
+ *   dy = a g rstd_post (w_post D - yh mean(yh w_post D));   dgate[t] = a sum(D w_post yh)
+ *   dw_post = a sum_t g D yh;                               dw_pre = sum_t dxn vh
+ * (without w_post: dy = a g D, dgate = a sum(D y)).  A gate of 0 gives dy = 0 and adds nothing to
+ * dw_post; its dgate is as above.  dx, dy [T, d] act; dgate [T], dw_post [d], dw_pre [d] float,
+ * each of the last three NULL if not wanted.  dx may be dv (in place).  ws is needed with dw_post
+ * or dw_pre: partial sums, added in a fixed order. */
+moe_status moe_block_norm_bwd(const moe_shape* s, const void* dv, const void* dxn, const void* v, const void* y,
+                              const float* gate, const void* w_post, const void* w_pre, const float* rstd_post,
+                              const float* rstd_pre, float res_scale, void* dx, void* dy, float* dgate,
+                              float* dw_post, float* dw_pre, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_combine and moe_block_norm_fwd in one pass: y[t] = y_add[t] + sum_j gates[t, j] *
+ * y_perm[slot_row[t, j]] (float, y_add first, then j in order) is normed from registers and not
+ * stored.  Arguments as in those calls. */
+moe_status moe_combine_norm(const moe_shape* s, const void* y_perm, const float* gates, const int32_t* slot_row,
+                            const void* y_add, const void* x, const float* gate, const void* w_post,
+                            const void* w_pre, float res_scale, float eps, void* v, void* xn, float* rstd_post,
+                            float* rstd_pre, void* stream);
+
+/* Backward of moe_combine_norm: moe_block_norm_bwd's outputs, and moe_combine_bwd's from the
+ * unrounded dy: dy_perm[slot_row[t, j]] = gates[t, j] dy[t], dgates[t, j] = <dy[t],
+ * y_perm[slot_row[t, j]]>.  y is rebuilt from the gathered rows.  dy [T, d] (the gradient of
+ * y_add) may be NULL.  dy_perm must not be y_perm. */
+moe_status moe_combine_norm_bwd(const moe_shape* s, const void* dv, const void* dxn, const void* v,
+                                const void* y_perm, const float* gates, const int32_t* slot_row, const void* y_add,
+                                const float* gate, const void* w_post, const void* w_pre, const float* rstd_post,
+                                const float* rstd_pre, float res_scale, void* dx, void* dy, void* dy_perm,
+                                float* dgates, float* dgate, float* dw_post, float* dw_pre, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * moe_tuning_reload: forget the tuning overrides read so far (see the file header), so each
  * is read from the environment again at its next use.  For tuning sweeps and tests that
  * change them within one process; it must not run while another host thread launches

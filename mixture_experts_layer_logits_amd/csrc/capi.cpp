@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <cstdlib>
@@ -13,6 +14,7 @@
 #include <tuple>
 
 #include "../../include/moe.h"
+#include "block.h"
 #include "gemm.h"
 #include "mx.h"
 #include "route.h"
@@ -76,6 +78,12 @@ inline hipStream_t S(void* st) { return static_cast<hipStream_t>(st); }
 
 inline moe_status launched(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ELAUNCH; }
 
+#define MOE_TRY(expr)                 \
+  do {                                \
+    moe_status _st = (expr);          \
+    if (_st != MOE_OK) return _st;    \
+  } while (0)
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int elem_bytes(const moe_shape* s) { return s->act == MOE_F32 ? 4 : 2; }
@@ -126,11 +134,62 @@ moe_status check_rows(const moe_shape* s, std::initializer_list<const void*> ps)
 
 bool rows_ok(const moe_shape* s, const void* p) { return p || s->T == 0; }
 
-#define MOE_TRY(expr)                 \
-  do {                                \
-    moe_status _st = (expr);          \
-    if (_st != MOE_OK) return _st;    \
-  } while (0)
+// Block-norm arguments that do not depend on the batch: the width the kernels hold, a positive
+// eps (forward) and a finite residual scale.
+moe_status check_norm(const moe_shape* s, float res_scale, float eps) {
+  MOE_TRY(check_shape(s));
+  if (s->d > kNormMaxWidth) return MOE_EINVAL;
+  if (!std::isfinite(res_scale) || !std::isfinite(eps) || !(eps > 0.f)) return MOE_EINVAL;
+  return MOE_OK;
+}
+
+// optional row or weight buffers: 16-byte aligned when given
+moe_status check_opt(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (p && !aligned16(p)) return MOE_EALIGN;
+  return MOE_OK;
+}
+
+// Forward of both norm entry points.  branch: the call has a block output to add (y, or routed
+// rows already checked by the caller).
+moe_status norm_fwd(const moe_shape* s, bool branch, const NormFwd& a, hipStream_t st) {
+  if (s->T == 0) return MOE_OK;
+  if (!branch && !a.w_pre) return MOE_EINVAL;                              // nothing to compute
+  if (!branch && (a.w_post || a.gate || a.v || a.rstd_post)) return MOE_EINVAL;  // nothing they apply to
+  if (!a.w_pre && (a.xn || a.rstd_pre)) return MOE_EINVAL;
+  if (!a.w_post && a.rstd_post) return MOE_EINVAL;
+  MOE_TRY(check_ptrs({a.x}));
+  if (branch) MOE_TRY(check_ptrs({a.v}));
+  if (a.w_pre) MOE_TRY(check_ptrs({a.xn}));
+  if ((a.w_pre && !a.rstd_pre) || (a.w_post && !a.rstd_post)) return MOE_ENULL;
+  MOE_TRY(check_opt({a.y, a.w_post, a.w_pre, a.y_add}));
+  return launched(block_norm_forward(elem_bytes(s), a, st));
+}
+
+moe_status norm_bwd(const moe_shape* s, bool branch, const NormBwd& a, size_t ws_bytes, hipStream_t st) {
+  if (a.dw_post || a.dw_pre) {
+    MOE_TRY(check_opt({a.dw_post, a.dw_pre}));
+    if (!a.part) return MOE_ENULL;
+    if (!aligned16(a.part)) return MOE_EALIGN;
+    if (ws_bytes < norm_workspace_bytes(s->T, s->d)) return MOE_EWORKSPACE;
+  }
+  if (s->T > 0) {
+    if (!branch && !a.w_pre) return MOE_EINVAL;
+    if (!branch && (a.w_post || a.gate || a.dy || a.dgate)) return MOE_EINVAL;
+    if (!a.w_pre && (a.dxn || a.dw_pre)) return MOE_EINVAL;
+    if (!a.w_post && a.dw_post) return MOE_EINVAL;
+    if (!a.gate && a.dgate) return MOE_EINVAL;
+    if (!a.w_pre && !a.dv) return MOE_ENULL;  // no gradient comes in
+    MOE_TRY(check_ptrs({a.dx}));
+    if (a.w_pre) {
+      MOE_TRY(check_ptrs({a.dxn, a.v}));
+      if (!a.rstd_pre) return MOE_ENULL;
+    }
+    if (a.w_post && !a.rstd_post) return MOE_ENULL;
+    MOE_TRY(check_opt({a.dv, a.v, a.y, a.w_post, a.w_pre, a.y_add, a.dy}));
+  }
+  return launched(block_norm_backward(elem_bytes(s), a, st));
+}
 
 GemmShape gshape(const moe_shape* s) { return GemmShape{s->T * s->k, s->d, s->f, s->E}; }
 
@@ -167,6 +226,10 @@ size_t moe_workspace_size(const moe_shape* s) {
     const size_t m = mx_workspace_bytes(s->T * s->k, s->d, s->f, s->E);
     if (m > b) b = m;
   }
+  const size_t bal = balance_workspace_bytes(s->T, s->E);
+  if (bal > b) b = bal;
+  const size_t nrm = s->d <= kNormMaxWidth ? norm_workspace_bytes(s->T, s->d) : 0;
+  if (nrm > b) b = nrm;
   return ((b + 255) / 256) * 256 + 256;
 }
 
@@ -579,6 +642,95 @@ moe_status moe_ffn_dgrad1_mx(const moe_shape* s, const uint8_t* dabq_rows, const
   if (ws_bytes < mx_workspace_bytes(g.R, g.d, g.f, g.E)) return MOE_EWORKSPACE;
   return launched(dgrad1_mx(g, offsets, nullptr, (const bf16_t*)W1, (const bf16_t*)W3, (bf16_t*)dx_perm, ws, S(st),
                             MxIn{dabq_rows, dabs_rows}));
+}
+
+// ---------------------------------------------------------------------------------------
+// Around the expert layer: balance loss, block norms, combine with norms
+// ---------------------------------------------------------------------------------------
+moe_status moe_balance_fwd(const moe_shape* s, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                           float* lse, int32_t* counts, float* prob_mean, float* loss, void* ws, size_t ws_bytes,
+                           void* st) {
+  MOE_TRY(check_shape(s));
+  if (!rows_ok(s, logits) || !rows_ok(s, topk_idx) || !rows_ok(s, lse)) return MOE_ENULL;
+  if (!counts || !prob_mean || !loss || !ws) return MOE_ENULL;
+  if (!aligned16(ws)) return MOE_EALIGN;
+  if (ws_bytes < balance_workspace_bytes(s->T, s->E)) return MOE_EWORKSPACE;
+  return launched(balance_forward(s->T, s->E, s->k, logits, topk_idx, mask, lse, counts, prob_mean, loss, ws, S(st)));
+}
+
+moe_status moe_balance_bwd(const moe_shape* s, const float* logits, const float* lse, const int32_t* counts,
+                           const float* dloss, const float* dgates, const float* gates, const int32_t* topk_idx,
+                           float* dlogits, void* st) {
+  MOE_TRY(check_shape(s));
+  if (!rows_ok(s, logits) || !rows_ok(s, lse) || !rows_ok(s, dlogits)) return MOE_ENULL;
+  if (!counts || !dloss) return MOE_ENULL;
+  if (dgates && (!gates || !topk_idx)) return MOE_ENULL;
+  return launched(
+      balance_backward(s->T, s->E, s->k, logits, lse, counts, dloss, dgates, gates, topk_idx, dlogits, S(st)));
+}
+
+moe_status moe_block_norm_fwd(const moe_shape* s, const void* x, const void* y, const float* gate,
+                              const void* w_post, const void* w_pre, float res_scale, float eps, void* v, void* xn,
+                              float* rstd_post, float* rstd_pre, void* st) {
+  MOE_TRY(check_norm(s, res_scale, eps));
+  NormFwd a{};
+  a.T = s->T; a.d = s->d;
+  a.x = x; a.y = y; a.w_post = w_post; a.w_pre = w_pre; a.gate = gate;
+  a.res_scale = res_scale; a.eps = eps;
+  a.v = v; a.xn = xn; a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+  return norm_fwd(s, y != nullptr, a, S(st));
+}
+
+moe_status moe_block_norm_bwd(const moe_shape* s, const void* dv, const void* dxn, const void* v, const void* y,
+                              const float* gate, const void* w_post, const void* w_pre, const float* rstd_post,
+                              const float* rstd_pre, float res_scale, void* dx, void* dy, float* dgate,
+                              float* dw_post, float* dw_pre, void* ws, size_t ws_bytes, void* st) {
+  MOE_TRY(check_norm(s, res_scale, 1.f));
+  if (s->T > 0 && y && !dy) return MOE_ENULL;
+  NormBwd a{};
+  a.T = s->T; a.d = s->d;
+  a.dv = dv; a.dxn = dxn; a.v = v; a.y = y; a.gate = gate; a.w_post = w_post; a.w_pre = w_pre;
+  a.rstd_post = rstd_post; a.rstd_pre = rstd_pre; a.res_scale = res_scale;
+  a.dx = dx; a.dy = dy; a.dgate = dgate; a.dw_post = dw_post; a.dw_pre = dw_pre;
+  a.part = static_cast<float*>(ws);
+  return norm_bwd(s, y != nullptr, a, ws_bytes, S(st));
+}
+
+moe_status moe_combine_norm(const moe_shape* s, const void* y_perm, const float* gates, const int32_t* slot_row,
+                            const void* y_add, const void* x, const float* gate, const void* w_post,
+                            const void* w_pre, float res_scale, float eps, void* v, void* xn, float* rstd_post,
+                            float* rstd_pre, void* st) {
+  MOE_TRY(check_norm(s, res_scale, eps));
+  MOE_TRY(check_rows(s, {y_perm}));
+  if (!rows_ok(s, gates) || !rows_ok(s, slot_row)) return MOE_ENULL;
+  NormFwd a{};
+  a.T = s->T; a.d = s->d; a.k = s->k;
+  a.x = x; a.y_perm = y_perm; a.y_add = y_add; a.gates = gates; a.slot_row = slot_row;
+  a.w_post = w_post; a.w_pre = w_pre; a.gate = gate;
+  a.res_scale = res_scale; a.eps = eps;
+  a.v = v; a.xn = xn; a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+  return norm_fwd(s, true, a, S(st));
+}
+
+moe_status moe_combine_norm_bwd(const moe_shape* s, const void* dv, const void* dxn, const void* v,
+                                const void* y_perm, const float* gates, const int32_t* slot_row, const void* y_add,
+                                const float* gate, const void* w_post, const void* w_pre, const float* rstd_post,
+                                const float* rstd_pre, float res_scale, void* dx, void* dy, void* dy_perm,
+                                float* dgates, float* dgate, float* dw_post, float* dw_pre, void* ws,
+                                size_t ws_bytes, void* st) {
+  MOE_TRY(check_norm(s, res_scale, 1.f));
+  MOE_TRY(check_rows(s, {y_perm, dy_perm}));
+  if (!rows_ok(s, gates) || !rows_ok(s, slot_row) || !rows_ok(s, dgates)) return MOE_ENULL;
+  if (y_perm && y_perm == dy_perm) return MOE_EINVAL;
+  NormBwd a{};
+  a.T = s->T; a.d = s->d; a.k = s->k;
+  a.dv = dv; a.dxn = dxn; a.v = v; a.y_perm = y_perm; a.y_add = y_add; a.gates = gates; a.slot_row = slot_row;
+  a.gate = gate; a.w_post = w_post; a.w_pre = w_pre; a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+  a.res_scale = res_scale;
+  a.dx = dx; a.dy = dy; a.dy_perm = dy_perm; a.dgates = dgates; a.dgate = dgate; a.dw_post = dw_post;
+  a.dw_pre = dw_pre;
+  a.part = static_cast<float*>(ws);
+  return norm_bwd(s, true, a, ws_bytes, S(st));
 }
 
 }  // extern "C"
