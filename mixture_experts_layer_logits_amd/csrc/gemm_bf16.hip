@@ -421,7 +421,9 @@ struct PipeOperand {
     for (int i = 0; i < PER_THREAD; i++)
       st.ptr[i] = reinterpret_cast<const char*>(rowptr(k0 + (wave + NW * i) * ROWS_PER_SEG) + col0);
     st.k_left = live ? k_end - k0 : 0;
-    st.col_bytes = (uint32_t)((col_end - col0 < BMN ? col_end - col0 : BMN) * 2);
+    // whole 16-byte loads: one that only begins inside the range would read as zero.  Rows whose
+    // width is no multiple of 8 (the router's score gradients) are padded with zero columns.
+    st.col_bytes = (uint32_t)(((col_end - col0 < BMN ? col_end - col0 : BMN) * 2 + 15) & ~15);
   }
   // the next k-step of the same rows
   static __device__ __forceinline__ void next(Stream& st) {
