@@ -430,4 +430,4 @@ def moe_combine_norm_bwd(shape, dv, dxn, v, y_perm, gates, slot_row, y_add, gate
                    dy, dy_perm, dgates, dgate, dw_post, dw_pre, ws, _nbytes(ws)), stream)
 
 
-from .layer import MoEExpertLayer  # noqa: E402  (re-export)
+from .layer import MoEBlock, MoEExpertLayer  # noqa: E402  (re-export)

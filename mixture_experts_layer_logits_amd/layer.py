@@ -57,6 +57,17 @@ inputs, so bit-identical ``ab`` and ``h``) before the gradient GEMMs.  This trad
 extra GEMM1 per step for R * 3f activation elements held between the passes, the
 memory / throughput trade the pages report for recomputing activations (unite.ai,
 section "Παραλληλισμός, Ακρίβεια και Τεχνικές Μνήμης").
+
+Router losses (``balance=(w_balance, w_z)``, learned routing): the forward also runs
+moe_balance_fwd, which leaves the balance loss and the z-loss in ``loss``, the kept tokens'
+per-expert counts in ``bal_counts`` and the mean probabilities in ``prob_mean``; ``mask`` (uint8
+[T], 0 = padding) leaves tokens out of all of them.  The backward then takes the gradient of
+w_balance loss[0] + w_z loss[1] with the gates' (moe_balance_bwd instead of moe_route_bwd).  That
+gradient reaches every expert's score, so the router's input gradient is the dense
+dlogits Wr (``router_dx_fused`` is off).
+
+``MoEBlock`` puts the layer between its norms: v = h + res_scale gate (norm(y) w_post) with
+y = MoE(norm(h) w_pre), and the norm of the next block in the same pass.
 """
 from __future__ import annotations
 
@@ -68,7 +79,8 @@ from . import (MOE_BF16, MOE_F32, MOE_MX_DGRAD1, MOE_MX_DGRAD2, MOE_MX_GEMM1, MO
                moe_ffn_dgrad1, moe_ffn_dgrad2, moe_ffn_dgrad2_mx, moe_ffn_gemm1_fwd, moe_ffn_gemm1_fwd_mx,
                moe_ffn_gemm2_fwd, moe_ffn_wgrad1, moe_ffn_wgrad1_mx, moe_ffn_wgrad2, moe_ffn_wgrad2_mx, moe_mx_cols_ld,
                moe_permute, moe_permute_bwd, moe_permute_bwd_router, moe_permute_mx, moe_route, moe_route_bwd,
-               moe_route_given, moe_router_bwd,
+               moe_route_given, moe_router_bwd, moe_balance_bwd, moe_balance_fwd, moe_block_norm_bwd,
+               moe_block_norm_fwd, moe_combine_norm, moe_combine_norm_bwd,
                moe_router_fwd, moe_workspace_size, mx_scope_bits)
 
 # the GEMMs that read the dispatched rows: all four must run MXFP8 for the MXFP8 dispatch
@@ -77,12 +89,14 @@ _DISPATCH_READERS = MOE_MX_GEMM1 | MOE_MX_WGRAD1 | MOE_MX_DGRAD2 | MOE_MX_WGRAD2
 
 class MoEExpertLayer:
     def __init__(self, T, d, f, E, k, act=MOE_BF16, gemm=None, device="cuda", recompute=False, shared_f=0,
-                 mx_dispatch=None, mx_scope=0, mx_fused_quant=True, router_dx_fused=True):
+                 mx_dispatch=None, mx_scope=0, mx_fused_quant=True, router_dx_fused=True, balance=None):
         self.shape = make_shape(T, d, f, E, k, act, gemm, mx_scope)
         self.recompute = recompute
         # the router's input gradient folded into the un-permute (k rows of Wr per token)
         # instead of a dense dlogits Wr GEMM written to dx_r and read back
-        self.router_dx_fused = bool(router_dx_fused)
+        # (the router losses' gradient is not zero outside the k chosen experts)
+        self.router_dx_fused = bool(router_dx_fused) and balance is None
+        self.balance = balance
         bits = mx_scope_bits(self.shape)
         # MXFP8 operands written by the producing bf16 GEMM's epilogue
         self.fq_h = bool(mx_fused_quant) and bool(bits & MOE_MX_GEMM2) and not bits & MOE_MX_GEMM1
@@ -141,6 +155,11 @@ class MoEExpertLayer:
         self.dlogits = e(T, E, dtype=f32)
         self.dx_r = None if self.router_dx_fused else e(T, d)
         self.dWr = e(E, d, dtype=f32)
+        if balance is not None:
+            w_balance, w_z = (float(w) for w in balance)
+            self.dloss = torch.tensor([w_balance, w_z], dtype=f32, device=dev)
+            self.lse, self.prob_mean, self.loss = e(T, dtype=f32), e(E, dtype=f32), e(2, dtype=f32)
+            self.bal_counts = e(E + 1, dtype=i32)
         self.dx = e(T, d)
         self.ws = torch.empty(moe_workspace_size(self.shape), dtype=torch.uint8, device=dev)
         self.learned = True
@@ -160,21 +179,37 @@ class MoEExpertLayer:
             self.ws_s = torch.empty(moe_workspace_size(self.shape_s), dtype=torch.uint8, device=dev)
 
     # -------------------------------------------------------------- forward
-    def route(self, x=None, Wr=None, bias=None, topk_idx=None):
+    def _check_losses(self, topk_idx, mask):
+        if (self.balance is not None and topk_idx is not None) or (self.balance is None and mask is not None):
+            raise ValueError("the router losses need learned routing, and a mask needs the router losses")
+
+    def route(self, x=None, Wr=None, bias=None, topk_idx=None, mask=None):
         s = self.shape
+        self._check_losses(topk_idx, mask)
         if topk_idx is None:
             self.learned = True
             moe_router_fwd(s, x, Wr, bias, self.logits)
             moe_route(s, self.logits, self.topk_idx, self.gates, self.counts, self.offsets, self.slot_row, self.ws)
+            if self.balance is not None:
+                moe_balance_fwd(s, self.logits, self.topk_idx, mask, self.lse, self.bal_counts, self.prob_mean,
+                                self.loss, self.ws)
         else:  # the caller's ids are only read; the layer's own topk_idx buffer is left alone
             self.learned = False
             moe_route_given(s, topk_idx, self.counts, self.offsets, self.slot_row, self.dev_err, self.ws)
 
-    def forward(self, x, W1, W3, W2, Wr=None, bias=None, topk_idx=None, gates=None, shared=None):
-        """shared: (W1s [1, fs, d], W3s [1, fs, d], W2s [1, d, fs]) of the shared expert."""
+    def forward(self, x, W1, W3, W2, Wr=None, bias=None, topk_idx=None, gates=None, shared=None, mask=None):
+        """shared: (W1s [1, fs, d], W3s [1, fs, d], W2s [1, d, fs]) of the shared expert.
+        mask: uint8 [T], 0 for a token the router losses leave out."""
+        y_add = self._experts_forward(x, W1, W3, W2, Wr, bias, topk_idx, gates, shared, mask)
+        moe_combine(self.shape, self.y_perm, self._params[-1], self.slot_row, y_add, self.y)
+        return self.y
+
+    def _experts_forward(self, x, W1, W3, W2, Wr, bias, topk_idx, gates, shared, mask):
+        """The forward up to the routed rows y_perm; returns the shared expert's output or None."""
         s = self.shape
+        self._check_losses(topk_idx, mask)
         self.steps += 1
-        self.route(x, Wr, bias, topk_idx)
+        self.route(x, Wr, bias, topk_idx, mask)
         g = self.gates if topk_idx is None else gates
         self._params = (x, W1, W3, W2, Wr, g)
         self._shared = shared
@@ -203,18 +238,24 @@ class MoEExpertLayer:
             moe_ffn_gemm2_fwd(s, self.h, W2, self.offsets, self.y_perm, self.ws)
         if self.recompute:  # the SwiGLU activations are not kept for the backward
             self.ab = self.h = None
-        moe_combine(s, self.y_perm, g, self.slot_row, y_add, self.y)
-        return self.y
+        return y_add
 
     # -------------------------------------------------------------- backward
-    def backward(self, dy):
-        s = self.shape
-        x, W1, W3, W2, Wr, g = self._params
+    def backward(self, dy, dloss=None):
+        """dloss: float32 [2] on the GPU, the weights of the router losses in place of the layer's."""
+        s, g = self.shape, self._params[-1]
         if self.mx_dispatch:
             moe_combine_bwd_mx(s, dy, self.y_perm, g, self.slot_row, self.row_src, self.offsets, self.dgates,
                                self.dyq_rows, self.dys_rows, self.dyq_cols, self.dys_cols)
         else:
             moe_combine_bwd(s, dy, self.y_perm, g, self.slot_row, self.dy_perm, self.dgates)
+        return self._experts_backward(dy, dloss)
+
+    def _experts_backward(self, dy, dloss=None):
+        """The backward behind the combine's: dy_perm and dgates are in place, dy is read by the
+        shared expert alone."""
+        s = self.shape
+        x, W1, W3, W2, Wr, g = self._params
         if self.recompute:  # regenerate a, b and h from the kept routed rows
             self.ab, self.h = self._e(self.R, 2 * self.f), self._e(self.R, self.f)
             self._gemm1(W1, W3)
@@ -235,7 +276,11 @@ class MoEExpertLayer:
                 moe_ffn_dgrad1(s, self.dab, W1, W3, self.offsets, self.dx_perm, self.ws)
         dx_r = None
         if self.learned:
-            moe_route_bwd(s, self.dgates, g, self.topk_idx, self.dlogits)
+            if self.balance is not None:
+                moe_balance_bwd(s, self.logits, self.lse, self.bal_counts, self.dloss if dloss is None else dloss,
+                                self.dgates, g, self.topk_idx, self.dlogits)
+            else:
+                moe_route_bwd(s, self.dgates, g, self.topk_idx, self.dlogits)
             moe_router_bwd(s, x, Wr, self.dlogits, self.dx_r, self.dWr, self.ws)
             dx_r = self.dx_r
         dx_add = None
@@ -292,6 +337,81 @@ class MoEExpertLayer:
         return n
 
 
+class MoEBlock:
+    """An expert layer between its norms (RMS norms over d, learned scales w_pre and w_post):
+
+      xn = norm(h) w_pre;  y = MoE(xn);  v = h + res_scale gate (norm(y) w_post)
+      xn_next = norm(v) w_next      the next block's xn, in the pass that writes v
+
+    forward   moe_block_norm_fwd (unless xn is given) -> the layer's calls up to y_perm
+              -> moe_combine_norm
+    backward  moe_combine_norm_bwd -> the layer's calls from dy_perm on
+              -> moe_block_norm_bwd (unless xn was given)
+
+    y is never stored: the combine's norm takes it from registers and the backward gathers it
+    again.  A layer with the MXFP8 dispatch writes its routed gradient rows in E4M3 from dy, so
+    there the combine and the norm are separate calls.  The block owns its buffers and holds one
+    forward at a time, like its layer, and its calls run on the current stream."""
+
+    def __init__(self, layer: MoEExpertLayer, res_scale=1.0, eps=1e-6):
+        self.layer, self.res_scale, self.eps = layer, float(res_scale), float(eps)
+        e, T, d, f32 = layer._e, layer.T, layer.d, torch.float32
+        self.xn, self.v, self.xn_next = e(T, d), e(T, d), e(T, d)
+        self.rstd_pre, self.rstd_post, self.rstd_next = e(T, dtype=f32), e(T, dtype=f32), e(T, dtype=f32)
+        self.dv, self.dh, self.dy = e(T, d), e(T, d), e(T, d)
+        self.dgate = e(T, dtype=f32)
+        self.dw_pre, self.dw_post, self.dw_next = e(d, dtype=f32), e(d, dtype=f32), e(d, dtype=f32)
+
+    def forward(self, h, W1, W3, W2, w_pre=None, w_post=None, gate=None, w_next=None, xn=None, Wr=None, bias=None,
+                topk_idx=None, gates=None, shared=None, mask=None):
+        """h [T, d]; w_pre, or xn = norm(h) w_pre from the block before (its xn_next); w_post [d] or
+        None (no norm behind the layer); gate float32 [T] or None; w_next [d] or None.  The rest
+        as MoEExpertLayer.forward.  Returns v; xn_next is left in the block."""
+        if (xn is None) == (w_pre is None):
+            raise ValueError("a block takes w_pre, or the xn of the block before")
+        L, s = self.layer, self.layer.shape
+        self._own_pre = xn is None
+        if self._own_pre:
+            xn = self.xn
+            moe_block_norm_fwd(s, h, None, None, None, w_pre, 1.0, self.eps, None, xn, None, self.rstd_pre)
+        y_add = L._experts_forward(xn, W1, W3, W2, Wr, bias, topk_idx, gates, shared, mask)
+        g = L._params[-1]
+        self._saved = (h, gate, w_pre, w_post, w_next, y_add)
+        out = (gate, w_post, w_next, self.res_scale, self.eps, self.v, None if w_next is None else self.xn_next,
+               None if w_post is None else self.rstd_post, None if w_next is None else self.rstd_next)
+        if L.mx_dispatch:
+            moe_combine(s, L.y_perm, g, L.slot_row, y_add, L.y)
+            moe_block_norm_fwd(s, h, L.y, *out)
+        else:
+            moe_combine_norm(s, L.y_perm, g, L.slot_row, y_add, h, *out)
+        return self.v
+
+    def backward(self, dv, dxn_next=None, dloss=None):
+        """dv [T, d] (None: v was used through xn_next only), dxn_next [T, d] with w_next, dloss as
+        MoEExpertLayer.backward.  Returns dh; with a given xn, (dh, dxn) for the block before.
+        dw_pre, dw_post, dw_next, dgate and the layer's gradients are left in their buffers."""
+        L, s = self.layer, self.layer.shape
+        h, gate, w_pre, w_post, w_next, y_add = self._saved
+        mid = (gate, w_post, w_next, None if w_post is None else self.rstd_post,
+               None if w_next is None else self.rstd_next, self.res_scale, self.dv)
+        tail = (None if gate is None else self.dgate, None if w_post is None else self.dw_post,
+                None if w_next is None else self.dw_next, L.ws)
+        g = L._params[-1]
+        if L.mx_dispatch:
+            moe_block_norm_bwd(s, dv, dxn_next, self.v, L.y, *mid, self.dy, *tail)
+            moe_combine_bwd_mx(s, self.dy, L.y_perm, g, L.slot_row, L.row_src, L.offsets, L.dgates, L.dyq_rows,
+                               L.dys_rows, L.dyq_cols, L.dys_cols)
+        else:
+            moe_combine_norm_bwd(s, dv, dxn_next, self.v, L.y_perm, g, L.slot_row, y_add, *mid,
+                                 None if y_add is None else self.dy, L.dy_perm, L.dgates, *tail)
+        dxn = L._experts_backward(self.dy, dloss)
+        if not self._own_pre:
+            return self.dv, dxn
+        moe_block_norm_bwd(s, self.dv, dxn, h, None, None, None, w_pre, None, self.rstd_pre, 1.0, self.dh, None, None,
+                           None, self.dw_pre, L.ws)
+        return self.dh
+
+
 class MoEExpertFunction(torch.autograd.Function):
     """y = MoE(x) with learned routing (optional constant per-expert router bias);
     gradients for x, Wr, W1, W3, W2.  The layer's buffers hold one forward at a time, so
@@ -315,3 +435,34 @@ class MoEExpertFunction(torch.autograd.Function):
                                "activations are gone (one layer object per in-flight forward)")
         L.backward(dy.contiguous())
         return L.dx.clone(), L.dWr.to(L.dtype), L.dW1.clone(), L.dW3.clone(), L.dW2.clone(), None, None
+
+
+class MoEBlockFunction(torch.autograd.Function):
+    """v, loss = block(h) with learned routing; gradients for h, w_pre, w_post, gate (float32 [T]
+    or None), Wr, W1, W3, W2.  loss is the layer's float32 [2] of router losses (balance, z), to
+    be weighted into the objective like any other value; its weights in the layer are not used.
+    The layer must have been made with ``balance``.  One forward at a time, as MoEExpertFunction."""
+
+    @staticmethod
+    def forward(ctx, h, w_pre, w_post, gate, Wr, W1, W3, W2, block: MoEBlock, bias=None, mask=None):
+        L = block.layer
+        if L.balance is None:
+            raise ValueError("MoEBlockFunction needs a layer with router losses (balance=(w_balance, w_z))")
+        c = lambda t: None if t is None else t.contiguous()  # noqa: E731
+        v = block.forward(c(h), c(W1), c(W3), c(W2), w_pre=c(w_pre), w_post=c(w_post), gate=c(gate), Wr=c(Wr),
+                          bias=c(bias), mask=c(mask))
+        ctx.block, ctx.step = block, L.steps
+        return v.clone(), L.loss.clone()
+
+    @staticmethod
+    def backward(ctx, dv, dloss):
+        B, L = ctx.block, ctx.block.layer
+        if L.steps != ctx.step:
+            raise RuntimeError("MoEBlockFunction: the layer ran another forward since this one; its saved "
+                               "activations are gone (one block object per in-flight forward)")
+        dh = B.backward(dv.contiguous(), dloss=dloss.contiguous())
+        _, gate, w_pre, w_post, _, _ = B._saved
+        dt = L.dtype
+        return (dh.clone(), B.dw_pre.to(dt), None if w_post is None else B.dw_post.to(dt),
+                None if gate is None else B.dgate.clone(), L.dWr.to(dt), L.dW1.clone(), L.dW3.clone(), L.dW2.clone(),
+                None, None, None)
