@@ -27,131 +27,199 @@ namespace {
 
 enum Src { kNone = 0, kLoad = 1, kGather = 2 };  // the branch y: absent, read, gathered from routed rows
 
+// Sum over the wave, the same in every lane: four exchanges inside each row of 16 lanes, then
+// the rows' sums passed on to lane 63 and read from there.  Register exchanges (DPP) take a
+// fraction of the time of six shuffles through the LDS crossbar, and the row sums stand on the
+// critical path of every row.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float wave_total(float v) {
+  v = dpp_add<0xB1, 0xF>(v);   // quad_perm [1,0,3,2]
+  v = dpp_add<0x4E, 0xF>(v);   // quad_perm [2,3,0,1]
+  v = dpp_add<0x141, 0xF>(v);  // row_half_mirror: the other quad of each 8
+  v = dpp_add<0x140, 0xF>(v);  // row_mirror: the other 8 of each 16
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast15 into rows 1 and 3
+  v = dpp_add<0x143, 0xC>(v);  // row_bcast31 into rows 2 and 3
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
 // Sums over the WPR waves of a row.  Consecutive sums alternate between two LDS buffers, so one
 // barrier each is enough: a buffer is written again only after a later barrier.
 template <int WPR, int NWAVES>
 struct RowSum {
-  float (*buf)[NWAVES];
+  float (*buf)[NWAVES][4];
+  int wave;
   int at = 0;
-  __device__ __forceinline__ float operator()(float v) {
-    v = wave_sum(v);
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    static_assert(N <= 4, "a buffer holds 4 sums a wave");
+#pragma unroll
+    for (int n = 0; n < N; n++) v[n] = wave_total(v[n]);
     if constexpr (WPR > 1) {
-      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-      if (lane == 0) buf[at][wave] = v;
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int n = 0; n < N; n++) buf[at][wave][n] = v[n];
       __syncthreads();
       const int w0 = wave / WPR * WPR;
-      v = 0.f;
 #pragma unroll
-      for (int w = 0; w < WPR; w++) v += buf[at][w0 + w];
+      for (int n = 0; n < N; n++) {
+        v[n] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WPR; w++) v[n] += buf[at][w0 + w][n];
+      }
       at ^= 1;
     }
-    return v;
+  }
+  __device__ __forceinline__ float operator()(float v) {
+    float a[1] = {v};
+    (*this)(a);
+    return a[0];
   }
 };
 
-template <int C>
-__device__ __forceinline__ void zero(float (&v)[C][8]) {
-#pragma unroll
-  for (int i = 0; i < C; i++)
-#pragma unroll
-    for (int c = 0; c < 8; c++) v[i][c] = 0.f;
-}
+// 8 consecutive elements as they lie in memory; rows are held in this form until used, so a
+// bf16 row costs half the registers of its floats.
+template <typename T> struct Raw;
+template <> struct Raw<bf16_t> {
+  uint4 q;
+  __device__ __forceinline__ void clear() { q = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const bf16_t* p) { q = *reinterpret_cast<const uint4*>(p); }
+  // nothing: the compiler may not carry the floats of an earlier use across this point
+  __device__ __forceinline__ void repack() { asm volatile("" : "+v"(q.x), "+v"(q.y), "+v"(q.z), "+v"(q.w)); }
+  __device__ __forceinline__ float operator[](int i) const {
+    const uint32_t w = i < 2 ? q.x : i < 4 ? q.y : i < 6 ? q.z : q.w;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
+template <> struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void repack() {}
+  __device__ __forceinline__ float operator[](int i) const {
+    return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
+  }
+};
 
-template <int C>
-__device__ __forceinline__ float dot(const float (&a)[C][8], const float (&b)[C][8]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < C; i++)
-#pragma unroll
-    for (int c = 0; c < 8; c++) s = fmaf(a[i][c], b[i][c], s);
-  return s;
-}
+#define MOE_EACH(i, c)           \
+  _Pragma("unroll") for (int i = 0; i < C; i++) \
+  _Pragma("unroll") for (int c = 0; c < 8; c++)
 
-// A lane's share of a row: chunks first + i * step (i < C) of 8 columns, those below nchunk
+// A lane's share of a row: chunks first + i * step (i < C) of 8 columns.  Chunks past the row
+// read as zero (they enter row sums) and are not stored.
 template <typename T, int C>
 struct Lane {
   int first, step, nchunk;
-  __device__ __forceinline__ void load(const T* row, float (&v)[C][8]) const {
+  __device__ __forceinline__ void load(const void* row0, int64_t at, Raw<T> (&v)[C]) const {
+    const T* row = static_cast<const T*>(row0) + at;
 #pragma unroll
-    for (int i = 0; i < C; i++)
-      if (first + i * step < nchunk) load8<T>(row + (first + i * step) * 8, v[i]);
+    for (int i = 0; i < C; i++) {
+      v[i].clear();
+      if (first + i * step < nchunk) v[i].load(row + (first + i * step) * 8);
+    }
   }
-  __device__ __forceinline__ void store(T* row, const float (&v)[C][8]) const {
+  __device__ __forceinline__ void store(void* row0, int64_t at, const float (&v)[C][8]) const {
+    T* row = static_cast<T*>(row0) + at;
 #pragma unroll
     for (int i = 0; i < C; i++)
       if (first + i * step < nchunk) store8<T>(row + (first + i * step) * 8, v[i]);
   }
 };
 
-// y[t] = y_add[t] + sum_j gates[t, j] y_perm[slot_row[t, j]], j in order
+// Routed rows are loaded kBatch at a time, all loads before the first use.  With k <= kBatch the
+// backward keeps them for the gate gradients instead of gathering them again.
+constexpr int kBatch = 4;
+
 template <typename T, int C>
-__device__ __forceinline__ void gather(const Lane<T, C>& ln, int64_t t, int d, int k, const T* y_perm, const T* y_add,
-                                       const float* gates, const int32_t* slot_row, float (&y)[C][8]) {
-  zero(y);
-  if (y_add) ln.load(y_add + t * d, y);
-  for (int j = 0; j < k; j++) {
-    const float g = gates[t * k + j];
-    float r[C][8];
-    zero(r);
-    ln.load(y_perm + (int64_t)slot_row[t * k + j] * d, r);
+struct Gather {
+  const void* y_perm;
+  const float* gates;       // of this token
+  const int32_t* slot_row;  // of this token
+  int k, d;
+  Raw<T> rows[kBatch][C];
+  __device__ __forceinline__ void load(const Lane<T, C>& ln, int j0) {
 #pragma unroll
-    for (int i = 0; i < C; i++)
-#pragma unroll
-      for (int c = 0; c < 8; c++) y[i][c] = fmaf(g, r[i][c], y[i][c]);
+    for (int j = 0; j < kBatch; j++)
+      if (j0 + j < k) ln.load(y_perm, (int64_t)slot_row[j0 + j] * d, rows[j]);
   }
-}
+  // y += sum_j gates[j] rows[j], j in order
+  __device__ __forceinline__ void sum(int j0, float (&y)[C][8]) const {
+#pragma unroll
+    for (int j = 0; j < kBatch; j++)
+      if (j0 + j < k) {
+        const float g = gates[j0 + j];
+        MOE_EACH(i, c) y[i][c] = fmaf(g, rows[j][i][c], y[i][c]);
+      }
+  }
+};
 
 template <typename T, int WPR, int C, int NWAVES, int SRC>
 __global__ void __launch_bounds__(NWAVES * 64) norm_fwd_kernel(const NormFwd a) {
   constexpr int RPB = NWAVES / WPR;
-  __shared__ float s_red[2][NWAVES];
-  RowSum<WPR, NWAVES> row_sum{s_red};
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float s_red[2][NWAVES][4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowSum<WPR, NWAVES> row_sum{s_red, wave};
   const Lane<T, C> ln{(wave % WPR) * kWave + lane, WPR * kWave, a.d / 8};
   const float inv_d = 1.f / (float)a.d;
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.T; base += (int64_t)gridDim.x * RPB) {
-    const int64_t t = base + wave / WPR;
-    const bool in = t < a.T;
+    // waves past the last row repeat it without storing (row sums may hold barriers)
+    const bool in = base + wave / WPR < a.T;
+    const int64_t t = in ? base + wave / WPR : a.T - 1;
+    const int64_t at = t * a.d;
     float v[C][8];
-    zero(v);
-    if (in) ln.load(static_cast<const T*>(a.x) + t * a.d, v);
+    Raw<T> x[C], w_post[C], w_pre[C];
+    ln.load(a.x, at, x);
     if constexpr (SRC != kNone) {
       float y[C][8];
-      zero(y);
-      if (in) {
-        if constexpr (SRC == kLoad) ln.load(static_cast<const T*>(a.y) + t * a.d, y);
-        else
-          gather<T, C>(ln, t, a.d, a.k, static_cast<const T*>(a.y_perm), static_cast<const T*>(a.y_add), a.gates,
-                       a.slot_row, y);
+      if constexpr (SRC == kLoad) {
+        Raw<T> raw[C];
+        ln.load(a.y, at, raw);
+        if (a.w_post) ln.load(a.w_post, 0, w_post);
+        if (a.w_pre) ln.load(a.w_pre, 0, w_pre);
+        MOE_EACH(i, c) y[i][c] = raw[i][c];
+      } else {
+        Gather<T, C> ga{a.y_perm, a.gates + t * a.k, a.slot_row + t * a.k, a.k, a.d};
+        Raw<T> raw[C];
+        ga.load(ln, 0);
+        if (a.y_add) ln.load(a.y_add, at, raw);
+        if (a.w_post) ln.load(a.w_post, 0, w_post);
+        if (a.w_pre) ln.load(a.w_pre, 0, w_pre);
+        MOE_EACH(i, c) y[i][c] = a.y_add ? raw[i][c] : 0.f;
+        ga.sum(0, y);
+        for (int j = kBatch; j < a.k; j += kBatch) {
+          ga.load(ln, j);
+          ga.sum(j, y);
+        }
       }
-      const float g = a.gate && in ? a.gate[t] : 1.f;
+      const float g = a.gate ? a.gate[t] : 1.f;
       float coef = a.res_scale * g;
       if (a.w_post) {
-        const float r = rsqrtf(row_sum(dot(y, y)) * inv_d + a.eps);
+        float ss = 0.f;
+        MOE_EACH(i, c) ss = fmaf(y[i][c], y[i][c], ss);
+        const float r = rsqrtf(row_sum(ss) * inv_d + a.eps);
         coef *= r;
         if (in && ln.first == 0) a.rstd_post[t] = r;
+        MOE_EACH(i, c) y[i][c] *= w_post[i][c];
       }
-      if (g != 0.f) {  // a closed gate drops the branch, whatever it holds
-        float w[C][8];
-        zero(w);  // columns past the row must stay zero: they enter the next row sum
-        if (a.w_post) ln.load(static_cast<const T*>(a.w_post), w);
-#pragma unroll
-        for (int i = 0; i < C; i++)
-#pragma unroll
-          for (int c = 0; c < 8; c++) v[i][c] = fmaf(coef * y[i][c], a.w_post ? w[i][c] : 1.f, v[i][c]);
-      }
-      if (in) ln.store(static_cast<T*>(a.v) + t * a.d, v);
+      // a closed gate drops the branch, whatever it holds
+      MOE_EACH(i, c) v[i][c] = g != 0.f ? fmaf(coef, y[i][c], x[i][c]) : x[i][c];
+      if (in) ln.store(a.v, at, v);
+    } else {
+      ln.load(a.w_pre, 0, w_pre);
+      MOE_EACH(i, c) v[i][c] = x[i][c];
     }
     if (a.w_pre) {
-      const float r = rsqrtf(row_sum(dot(v, v)) * inv_d + a.eps);
+      float ss = 0.f;
+      MOE_EACH(i, c) ss = fmaf(v[i][c], v[i][c], ss);
+      const float r = rsqrtf(row_sum(ss) * inv_d + a.eps);
+      MOE_EACH(i, c) v[i][c] = v[i][c] * r * w_pre[i][c];
       if (in) {
-        float w[C][8];
-        ln.load(static_cast<const T*>(a.w_pre), w);
-#pragma unroll
-        for (int i = 0; i < C; i++)
-#pragma unroll
-          for (int c = 0; c < 8; c++) v[i][c] = v[i][c] * r * w[i][c];
-        ln.store(static_cast<T*>(a.xn) + t * a.d, v);
+        ln.store(a.xn, at, v);
         if (ln.first == 0) a.rstd_pre[t] = r;
       }
     }
@@ -159,111 +227,136 @@ __global__ void __launch_bounds__(NWAVES * 64) norm_fwd_kernel(const NormFwd a) 
 }
 
 template <typename T, int WPR, int C, int NWAVES, int SRC>
-__global__ void __launch_bounds__(NWAVES * 64) norm_bwd_kernel(const NormBwd a) {
+__global__ void __launch_bounds__(NWAVES * 64)
+    __attribute__((amdgpu_waves_per_eu(4))) norm_bwd_kernel(const NormBwd a) {
   constexpr int RPB = NWAVES / WPR;
-  __shared__ float s_red[2][NWAVES];
+  __shared__ float s_red[2][NWAVES][4];
   __shared__ float s_acc[RPB > 1 ? NWAVES * kWave * 8 : 1];
-  RowSum<WPR, NWAVES> row_sum{s_red};
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowSum<WPR, NWAVES> row_sum{s_red, wave};
   const Lane<T, C> ln{(wave % WPR) * kWave + lane, WPR * kWave, a.d / 8};
   const float inv_d = 1.f / (float)a.d;
   float acc_pre[C][8], acc_post[C][8];
-  zero(acc_pre);
-  zero(acc_post);
+  MOE_EACH(i, c) acc_pre[i][c] = acc_post[i][c] = 0.f;
+
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.T; base += (int64_t)gridDim.x * RPB) {
-    const int64_t t = base + wave / WPR;
-    const bool in = t < a.T;
-    float D[C][8];
-    zero(D);
-    if (in && a.dv) ln.load(static_cast<const T*>(a.dv) + t * a.d, D);
+    // waves past the last row repeat it: nothing of theirs is stored or added to the weights' sums
+    const bool in = base + wave / WPR < a.T;
+    const int64_t t = in ? base + wave / WPR : a.T - 1;
+    const int64_t at = t * a.d;
+    const float* gates = a.gates + t * a.k;
+    const int32_t* slots = a.slot_row + t * a.k;
+    Raw<T> dv[C], dxn[C], v[C], w_pre[C], w_post[C], y_raw[C];
+    Raw<T> rows[SRC == kGather ? kBatch : 1][C];
+    if constexpr (SRC == kGather) {
+#pragma unroll
+      for (int j = 0; j < kBatch; j++)
+        if (j < a.k) ln.load(a.y_perm, (int64_t)slots[j] * a.d, rows[j]);
+      if (a.y_add) ln.load(a.y_add, at, y_raw);
+    }
+    if constexpr (SRC == kLoad) ln.load(a.y, at, y_raw);
     if (a.w_pre) {
-      float vh[C][8], u[C][8], w[C][8];
-      zero(vh);
-      zero(u);
-      zero(w);
-      if (in) {
-        ln.load(static_cast<const T*>(a.v) + t * a.d, vh);
-        ln.load(static_cast<const T*>(a.dxn) + t * a.d, u);
-        ln.load(static_cast<const T*>(a.w_pre), w);
+      ln.load(a.v, at, v);
+      ln.load(a.dxn, at, dxn);
+      ln.load(a.w_pre, 0, w_pre);
+    }
+    if (a.dv) ln.load(a.dv, at, dv);
+    if constexpr (SRC != kNone)
+      if (a.w_post) ln.load(a.w_post, 0, w_post);
+
+    float D[C][8];
+    MOE_EACH(i, c) D[i][c] = a.dv ? dv[i][c] : 0.f;
+    if (a.w_pre) {
+      const float r = a.rstd_pre[t];
+      float s = 0.f;
+      MOE_EACH(i, c) {
+        const float q = dxn[i][c] * (v[i][c] * r);
+        s = fmaf(q, w_pre[i][c], s);
+        acc_pre[i][c] += in ? q : 0.f;
       }
-      const float r = in ? a.rstd_pre[t] : 0.f;
+      const float m = row_sum(s) * inv_d * r;  // mean(vh w_pre dxn) r
 #pragma unroll
-      for (int i = 0; i < C; i++)
+      for (int i = 0; i < C; i++) {
+        v[i].repack();
+        dxn[i].repack();
+        w_pre[i].repack();
+      }
+      MOE_EACH(i, c) D[i][c] = fmaf(r, fmaf(-m, v[i][c], dxn[i][c] * w_pre[i][c]), D[i][c]);
+    }
+    if (in) ln.store(a.dx, at, D);
+    if constexpr (SRC != kNone) {
+      float y[C][8];
+      if constexpr (SRC == kLoad) {
+        MOE_EACH(i, c) y[i][c] = y_raw[i][c];
+      } else {
+        MOE_EACH(i, c) y[i][c] = a.y_add ? y_raw[i][c] : 0.f;
 #pragma unroll
-        for (int c = 0; c < 8; c++) {
-          vh[i][c] *= r;
-          acc_pre[i][c] = fmaf(u[i][c], vh[i][c], acc_pre[i][c]);
-          u[i][c] *= w[i][c];
+        for (int j = 0; j < kBatch; j++)
+          if (j < a.k) {
+            const float gj = gates[j];
+            MOE_EACH(i, c) y[i][c] = fmaf(gj, rows[j][i][c], y[i][c]);
+#pragma unroll
+            for (int i = 0; i < C; i++) rows[j][i].repack();
+          }
+        for (int j = kBatch; j < a.k; j++) {
+          Raw<T> row[C];
+          ln.load(a.y_perm, (int64_t)slots[j] * a.d, row);
+          const float gj = gates[j];
+          MOE_EACH(i, c) y[i][c] = fmaf(gj, row[i][c], y[i][c]);
         }
-      const float m = row_sum(dot(vh, u)) * inv_d;
-#pragma unroll
-      for (int i = 0; i < C; i++)
-#pragma unroll
-        for (int c = 0; c < 8; c++) D[i][c] = fmaf(r, fmaf(-m, vh[i][c], u[i][c]), D[i][c]);
-    }
-    float y[C][8];
-    if constexpr (SRC != kNone) {
-      zero(y);
-      if (in) {
-        if constexpr (SRC == kLoad) ln.load(static_cast<const T*>(a.y) + t * a.d, y);
-        else
-          gather<T, C>(ln, t, a.d, a.k, static_cast<const T*>(a.y_perm), static_cast<const T*>(a.y_add), a.gates,
-                       a.slot_row, y);
       }
-    }
-    if (in) ln.store(static_cast<T*>(a.dx) + t * a.d, D);
-    if constexpr (SRC != kNone) {
-      const float g = a.gate && in ? a.gate[t] : 1.f;
+      const float g = a.gate ? a.gate[t] : 1.f;
       const bool open = g != 0.f;
       const float ag = a.res_scale * g;
       if (a.w_post) {
-        const float r = in ? a.rstd_post[t] : 0.f;
-        float w[C][8];
-        zero(w);
-        ln.load(static_cast<const T*>(a.w_post), w);
-#pragma unroll
-        for (int i = 0; i < C; i++)
-#pragma unroll
-          for (int c = 0; c < 8; c++) {
-            y[i][c] *= r;
-            if (open) acc_post[i][c] = fmaf(ag * D[i][c], y[i][c], acc_post[i][c]);
-            D[i][c] *= w[i][c];
-          }
-        const float s = row_sum(dot(D, y));
+        const float r = a.rstd_post[t];
+        const bool adds = in && open;
+        float s = 0.f;
+        MOE_EACH(i, c) {
+          y[i][c] *= r;
+          const float q = D[i][c] * y[i][c];
+          acc_post[i][c] += adds ? ag * q : 0.f;
+          s = fmaf(q, w_post[i][c], s);
+          D[i][c] *= w_post[i][c];
+        }
+        s = row_sum(s);
         if (in && a.dgate && ln.first == 0) a.dgate[t] = a.res_scale * s;
         const float m = s * inv_d, ar = ag * r;
-#pragma unroll
-        for (int i = 0; i < C; i++)
-#pragma unroll
-          for (int c = 0; c < 8; c++) D[i][c] = open ? ar * fmaf(-m, y[i][c], D[i][c]) : 0.f;
+        MOE_EACH(i, c) D[i][c] = open ? ar * fmaf(-m, y[i][c], D[i][c]) : 0.f;
       } else {
         if (a.dgate) {
-          const float s = row_sum(dot(D, y));
+          float s = 0.f;
+          MOE_EACH(i, c) s = fmaf(D[i][c], y[i][c], s);
+          s = row_sum(s);
           if (in && ln.first == 0) a.dgate[t] = a.res_scale * s;
         }
-#pragma unroll
-        for (int i = 0; i < C; i++)
-#pragma unroll
-          for (int c = 0; c < 8; c++) D[i][c] = open ? ag * D[i][c] : 0.f;
+        MOE_EACH(i, c) D[i][c] = open ? ag * D[i][c] : 0.f;
       }
-      if (in && a.dy) ln.store(static_cast<T*>(a.dy) + t * a.d, D);
+      if (in && a.dy) ln.store(a.dy, at, D);
       if constexpr (SRC == kGather) {
-        for (int j = 0; j < a.k; j++) {
-          float p[C][8];
-          zero(p);
-          if (in) {
-            const int64_t row = (int64_t)a.slot_row[t * a.k + j] * a.d;
-            ln.load(static_cast<const T*>(a.y_perm) + row, p);
-            const float gj = a.gates[t * a.k + j];
-            float o[C][8];
-#pragma unroll
-            for (int i = 0; i < C; i++)
-#pragma unroll
-              for (int c = 0; c < 8; c++) o[i][c] = gj * D[i][c];
-            ln.store(static_cast<T*>(a.dy_perm) + row, o);
+        auto routed = [&](int j, const Raw<T>(&row)[C]) {  // one row of dy_perm; this lane's part of dgates
+          const float gj = gates[j];
+          float o[C][8];
+          float s = 0.f;
+          MOE_EACH(i, c) {
+            s = fmaf(D[i][c], row[i][c], s);
+            o[i][c] = gj * D[i][c];
           }
-          const float s = row_sum(dot(D, p));
-          if (in && ln.first == 0) a.dgates[t * a.k + j] = s;
+          if (in) ln.store(a.dy_perm, (int64_t)slots[j] * a.d, o);
+          return s;
+        };
+        float s[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; j++) s[j] = j < a.k ? routed(j, rows[j]) : 0.f;
+        row_sum(s);
+        if (in && ln.first == 0)
+#pragma unroll
+          for (int j = 0; j < kBatch; j++)
+            if (j < a.k) a.dgates[t * a.k + j] = s[j];
+        for (int j = kBatch; j < a.k; j++) {
+          ln.load(a.y_perm, (int64_t)slots[j] * a.d, rows[0]);
+          const float sj = row_sum(routed(j, rows[0]));
+          if (in && ln.first == 0) a.dgates[t * a.k + j] = sj;
         }
       }
     }
@@ -299,47 +392,55 @@ __global__ void __launch_bounds__(NWAVES * 64) norm_bwd_kernel(const NormBwd a) 
   if (a.dw_pre) reduce(acc_pre, a.part + ((int64_t)gridDim.x + blockIdx.x) * a.d);
 }
 
-// dw[c] = sum over the G workgroups, in order, of part[g][c]: 64 columns per workgroup, 16 runs
-// of rows that meet in LDS.  blockIdx.y: dw_post, dw_pre.
+// dw[c] = sum over the G workgroups of part[g][c], in a fixed order: 16 columns per workgroup, 64
+// runs of rows that meet in LDS (a launch of d / 16 workgroups keeps every load of a run in
+// flight; 64 columns each left most of the chip idle).  blockIdx.y: dw_post, dw_pre.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(int d, int G, const float* __restrict__ part,
                                                        float* __restrict__ dw_post, float* __restrict__ dw_pre) {
-  __shared__ float s[16][64];
+  constexpr int COLS = 16, RUNS = 64;
+  __shared__ float s[RUNS][COLS];
   float* out = blockIdx.y == 0 ? dw_post : dw_pre;
   if (!out) return;
-  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
-  const float* p = part + (int64_t)blockIdx.y * G * d + col;
+  const int col = threadIdx.x % COLS, run = threadIdx.x / COLS;
+  const float* p = part + (int64_t)blockIdx.y * G * d + blockIdx.x * COLS + col;
   float sum = 0.f;
-  for (int g = run; g < G; g += 16) sum += p[(int64_t)g * d];
-  s[run][lane] = sum;
+#pragma unroll 4
+  for (int g = run; g < G; g += RUNS) sum += p[(int64_t)g * d];
+  s[run][col] = sum;
   __syncthreads();
-  if (run == 0) {
-    sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < 16; r++) sum += s[r][lane];
-    out[col] = sum;
+  for (int n = RUNS / 2; n > 0; n /= 2) {
+    if (run < n) s[run][col] += s[run + n][col];
+    __syncthreads();
   }
+  if (run == 0) out[blockIdx.x * COLS + col] = s[0][col];
 }
 
 // Calls f(WPR, C, NWAVES) with the waves per row, chunks per lane and waves per workgroup that
 // hold a row of d.
-template <class F>
-hipError_t for_width(int d, F&& f) {
-#define MOE_NORM_CASE(WPR, C, NWAVES)                                                                \
-  if (d <= WPR * C * 512)                                                                            \
+#define MOE_NORM_CASE(WPR, C, NWAVES) \
+  if (d <= WPR * C * 512) \
     return f(std::integral_constant<int, WPR>{}, std::integral_constant<int, C>{}, std::integral_constant<int, NWAVES>{});
+template <class F>
+hipError_t for_width_fwd(int d, F&& f) {
   MOE_NORM_CASE(1, 1, 4) MOE_NORM_CASE(1, 2, 4) MOE_NORM_CASE(2, 2, 4) MOE_NORM_CASE(4, 2, 4) MOE_NORM_CASE(8, 2, 8)
   MOE_NORM_CASE(16, 2, 16)
-#undef MOE_NORM_CASE
   return hipErrorInvalidValue;
 }
+template <class F>
+hipError_t for_width_bwd(int d, F&& f) {
+  MOE_NORM_CASE(1, 1, 8) MOE_NORM_CASE(2, 1, 8) MOE_NORM_CASE(4, 1, 8) MOE_NORM_CASE(8, 1, 8) MOE_NORM_CASE(16, 1, 16)
+  MOE_NORM_CASE(16, 2, 16)
+  return hipErrorInvalidValue;
+}
+#undef MOE_NORM_CASE
 
 // one pass of rows per workgroup; more rows than a launch holds threads for go round again
 constexpr int64_t kNormFwdBlocks = 1 << 20;
 
 template <typename T>
 hipError_t fwd_t(const NormFwd& a, hipStream_t st) {
-  return for_width(a.d, [&](auto wpr, auto c, auto nw) {
+  return for_width_fwd(a.d, [&](auto wpr, auto c, auto nw) {
     constexpr int RPB = nw() / wpr();
     const int64_t rows = ((int64_t)a.T + RPB - 1) / RPB;
     const dim3 grid((unsigned)(rows < kNormFwdBlocks ? rows : kNormFwdBlocks)), block(nw() * 64);
@@ -358,7 +459,7 @@ int bwd_grid(int T, int rpb) {
 template <typename T>
 hipError_t bwd_t(const NormBwd& a, hipStream_t st) {
   int G = 0;
-  const hipError_t err = for_width(a.d, [&](auto wpr, auto c, auto nw) {
+  const hipError_t err = for_width_bwd(a.d, [&](auto wpr, auto c, auto nw) {
     G = bwd_grid(a.T, nw() / wpr());
     if (G == 0) return hipSuccess;
     const dim3 grid(G), block(nw() * 64);
@@ -368,7 +469,7 @@ hipError_t bwd_t(const NormBwd& a, hipStream_t st) {
     return hipGetLastError();
   });
   if (err != hipSuccess || (!a.dw_post && !a.dw_pre)) return err;
-  hipLaunchKernelGGL(norm_dw_kernel, dim3(a.d / 64, 2), dim3(1024), 0, st, a.d, G, a.part, a.dw_post, a.dw_pre);
+  hipLaunchKernelGGL(norm_dw_kernel, dim3(a.d / 16, 2), dim3(1024), 0, st, a.d, G, a.part, a.dw_post, a.dw_pre);
   return hipGetLastError();
 }
 
