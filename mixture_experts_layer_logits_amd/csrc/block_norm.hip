@@ -226,9 +226,16 @@ __global__ void __launch_bounds__(NWAVES * 64) norm_fwd_kernel(const NormFwd a) 
   }
 }
 
+// Waves per SIMD the registers are held to: 4 (128 registers), which the bf16 kernels meet; float
+// rows that gather would spill there (44 to 53 registers), so they get twice as many.
+template <typename T, int SRC, int NWAVES>
+constexpr int bwd_waves_per_eu() {
+  return sizeof(T) == 4 && SRC == kGather && NWAVES < 16 ? 2 : 4;
+}
+
 template <typename T, int WPR, int C, int NWAVES, int SRC>
 __global__ void __launch_bounds__(NWAVES * 64)
-    __attribute__((amdgpu_waves_per_eu(4))) norm_bwd_kernel(const NormBwd a) {
+    __attribute__((amdgpu_waves_per_eu(bwd_waves_per_eu<T, SRC, NWAVES>()))) norm_bwd_kernel(const NormBwd a) {
   constexpr int RPB = NWAVES / WPR;
   __shared__ float s_red[2][NWAVES][4];
   __shared__ float s_acc[RPB > 1 ? NWAVES * kWave * 8 : 1];
@@ -239,30 +246,54 @@ __global__ void __launch_bounds__(NWAVES * 64)
   float acc_pre[C][8], acc_post[C][8];
   MOE_EACH(i, c) acc_pre[i][c] = acc_post[i][c] = 0.f;
 
-  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.T; base += (int64_t)gridDim.x * RPB) {
-    // waves past the last row repeat it: nothing of theirs is stored or added to the weights' sums
-    const bool in = base + wave / WPR < a.T;
-    const int64_t t = in ? base + wave / WPR : a.T - 1;
-    const int64_t at = t * a.d;
-    const float* gates = a.gates + t * a.k;
-    const int32_t* slots = a.slot_row + t * a.k;
-    Raw<T> dv[C], dxn[C], v[C], w_pre[C], w_post[C], y_raw[C];
-    Raw<T> rows[SRC == kGather ? kBatch : 1][C];
-    if constexpr (SRC == kGather) {
-#pragma unroll
-      for (int j = 0; j < kBatch; j++)
-        if (j < a.k) ln.load(a.y_perm, (int64_t)slots[j] * a.d, rows[j]);
-      if (a.y_add) ln.load(a.y_add, at, y_raw);
-    }
-    if constexpr (SRC == kLoad) ln.load(a.y, at, y_raw);
+  // The gradient at v reads one set of rows (dv, dxn, v), the branch another (y, or the routed
+  // rows).  Each set's loads are issued before the other is worked on, the first one's a row
+  // ahead, so memory stays busy across the row sums without registers for a second row.
+  Raw<T> w_pre[C], w_post[C], dv[C], dxn[C], v[C], y_raw[C];
+  Raw<T> rows[SRC == kGather ? kBatch : 1][C];
+  const int64_t stride = (int64_t)gridDim.x * RPB;
+  int64_t next = (int64_t)blockIdx.x * RPB + wave / WPR;
+  // rows past the last one repeat it: nothing of them is stored or added to the weights' sums
+  auto clamped = [&](int64_t t) { return t < a.T ? t : (int64_t)a.T - 1; };
+  auto load_stream = [&](int64_t t) {
+    const int64_t at = clamped(t) * a.d;
     if (a.w_pre) {
       ln.load(a.v, at, v);
       ln.load(a.dxn, at, dxn);
-      ln.load(a.w_pre, 0, w_pre);
     }
     if (a.dv) ln.load(a.dv, at, dv);
-    if constexpr (SRC != kNone)
-      if (a.w_post) ln.load(a.w_post, 0, w_post);
+  };
+  int32_t slot[SRC == kGather ? kBatch : 1];  // the first routed rows of the next token
+  auto load_slots = [&](int64_t t) {
+    if constexpr (SRC == kGather) {
+#pragma unroll
+      for (int j = 0; j < kBatch; j++) slot[j] = j < a.k ? a.slot_row[clamped(t) * a.k + j] : 0;
+    }
+  };
+  load_slots(next);
+  load_stream(next);
+  if (a.w_pre) ln.load(a.w_pre, 0, w_pre);
+  if constexpr (SRC != kNone)
+    if (a.w_post) ln.load(a.w_post, 0, w_post);
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.T; base += stride) {
+    const bool in = next < a.T;
+    const int64_t t = clamped(next), at = t * a.d;
+    const float* gates = a.gates + t * a.k;
+    const int32_t* slots = a.slot_row + t * a.k;
+    next += stride;
+    if constexpr (SRC == kGather) {
+#pragma unroll
+      for (int j = 0; j < kBatch; j++)
+        if (j < a.k) ln.load(a.y_perm, (int64_t)slot[j] * a.d, rows[j]);
+      if (a.y_add) ln.load(a.y_add, at, y_raw);
+      load_slots(next);
+    }
+    if constexpr (SRC == kLoad) ln.load(a.y, at, y_raw);
+#pragma unroll
+    for (int i = 0; i < C; i++) {
+      w_pre[i].repack();
+      w_post[i].repack();
+    }
 
     float D[C][8];
     MOE_EACH(i, c) D[i][c] = a.dv ? dv[i][c] : 0.f;
@@ -284,6 +315,7 @@ __global__ void __launch_bounds__(NWAVES * 64)
       MOE_EACH(i, c) D[i][c] = fmaf(r, fmaf(-m, v[i][c], dxn[i][c] * w_pre[i][c]), D[i][c]);
     }
     if (in) ln.store(a.dx, at, D);
+    load_stream(next);
     if constexpr (SRC != kNone) {
       float y[C][8];
       if constexpr (SRC == kLoad) {
@@ -388,8 +420,9 @@ __global__ void __launch_bounds__(NWAVES * 64)
       if (wave < WPR && chunk < ln.nchunk) store8<float>(out + chunk * 8, sum);
     }
   };
-  if (a.dw_post) reduce(acc_post, a.part + (int64_t)blockIdx.x * a.d);
-  if (a.dw_pre) reduce(acc_pre, a.part + ((int64_t)gridDim.x + blockIdx.x) * a.d);
+  const bool alone = gridDim.x == 1;  // then the sums are whole
+  if (a.dw_post) reduce(acc_post, alone ? a.dw_post : a.part + (int64_t)blockIdx.x * a.d);
+  if (a.dw_pre) reduce(acc_pre, alone ? a.dw_pre : a.part + ((int64_t)gridDim.x + blockIdx.x) * a.d);
 }
 
 // dw[c] = sum over the G workgroups of part[g][c], in a fixed order: 16 columns per workgroup, 64
@@ -451,31 +484,39 @@ hipError_t fwd_t(const NormFwd& a, hipStream_t st) {
   });
 }
 
-int bwd_grid(int T, int rpb) {
+// Up to 4 rows a wave in one workgroup, which then needs no second launch (2.4 us) to add up
+// weight gradients; more rows take every resident workgroup, kNormBlocks at most.
+int bwd_grid(int T, int rpb, int resident) {
   const int64_t g = ((int64_t)T + rpb - 1) / rpb;
-  return (int)(g < kNormBlocks ? g : kNormBlocks);
+  if (g <= 4) return g > 0;
+  const int most = resident < kNormBlocks ? resident : kNormBlocks;
+  return (int)(g < most ? g : most);
 }
 
 template <typename T>
 hipError_t bwd_t(const NormBwd& a, hipStream_t st) {
   int G = 0;
   const hipError_t err = for_width_bwd(a.d, [&](auto wpr, auto c, auto nw) {
-    G = bwd_grid(a.T, nw() / wpr());
-    if (G == 0) return hipSuccess;
-    const dim3 grid(G), block(nw() * 64);
-    if (a.y_perm) hipLaunchKernelGGL((norm_bwd_kernel<T, wpr(), c(), nw(), kGather>), grid, block, 0, st, a);
-    else if (a.y) hipLaunchKernelGGL((norm_bwd_kernel<T, wpr(), c(), nw(), kLoad>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((norm_bwd_kernel<T, wpr(), c(), nw(), kNone>), grid, block, 0, st, a);
-    return hipGetLastError();
+    auto launch = [&](auto kern) {
+      G = bwd_grid(a.T, nw() / wpr(),
+                   device_cu_count() * kernel_occupancy(reinterpret_cast<const void*>(kern), nw() * 64, 0));
+      if (G > 0) hipLaunchKernelGGL(kern, dim3(G), dim3(nw() * 64), 0, st, a);
+      return G > 0 ? hipGetLastError() : hipSuccess;
+    };
+    if (a.y_perm) return launch(norm_bwd_kernel<T, wpr(), c(), nw(), kGather>);
+    if (a.y) return launch(norm_bwd_kernel<T, wpr(), c(), nw(), kLoad>);
+    return launch(norm_bwd_kernel<T, wpr(), c(), nw(), kNone>);
   });
-  if (err != hipSuccess || (!a.dw_post && !a.dw_pre)) return err;
+  if (err != hipSuccess || G == 1 || (!a.dw_post && !a.dw_pre)) return err;
   hipLaunchKernelGGL(norm_dw_kernel, dim3(a.d / 16, 2), dim3(1024), 0, st, a.d, G, a.part, a.dw_post, a.dw_pre);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t norm_workspace_bytes(int T, int d) { return (size_t)bwd_grid(T, 1) * d * 2 * sizeof(float); }
+size_t norm_workspace_bytes(int T, int d) {
+  return (size_t)(T < kNormBlocks ? T : kNormBlocks) * d * 2 * sizeof(float);
+}
 
 hipError_t block_norm_forward(int elem_bytes, const NormFwd& a, hipStream_t st) {
   if (a.T == 0) return hipSuccess;
