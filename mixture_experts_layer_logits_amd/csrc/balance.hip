@@ -9,11 +9,12 @@
 // c_e is a count and has no gradient.  Both passes read the scores once; what bounds them is HBM
 // at large T and launch latency below about 4 MB of scores.
 //
-// A token's scores lie across LPT lanes (a power of two, at most a wave), 4 consecutive experts
-// per 16-byte load and NV loads per lane, so a wave holds 64 / LPT tokens and the softmax takes
-// log2(LPT) exchange steps.  Column sums stay in registers over a wave's tokens and meet in a
-// fixed order: across the wave's tokens, the workgroup's waves, then the workgroups (a second
-// launch, in double), so the result is the same bits on every run.
+// A token's scores lie across LPT lanes (a power of two, at most a wave, and at least k), 4
+// consecutive experts per 16-byte load and NV loads per lane, so a wave holds 64 / LPT tokens, the
+// softmax takes log2(LPT) exchange steps, and lane j holds the token's choice j.  Column sums stay
+// in registers over a wave's tokens and meet in a fixed order: across the wave's tokens, the
+// workgroup's waves, then the workgroups (a second launch, in double), so the result is the same
+// bits on every run.
 #include <cmath>
 
 #include "block.h"
@@ -42,6 +43,18 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
+// lane j's value, of each group of LPT lanes
+template <int LPT>
+__device__ __forceinline__ float from_lane(float v, int j) {
+  if constexpr (LPT == kWave) return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
+  else return __shfl(v, j, LPT);
+}
+template <int LPT>
+__device__ __forceinline__ int from_lane(int v, int j) {
+  if constexpr (LPT == kWave) return __builtin_amdgcn_readlane(v, j);
+  else return __shfl(v, j, LPT);
+}
+
 // the 4 scores at columns e0 .. e0+3 of a row (columns past E: -inf)
 template <bool VEC>
 __device__ __forceinline__ void load_scores(const float* row, int e0, int E, float (&v)[4]) {
@@ -55,24 +68,74 @@ __device__ __forceinline__ void load_scores(const float* row, int e0, int E, flo
   }
 }
 
-// Partial sums per workgroup, in ws: prob [G][E] float, then count [G][E] int32, then
-// z [G] float and kept [G] int32.
+// Workspace: the sum kernel's meeting point, then one row of partial sums per workgroup.
+struct BalancePart {
+  double* dots;      // [kMaxExperts / kSumCols] a sum workgroup's share of sum_e c_e P_e
+  uint32_t* ticket;  // sum workgroups done; zeroed by the forward's first workgroup
+  float* prob;       // [G][E]
+  int32_t* count;    // [G][E]
+  float* z;          // [G]
+  int32_t* kept;     // [G]
+};
+constexpr int kSumCols = 64;
+constexpr size_t kPartHeader = 256;
+static_assert((kMaxExperts / kSumCols) * sizeof(double) + sizeof(uint32_t) <= kPartHeader, "header holds both");
+
+BalancePart carve(void* ws, int G, int E) {
+  BalancePart b;
+  b.dots = static_cast<double*>(ws);
+  b.ticket = reinterpret_cast<uint32_t*>(b.dots + kMaxExperts / kSumCols);
+  b.prob = reinterpret_cast<float*>(static_cast<char*>(ws) + kPartHeader);
+  b.count = reinterpret_cast<int32_t*>(b.prob + (size_t)G * E);
+  b.z = reinterpret_cast<float*>(b.count + (size_t)G * E);
+  b.kept = reinterpret_cast<int32_t*>(b.z + G);
+  return b;
+}
+
+__device__ __forceinline__ double wave_sum_double(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  return v;
+}
+
+// Column e's outputs from its whole sums; returns its term of sum_e c_e P_e.
+__device__ __forceinline__ double finish_column(int e, double prob, int count, double inv_n, int32_t* counts,
+                                                float* prob_mean) {
+  counts[e] = count;
+  prob_mean[e] = (float)(prob * inv_n);
+  return count * (prob * inv_n);
+}
+__device__ __forceinline__ void finish_loss(int E, int k, double dot, double z, int n, double inv_n, int32_t* counts,
+                                            float* loss) {
+  counts[E] = n;
+  loss[0] = (float)(dot * inv_n * E / k);
+  loss[1] = (float)(z * inv_n);
+}
+
+constexpr int kFwdThreads = 1024;
+constexpr int kFwdWaves = kFwdThreads / kWave;
+
+// What a lane loads of its token: its scores, its choice (lanes below k) and, a pass earlier, the
+// mask byte that decides whether there is anything to load.
 template <int LPT, int NV, bool VEC>
-__global__ void __launch_bounds__(kThreads) balance_fwd_kernel(int T, int E, int k, const float* __restrict__ logits,
-                                                               const int32_t* __restrict__ topk_idx,
-                                                               const uint8_t* __restrict__ mask,
-                                                               float* __restrict__ lse, float* __restrict__ part_p,
-                                                               int32_t* __restrict__ part_c,
-                                                               float* __restrict__ part_z,
-                                                               int32_t* __restrict__ part_n) {
+__global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(int T, int E, int k,
+                                                                  const float* __restrict__ logits,
+                                                                  const int32_t* __restrict__ topk_idx,
+                                                                  const uint8_t* __restrict__ mask,
+                                                                  float* __restrict__ lse, const BalancePart part,
+                                                                  int32_t* __restrict__ counts,
+                                                                  float* __restrict__ prob_mean,
+                                                                  float* __restrict__ loss) {
   constexpr int TW = kWave / LPT;  // tokens of a wave
+  constexpr int HALF = kFwdWaves / 2;
   __shared__ int s_cnt[kMaxExperts];
-  __shared__ float s_p[kWaves][kMaxExperts];
-  __shared__ float s_z[kWaves];
-  __shared__ int s_n[kWaves];
+  __shared__ float s_p[HALF][kMaxExperts];
+  __shared__ float s_z[kFwdWaves];
+  __shared__ int s_n[kFwdWaves];
+  __shared__ double s_dot[kFwdWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int q = lane % LPT, sub = lane / LPT;
-  for (int e = tid; e < E; e += kThreads) s_cnt[e] = 0;
+  for (int e = tid; e < E; e += kFwdThreads) s_cnt[e] = 0;
   __syncthreads();
   float acc[NV][4];
 #pragma unroll
@@ -81,20 +144,32 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(int T, int E, int
     for (int c = 0; c < 4; c++) acc[i][c] = 0.f;
   float z = 0.f;
   int n = 0;
-  const int64_t stride = (int64_t)gridDim.x * kWaves * TW;
-  for (int64_t t = ((int64_t)blockIdx.x * kWaves + wave) * TW + sub; t - sub < T; t += stride) {
-    const bool live = t < T && (!mask || mask[t] != 0);
-    float v[NV][4];
-    float top = kNegInf;
+  const int64_t stride = (int64_t)gridDim.x * kFwdWaves * TW;
+  int64_t t = ((int64_t)blockIdx.x * kFwdWaves + wave) * TW + sub;
+  auto live_at = [&](int64_t at) { return at < T && (!mask || mask[at] != 0); };
+  auto load = [&](int64_t at, bool live, float (&v)[NV][4], int& e) {
+    e = 0;
+    if (live && q < k) e = topk_idx[at * k + q];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       v[i][0] = v[i][1] = v[i][2] = v[i][3] = kNegInf;
-      if (live) load_scores<VEC>(logits + t * E, 4 * (q + LPT * i), E, v[i]);
+      if (live) load_scores<VEC>(logits + at * E, 4 * (q + LPT * i), E, v[i]);
+    }
+  };
+  float v[NV][4], ahead[NV][4];
+  int e, e_ahead;
+  load(t, live_at(t), v, e);
+  bool live_ahead = live_at(t + stride);
+  for (; t - sub < T; t += stride) {
+    load(t + stride, live_ahead, ahead, e_ahead);
+    live_ahead = live_at(t + 2 * stride);
+    float top = kNegInf;
+#pragma unroll
+    for (int i = 0; i < NV; i++)
 #pragma unroll
       for (int c = 0; c < 4; c++) top = (v[i][c] > top || v[i][c] != v[i][c]) ? v[i][c] : top;
-    }
     top = group_max<LPT>(top);
-    const bool kept = live && top != kNegInf;
+    const bool kept = top != kNegInf;  // a token left out holds -inf throughout
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; i++)
@@ -110,11 +185,7 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(int T, int E, int
       for (int i = 0; i < NV; i++)
 #pragma unroll
         for (int c = 0; c < 4; c++) acc[i][c] = fmaf(v[i][c], inv, acc[i][c]);
-      for (int j = q; j < k; j += LPT) {
-        int e = topk_idx[t * k + j];
-        e = e < 0 ? 0 : (e >= E ? E - 1 : e);
-        atomicAdd(&s_cnt[e], 1);
-      }
+      if (q < k) atomicAdd(&s_cnt[e < 0 ? 0 : (e >= E ? E - 1 : e)], 1);
     }
     if (q == 0 && t < T) {
       const float l = kept ? top + logf(sum) : kNegInf;
@@ -124,8 +195,14 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(int T, int E, int
         n++;
       }
     }
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+      for (int c = 0; c < 4; c++) v[i][c] = ahead[i][c];
+    e = e_ahead;
   }
-  // the wave's tokens, then the workgroup's waves
+  // the wave's tokens, then the workgroup's waves: the upper half hands its sums to the lower one,
+  // whose sums are then added column by column
 #pragma unroll
   for (int o = LPT; o < kWave; o <<= 1)
 #pragma unroll
@@ -134,102 +211,124 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(int T, int E, int
       for (int c = 0; c < 4; c++) acc[i][c] += __shfl_xor(acc[i][c], o, kWave);
   z = wave_sum(z);
   n = wave_sum_int(n);
-  if (sub == 0) {
-#pragma unroll
-    for (int i = 0; i < NV; i++)
-#pragma unroll
-      for (int c = 0; c < 4; c++) {
-        const int e = 4 * (q + LPT * i) + c;
-        if (e < E) s_p[wave][e] = acc[i][c];
-      }
-  }
   if (lane == 0) {
     s_z[wave] = z;
     s_n[wave] = n;
   }
-  __syncthreads();
-  for (int e = tid; e < E; e += kThreads) {
-    float p = 0.f;
+  auto each_column = [&](auto&& f) {
+    if (sub == 0) {
 #pragma unroll
-    for (int w = 0; w < kWaves; w++) p += s_p[w][e];
-    part_p[(int64_t)blockIdx.x * E + e] = p;
-    part_c[(int64_t)blockIdx.x * E + e] = s_cnt[e];
+      for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          const int col = 4 * (q + LPT * i) + c;
+          if (col < E) f(s_p[wave % HALF][col], acc[i][c]);
+        }
+    }
+  };
+  if (wave >= HALF) each_column([](float& s, float a) { s = a; });
+  __syncthreads();
+  if (wave < HALF) each_column([](float& s, float a) { s += a; });
+  __syncthreads();
+  z = 0.f;
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < kFwdWaves; w++) {
+    z += s_z[w];
+    n += s_n[w];
+  }
+  float p = 0.f;  // thread e < E: the workgroup's sum of column e
+  if (tid < E) {
+#pragma unroll
+    for (int w = 0; w < HALF; w++) p += s_p[w][tid];
+  }
+  if (gridDim.x == 1) {  // the sums are whole: no second launch
+    const double inv_n = n > 0 ? 1.0 / n : 0.0;
+    const double dot = wave_sum_double(tid < E ? finish_column(tid, p, s_cnt[tid], inv_n, counts, prob_mean) : 0.0);
+    if (lane == 0) s_dot[wave] = dot;
+    __syncthreads();
+    if (tid == 0) {
+      double all = 0.0;
+      for (int w = 0; w < kFwdWaves; w++) all += s_dot[w];
+      finish_loss(E, k, all, z, n, inv_n, counts, loss);
+    }
+    return;
+  }
+  if (tid < E) {
+    part.prob[(int64_t)blockIdx.x * E + tid] = p;
+    part.count[(int64_t)blockIdx.x * E + tid] = s_cnt[tid];
   }
   if (tid == 0) {
-    float zs = 0.f;
-    int ns = 0;
-    for (int w = 0; w < kWaves; w++) {
-      zs += s_z[w];
-      ns += s_n[w];
-    }
-    part_z[blockIdx.x] = zs;
-    part_n[blockIdx.x] = ns;
+    part.z[blockIdx.x] = z;
+    part.kept[blockIdx.x] = n;
+    if (blockIdx.x == 0) *part.ticket = 0;
   }
 }
 
-// One workgroup: the G rows of partial sums added in order (double), then the losses.
-__global__ void __launch_bounds__(1024) balance_sum_kernel(int E, int k, int G, const float* __restrict__ part_p,
-                                                           const int32_t* __restrict__ part_c,
-                                                           const float* __restrict__ part_z,
-                                                           const int32_t* __restrict__ part_n,
+// The G rows of partial sums added in a fixed order (double): 64 columns per workgroup, 16 runs of
+// rows.  The workgroup that comes last (device-wide ticket) adds the workgroups' shares of
+// sum_e c_e P_e, in order, and writes the losses.
+__global__ void __launch_bounds__(1024) balance_sum_kernel(int E, int k, int G, const BalancePart part,
                                                            int32_t* __restrict__ counts, float* __restrict__ prob_mean,
                                                            float* __restrict__ loss) {
-  __shared__ double s_p[1024];
-  __shared__ int s_c[1024];
-  __shared__ double s_dot[16];
-  __shared__ double s_zn[2];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  // thread (part, expert) adds one run of rows of one expert
-  const int P = 1024 / E > 0 ? 1024 / E : 1;
-  const int part = tid / E, e = tid - part * E;
+  constexpr int RUNS = 16;
+  __shared__ double s_p[RUNS][kSumCols];
+  __shared__ int s_c[RUNS][kSumCols];
+  __shared__ double s_z;
+  __shared__ int s_n;
+  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
+  const int col = blockIdx.x * kSumCols + lane;
   double p = 0.0;
   int c = 0;
-  if (part < P)
-    for (int g = part; g < G; g += P) {
-      p += part_p[(int64_t)g * E + e];
-      c += part_c[(int64_t)g * E + e];
+  if (col < E) {
+#pragma unroll 8
+    for (int g = run; g < G; g += RUNS) {
+      p += part.prob[(int64_t)g * E + col];
+      c += part.count[(int64_t)g * E + col];
     }
-  s_p[tid] = p;
-  s_c[tid] = c;
-  if (wave == 0) {
+  }
+  s_p[run][lane] = p;
+  s_c[run][lane] = c;
+  if (run == RUNS - 1) {
     double z = 0.0;
     int n = 0;
+#pragma unroll 4
     for (int g = lane; g < G; g += kWave) {
-      z += part_z[g];
-      n += part_n[g];
+      z += part.z[g];
+      n += part.kept[g];
     }
-    for (int o = 32; o > 0; o >>= 1) z += __shfl_xor(z, o, kWave);
+    z = wave_sum_double(z);
     n = wave_sum_int(n);
     if (lane == 0) {
-      s_zn[0] = z;
-      s_zn[1] = n;
+      s_z = z;
+      s_n = n;
     }
   }
   __syncthreads();
-  const int n = (int)s_zn[1];
-  const double inv = n > 0 ? 1.0 / n : 0.0;
+  if (run != 0) return;
+  const double inv_n = s_n > 0 ? 1.0 / s_n : 0.0;
   double dot = 0.0;
-  if (tid < E) {
-    double pe = 0.0;
-    int ce = 0;
-    for (int r = 0; r < P; r++) {
-      pe += s_p[r * E + tid];
-      ce += s_c[r * E + tid];
+  if (col < E) {
+    p = 0.0;
+    c = 0;
+#pragma unroll
+    for (int r = 0; r < RUNS; r++) {
+      p += s_p[r][lane];
+      c += s_c[r][lane];
     }
-    counts[tid] = ce;
-    prob_mean[tid] = (float)(pe * inv);
-    dot = ce * (pe * inv);
+    dot = finish_column(col, p, c, inv_n, counts, prob_mean);
   }
-  for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
-  if (lane == 0) s_dot[wave] = dot;
-  __syncthreads();
-  if (tid == 0) {
-    double sum = 0.0;
-    for (int w = 0; w < 16; w++) sum += s_dot[w];
-    counts[E] = n;
-    loss[0] = (float)(sum * inv * E / k);
-    loss[1] = (float)(s_zn[0] * inv);
+  dot = wave_sum_double(dot);
+  if (lane != 0) return;
+  if (gridDim.x > 1) {
+    __hip_atomic_store(&part.dots[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t before = __hip_atomic_fetch_add(part.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    if (before != gridDim.x - 1) return;
+    dot = 0.0;
+    for (unsigned b = 0; b < gridDim.x; b++)
+      dot += __hip_atomic_load(&part.dots[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+  finish_loss(E, k, dot, s_z, s_n, inv_n, counts, loss);
 }
 
 // dlogits, written in full: the losses' gradient plus, with dgates, the gates' gradient of
@@ -263,6 +362,13 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
     const bool in = t < T;
     const float l = in ? lse[t] : kNegInf;
     const bool kept = l != kNegInf;
+    float g = 0.f, dg = 0.f;
+    int id = -1;
+    if (dgates && in && q < k) {
+      g = gates[t * k + q];
+      dg = dgates[t * k + q];
+      id = topk_idx[t * k + q];
+    }
     float p[NV][4];
     float inner = 0.f;
 #pragma unroll
@@ -283,31 +389,28 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
     for (int i = 0; i < NV; i++)
 #pragma unroll
       for (int c = 0; c < 4; c++) p[i][c] = kept ? p[i][c] * fmaf(a, share[i][c] - inner, bl) : 0.f;
-    if (!in) continue;
-    if (dgates) {
-      const float* g = gates + t * k;
-      const float* dg = dgates + t * k;
-      const int32_t* id = topk_idx + t * k;
+    if (dgates) {  // lane j of the group holds choice j; each is passed round in order
       float gsum = 0.f;
-      for (int j = 0; j < k; j++) gsum = fmaf(g[j], dg[j], gsum);
+      for (int j = 0; j < k; j++) gsum = fmaf(from_lane<LPT>(g, j), from_lane<LPT>(dg, j), gsum);
+      const float gv = g * (dg - gsum);
       float gate[NV][4];
 #pragma unroll
       for (int i = 0; i < NV; i++) gate[i][0] = gate[i][1] = gate[i][2] = gate[i][3] = 0.f;
       for (int j = 0; j < k; j++) {
-        const float gv = g[j] * (dg[j] - gsum);
+        const float gj = from_lane<LPT>(gv, j);
+        const int r0 = from_lane<LPT>(id, j) - 4 * q;
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-          const int r = id[j] - 4 * (q + LPT * i);
+        for (int i = 0; i < NV; i++)
 #pragma unroll
           for (int c = 0; c < 4; c++)
-            if (r == c) gate[i][c] += gv;
-        }
+            if (r0 - 4 * LPT * i == c) gate[i][c] += gj;
       }
 #pragma unroll
       for (int i = 0; i < NV; i++)
 #pragma unroll
         for (int c = 0; c < 4; c++) p[i][c] += gate[i][c];
     }
+    if (!in) continue;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       const int e0 = 4 * (q + LPT * i);
@@ -327,57 +430,54 @@ bool vec_ok(int E, const void* a, const void* b) {
   return E % 4 == 0 && ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15) == 0;
 }
 
-// Calls f(LPT, NV) with the lanes per token and loads per lane that hold E scores.
-template <class F>
-hipError_t for_experts(int E, F&& f) {
-  using std::integral_constant;
-  const int e4 = (E + 3) / 4;
-#define MOE_BAL_CASE(LIMIT, LPT, NV) \
-  if (e4 <= LIMIT) return f(integral_constant<int, LPT>{}, integral_constant<int, NV>{});
-  MOE_BAL_CASE(1, 1, 1) MOE_BAL_CASE(2, 2, 1) MOE_BAL_CASE(4, 4, 1) MOE_BAL_CASE(8, 8, 1) MOE_BAL_CASE(16, 16, 1)
-  MOE_BAL_CASE(32, 32, 1) MOE_BAL_CASE(64, 64, 1) MOE_BAL_CASE(128, 64, 2) MOE_BAL_CASE(256, 64, 4)
-#undef MOE_BAL_CASE
-  return hipErrorInvalidValue;
-}
-
-int lanes_per_token(int E) {
+int lanes_per_token(int E, int k) {
   int l = 1;
-  while (l < 64 && 4 * l < E) l *= 2;
+  while (l < kWave && (4 * l < E || l < k)) l *= 2;
   return l;
 }
 
-// workgroups that give every wave at most one pass, up to `most`
-int balance_grid(int T, int E, int most) {
-  const int64_t per = (int64_t)kWaves * (kWave / lanes_per_token(E));
+// Calls f(LPT, NV) with the lanes per token and loads per lane that hold E scores and k choices.
+template <class F>
+hipError_t for_experts(int E, int k, F&& f) {
+  using std::integral_constant;
+  switch (lanes_per_token(E, k)) {
+#define MOE_BAL_CASE(LPT) \
+  case LPT: return f(integral_constant<int, LPT>{}, integral_constant<int, 1>{});
+    MOE_BAL_CASE(1) MOE_BAL_CASE(2) MOE_BAL_CASE(4) MOE_BAL_CASE(8) MOE_BAL_CASE(16) MOE_BAL_CASE(32)
+#undef MOE_BAL_CASE
+  }
+  if (E <= 256) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (E <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+}
+
+// workgroups of `waves` waves that give each `passes` rounds of tokens, up to `most`
+int balance_grid(int T, int E, int k, int waves, int passes, int most) {
+  const int64_t per = (int64_t)waves * (kWave / lanes_per_token(E, k)) * passes;
   const int64_t g = (T + per - 1) / per;
   return (int)(g < 1 ? 1 : (g > most ? most : g));
 }
+int balance_fwd_grid(int T, int E, int k) { return balance_grid(T, E, k, kFwdWaves, 4, kBalanceBlocks); }
 
 }  // namespace
 
-size_t balance_workspace_bytes(int T, int E) {
-  return (size_t)balance_grid(T, E, kBalanceBlocks) * ((size_t)E * 2 + 2) * sizeof(float);
+size_t balance_workspace_bytes(int T, int E, int k) {
+  return kPartHeader + (size_t)balance_fwd_grid(T, E, k) * ((size_t)E * 2 + 2) * sizeof(float);
 }
 
 hipError_t balance_forward(int T, int E, int k, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
                            float* lse, int32_t* counts, float* prob_mean, float* loss, void* ws, hipStream_t st) {
-  const int G = balance_grid(T, E, kBalanceBlocks);
-  float* part_p = static_cast<float*>(ws);
-  int32_t* part_c = reinterpret_cast<int32_t*>(part_p + (size_t)G * E);
-  float* part_z = reinterpret_cast<float*>(part_c + (size_t)G * E);
-  int32_t* part_n = reinterpret_cast<int32_t*>(part_z + G);
+  const int G = balance_fwd_grid(T, E, k);
+  const BalancePart part = carve(ws, G, E);
   const bool vec = vec_ok(E, logits, logits);
-  const hipError_t err = for_experts(E, [&](auto lpt, auto nv) {
-    if (vec)
-      hipLaunchKernelGGL((balance_fwd_kernel<lpt(), nv(), true>), dim3(G), dim3(kThreads), 0, st, T, E, k, logits,
-                         topk_idx, mask, lse, part_p, part_c, part_z, part_n);
-    else
-      hipLaunchKernelGGL((balance_fwd_kernel<lpt(), nv(), false>), dim3(G), dim3(kThreads), 0, st, T, E, k, logits,
-                         topk_idx, mask, lse, part_p, part_c, part_z, part_n);
+  const hipError_t err = for_experts(E, k, [&](auto lpt, auto nv) {
+    const auto kern = vec ? balance_fwd_kernel<lpt(), nv(), true> : balance_fwd_kernel<lpt(), nv(), false>;
+    hipLaunchKernelGGL(kern, dim3(G), dim3(kFwdThreads), 0, st, T, E, k, logits, topk_idx, mask, lse, part, counts,
+                       prob_mean, loss);
     return hipGetLastError();
   });
-  if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(balance_sum_kernel, dim3(1), dim3(1024), 0, st, E, k, G, part_p, part_c, part_z, part_n, counts,
+  if (err != hipSuccess || G == 1) return err;
+  hipLaunchKernelGGL(balance_sum_kernel, dim3((E + kSumCols - 1) / kSumCols), dim3(1024), 0, st, E, k, G, part, counts,
                      prob_mean, loss);
   return hipGetLastError();
 }
@@ -386,9 +486,9 @@ hipError_t balance_backward(int T, int E, int k, const float* logits, const floa
                             const float* dloss, const float* dgates, const float* gates, const int32_t* topk_idx,
                             float* dlogits, hipStream_t st) {
   if (T == 0) return hipSuccess;
-  const int G = balance_grid(T, E, device_cu_count() * 8);
+  const int G = balance_grid(T, E, k, kWaves, 1, device_cu_count() * 8);
   const bool vec = vec_ok(E, logits, dlogits);
-  return for_experts(E, [&](auto lpt, auto nv) {
+  return for_experts(E, k, [&](auto lpt, auto nv) {
     if (vec)
       hipLaunchKernelGGL((balance_bwd_kernel<lpt(), nv(), true>), dim3(G), dim3(kThreads), 0, st, T, E, k, logits, lse,
                          counts, dloss, dgates, gates, topk_idx, dlogits);

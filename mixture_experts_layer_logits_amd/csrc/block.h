@@ -10,7 +10,7 @@ namespace moe {
 
 // ------------------------------------------------------------------ balance loss
 constexpr int kBalanceBlocks = 256;  // most workgroups (rows of partial sums) of the forward
-size_t balance_workspace_bytes(int T, int E);
+size_t balance_workspace_bytes(int T, int E, int k);
 hipError_t balance_forward(int T, int E, int k, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
                            float* lse, int32_t* counts, float* prob_mean, float* loss, void* ws, hipStream_t st);
 hipError_t balance_backward(int T, int E, int k, const float* logits, const float* lse, const int32_t* counts,

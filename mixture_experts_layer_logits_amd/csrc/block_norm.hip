@@ -134,6 +134,10 @@ struct Lane {
 // Routed rows are loaded kBatch at a time, all loads before the first use.  With k <= kBatch the
 // backward keeps them for the gate gradients instead of gathering them again.
 constexpr int kBatch = 4;
+// Rows past 8192 columns take 16 waves at two chunks a lane and at most 128 registers: there the
+// backward keeps one routed row and no weights (they are read again each row) and loads no row
+// ahead.
+template <int C, int NWAVES> constexpr bool kTight = C == 2 && NWAVES == 16;
 
 template <typename T, int C>
 struct Gather {
@@ -227,16 +231,18 @@ __global__ void __launch_bounds__(NWAVES * 64) norm_fwd_kernel(const NormFwd a) 
 }
 
 // Waves per SIMD the registers are held to: 4 (128 registers), which the bf16 kernels meet; float
-// rows that gather would spill there (44 to 53 registers), so they get twice as many.
-template <typename T, int SRC, int NWAVES>
+// rows that gather would spill there (44 to 53 registers), and so would two chunks a lane, so
+// they get twice as many.
+template <typename T, int C, int SRC, int NWAVES>
 constexpr int bwd_waves_per_eu() {
-  return sizeof(T) == 4 && SRC == kGather && NWAVES < 16 ? 2 : 4;
+  return NWAVES < 16 && SRC == kGather && (sizeof(T) == 4 || C == 2) ? 2 : 4;
 }
 
 template <typename T, int WPR, int C, int NWAVES, int SRC>
 __global__ void __launch_bounds__(NWAVES * 64)
-    __attribute__((amdgpu_waves_per_eu(bwd_waves_per_eu<T, SRC, NWAVES>()))) norm_bwd_kernel(const NormBwd a) {
+    __attribute__((amdgpu_waves_per_eu(bwd_waves_per_eu<T, C, SRC, NWAVES>()))) norm_bwd_kernel(const NormBwd a) {
   constexpr int RPB = NWAVES / WPR;
+  constexpr int kKeep = kTight<C, NWAVES> ? 1 : kBatch;
   __shared__ float s_red[2][NWAVES][4];
   __shared__ float s_acc[RPB > 1 ? NWAVES * kWave * 8 : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(NWAVES * 64)
   // rows).  Each set's loads are issued before the other is worked on, the first one's a row
   // ahead, so memory stays busy across the row sums without registers for a second row.
   Raw<T> w_pre[C], w_post[C], dv[C], dxn[C], v[C], y_raw[C];
-  Raw<T> rows[SRC == kGather ? kBatch : 1][C];
+  Raw<T> rows[SRC == kGather ? kKeep : 1][C];
   const int64_t stride = (int64_t)gridDim.x * RPB;
   int64_t next = (int64_t)blockIdx.x * RPB + wave / WPR;
   // rows past the last one repeat it: nothing of them is stored or added to the weights' sums
@@ -263,36 +269,41 @@ __global__ void __launch_bounds__(NWAVES * 64)
     }
     if (a.dv) ln.load(a.dv, at, dv);
   };
-  int32_t slot[SRC == kGather ? kBatch : 1];  // the first routed rows of the next token
+  int32_t slot[SRC == kGather ? kKeep : 1];  // the first routed rows of the next token
   auto load_slots = [&](int64_t t) {
     if constexpr (SRC == kGather) {
 #pragma unroll
-      for (int j = 0; j < kBatch; j++) slot[j] = j < a.k ? a.slot_row[clamped(t) * a.k + j] : 0;
+      for (int j = 0; j < kKeep; j++) slot[j] = j < a.k ? a.slot_row[clamped(t) * a.k + j] : 0;
     }
   };
   load_slots(next);
-  load_stream(next);
-  if (a.w_pre) ln.load(a.w_pre, 0, w_pre);
-  if constexpr (SRC != kNone)
+  if constexpr (!kTight<C, NWAVES>) load_stream(next);
+  if (!kTight<C, NWAVES> && a.w_pre) ln.load(a.w_pre, 0, w_pre);
+  if constexpr (SRC != kNone && !kTight<C, NWAVES>)
     if (a.w_post) ln.load(a.w_post, 0, w_post);
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.T; base += stride) {
     const bool in = next < a.T;
     const int64_t t = clamped(next), at = t * a.d;
     const float* gates = a.gates + t * a.k;
     const int32_t* slots = a.slot_row + t * a.k;
+    if constexpr (kTight<C, NWAVES>) load_stream(next);
     next += stride;
     if constexpr (SRC == kGather) {
 #pragma unroll
-      for (int j = 0; j < kBatch; j++)
+      for (int j = 0; j < kKeep; j++)
         if (j < a.k) ln.load(a.y_perm, (int64_t)slot[j] * a.d, rows[j]);
       if (a.y_add) ln.load(a.y_add, at, y_raw);
       load_slots(next);
     }
     if constexpr (SRC == kLoad) ln.load(a.y, at, y_raw);
+    if constexpr (kTight<C, NWAVES>) {
+      if (a.w_pre) ln.load(a.w_pre, 0, w_pre);
+    } else {
 #pragma unroll
-    for (int i = 0; i < C; i++) {
-      w_pre[i].repack();
-      w_post[i].repack();
+      for (int i = 0; i < C; i++) {
+        w_pre[i].repack();
+        w_post[i].repack();
+      }
     }
 
     float D[C][8];
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(NWAVES * 64)
       MOE_EACH(i, c) D[i][c] = fmaf(r, fmaf(-m, v[i][c], dxn[i][c] * w_pre[i][c]), D[i][c]);
     }
     if (in) ln.store(a.dx, at, D);
-    load_stream(next);
+    if constexpr (!kTight<C, NWAVES>) load_stream(next);
     if constexpr (SRC != kNone) {
       float y[C][8];
       if constexpr (SRC == kLoad) {
@@ -323,20 +334,22 @@ __global__ void __launch_bounds__(NWAVES * 64)
       } else {
         MOE_EACH(i, c) y[i][c] = a.y_add ? y_raw[i][c] : 0.f;
 #pragma unroll
-        for (int j = 0; j < kBatch; j++)
+        for (int j = 0; j < kKeep; j++)
           if (j < a.k) {
             const float gj = gates[j];
             MOE_EACH(i, c) y[i][c] = fmaf(gj, rows[j][i][c], y[i][c]);
 #pragma unroll
             for (int i = 0; i < C; i++) rows[j][i].repack();
           }
-        for (int j = kBatch; j < a.k; j++) {
+        for (int j = kKeep; j < a.k; j++) {
           Raw<T> row[C];
           ln.load(a.y_perm, (int64_t)slots[j] * a.d, row);
           const float gj = gates[j];
           MOE_EACH(i, c) y[i][c] = fmaf(gj, row[i][c], y[i][c]);
         }
       }
+      if constexpr (kTight<C, NWAVES>)
+        if (a.w_post) ln.load(a.w_post, 0, w_post);
       const float g = a.gate ? a.gate[t] : 1.f;
       const bool open = g != 0.f;
       const float ag = a.res_scale * g;
@@ -377,15 +390,15 @@ __global__ void __launch_bounds__(NWAVES * 64)
           if (in) ln.store(a.dy_perm, (int64_t)slots[j] * a.d, o);
           return s;
         };
-        float s[kBatch];
+        float s[kKeep];
 #pragma unroll
-        for (int j = 0; j < kBatch; j++) s[j] = j < a.k ? routed(j, rows[j]) : 0.f;
+        for (int j = 0; j < kKeep; j++) s[j] = j < a.k ? routed(j, rows[j]) : 0.f;
         row_sum(s);
         if (in && ln.first == 0)
 #pragma unroll
-          for (int j = 0; j < kBatch; j++)
+          for (int j = 0; j < kKeep; j++)
             if (j < a.k) a.dgates[t * a.k + j] = s[j];
-        for (int j = kBatch; j < a.k; j++) {
+        for (int j = kKeep; j < a.k; j++) {
           ln.load(a.y_perm, (int64_t)slots[j] * a.d, rows[0]);
           const float sj = row_sum(routed(j, rows[0]));
           if (in && ln.first == 0) a.dgates[t * a.k + j] = sj;
@@ -460,9 +473,14 @@ hipError_t for_width_fwd(int d, F&& f) {
   MOE_NORM_CASE(16, 2, 16)
   return hipErrorInvalidValue;
 }
-template <class F>
+// Backward: one chunk a lane, so a row's accumulators and both sets of rows fit 128 registers.  A
+// gathering row of more than 4096 columns takes 8 waves at two chunks instead of 16 at one, whose
+// 128 registers it overflows (d = 8192, k = 4, T = 8192: 393 against 524 us); without a gather 16
+// waves are faster (54 against 59 us).
+template <int SRC, class F>
 hipError_t for_width_bwd(int d, F&& f) {
-  MOE_NORM_CASE(1, 1, 8) MOE_NORM_CASE(2, 1, 8) MOE_NORM_CASE(4, 1, 8) MOE_NORM_CASE(8, 1, 8) MOE_NORM_CASE(16, 1, 16)
+  MOE_NORM_CASE(1, 1, 8) MOE_NORM_CASE(2, 1, 8) MOE_NORM_CASE(4, 1, 8) MOE_NORM_CASE(8, 1, 8)
+  if constexpr (SRC == kGather) { MOE_NORM_CASE(8, 2, 8) } else { MOE_NORM_CASE(16, 1, 16) }
   MOE_NORM_CASE(16, 2, 16)
   return hipErrorInvalidValue;
 }
@@ -484,28 +502,25 @@ hipError_t fwd_t(const NormFwd& a, hipStream_t st) {
   });
 }
 
-// Up to 4 rows a wave in one workgroup, which then needs no second launch (2.4 us) to add up
+// Up to 2 rows a wave in one workgroup, which then needs no second launch (2.4 us) to add up
 // weight gradients; more rows take every resident workgroup, kNormBlocks at most.
 int bwd_grid(int T, int rpb, int resident) {
   const int64_t g = ((int64_t)T + rpb - 1) / rpb;
-  if (g <= 4) return g > 0;
+  if (g <= 2) return g > 0;
   const int most = resident < kNormBlocks ? resident : kNormBlocks;
   return (int)(g < most ? g : most);
 }
 
-template <typename T>
+template <typename T, int SRC>
 hipError_t bwd_t(const NormBwd& a, hipStream_t st) {
   int G = 0;
-  const hipError_t err = for_width_bwd(a.d, [&](auto wpr, auto c, auto nw) {
-    auto launch = [&](auto kern) {
-      G = bwd_grid(a.T, nw() / wpr(),
-                   device_cu_count() * kernel_occupancy(reinterpret_cast<const void*>(kern), nw() * 64, 0));
-      if (G > 0) hipLaunchKernelGGL(kern, dim3(G), dim3(nw() * 64), 0, st, a);
-      return G > 0 ? hipGetLastError() : hipSuccess;
-    };
-    if (a.y_perm) return launch(norm_bwd_kernel<T, wpr(), c(), nw(), kGather>);
-    if (a.y) return launch(norm_bwd_kernel<T, wpr(), c(), nw(), kLoad>);
-    return launch(norm_bwd_kernel<T, wpr(), c(), nw(), kNone>);
+  const hipError_t err = for_width_bwd<SRC>(a.d, [&](auto wpr, auto c, auto nw) {
+    const auto kern = norm_bwd_kernel<T, wpr(), c(), nw(), SRC>;
+    G = bwd_grid(a.T, nw() / wpr(),
+                 device_cu_count() * kernel_occupancy(reinterpret_cast<const void*>(kern), nw() * 64, 0));
+    if (G == 0) return hipSuccess;
+    hipLaunchKernelGGL(kern, dim3(G), dim3(nw() * 64), 0, st, a);
+    return hipGetLastError();
   });
   if (err != hipSuccess || G == 1 || (!a.dw_post && !a.dw_pre)) return err;
   hipLaunchKernelGGL(norm_dw_kernel, dim3(a.d / 16, 2), dim3(1024), 0, st, a.d, G, a.part, a.dw_post, a.dw_pre);
@@ -524,7 +539,9 @@ hipError_t block_norm_forward(int elem_bytes, const NormFwd& a, hipStream_t st) 
 }
 
 hipError_t block_norm_backward(int elem_bytes, const NormBwd& a, hipStream_t st) {
-  return elem_bytes == 4 ? bwd_t<float>(a, st) : bwd_t<bf16_t>(a, st);
+  if (a.y_perm) return elem_bytes == 4 ? bwd_t<float, kGather>(a, st) : bwd_t<bf16_t, kGather>(a, st);
+  if (a.y) return elem_bytes == 4 ? bwd_t<float, kLoad>(a, st) : bwd_t<bf16_t, kLoad>(a, st);
+  return elem_bytes == 4 ? bwd_t<float, kNone>(a, st) : bwd_t<bf16_t, kNone>(a, st);
 }
 
 }  // namespace moe

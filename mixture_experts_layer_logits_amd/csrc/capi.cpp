@@ -226,7 +226,7 @@ size_t moe_workspace_size(const moe_shape* s) {
     const size_t m = mx_workspace_bytes(s->T * s->k, s->d, s->f, s->E);
     if (m > b) b = m;
   }
-  const size_t bal = balance_workspace_bytes(s->T, s->E);
+  const size_t bal = balance_workspace_bytes(s->T, s->E, s->k);
   if (bal > b) b = bal;
   const size_t nrm = s->d <= kNormMaxWidth ? norm_workspace_bytes(s->T, s->d) : 0;
   if (nrm > b) b = nrm;
@@ -654,7 +654,7 @@ moe_status moe_balance_fwd(const moe_shape* s, const float* logits, const int32_
   if (!rows_ok(s, logits) || !rows_ok(s, topk_idx) || !rows_ok(s, lse)) return MOE_ENULL;
   if (!counts || !prob_mean || !loss || !ws) return MOE_ENULL;
   if (!aligned16(ws)) return MOE_EALIGN;
-  if (ws_bytes < balance_workspace_bytes(s->T, s->E)) return MOE_EWORKSPACE;
+  if (ws_bytes < balance_workspace_bytes(s->T, s->E, s->k)) return MOE_EWORKSPACE;
   return launched(balance_forward(s->T, s->E, s->k, logits, topk_idx, mask, lse, counts, prob_mean, loss, ws, S(st)));
 }
 
