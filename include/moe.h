@@ -423,7 +423,8 @@ moe_status moe_balance_fwd(const moe_shape* s, const float* logits, const int32_
  *                   + (e chosen by t: g_e (dgates_e - sum_j g_j dgates_j), as moe_route_bwd)
  * dgates, gates, topk_idx [T, k]: all three, or dgates NULL for the losses' gradient alone.  A
  * token left out (lse -inf) keeps its gates' gradient.  dlogits [T, E] float written in full; with
- * dloss zero it equals moe_route_bwd's.  dloss [2] float, on the device.
+ * dloss zero it is moe_route_bwd's but for the order in which sum_j is added.  dloss [2] float, on
+ * the device.
  * Ranks of a data-parallel job that add up counts (all E + 1 of them) between the two calls get
  * the gradient of the losses over all their tokens.  These gradients are not zero outside a
  * token's chosen experts: the router's input gradient then needs moe_router_bwd's dx_r

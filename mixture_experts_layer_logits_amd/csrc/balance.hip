@@ -27,32 +27,36 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr float kNegInf = -INFINITY;
 
-template <int LPT>
+// The other half's value at distance N (lane ^ N for N = 1, 2, 16, 32; for 4 and 8 a lane of the
+// other half, which does in a reduction whose halves are uniform).  Register exchanges: the LDS
+// crossbar behind shuffles is what bounded the backward (65521 tokens, E = 96: see below).
+template <int N>
+__device__ __forceinline__ float other_half(float v) {
+  const int x = __float_as_int(v);
+  if constexpr (N <= 8) {
+    constexpr int ctrl = N == 1 ? 0xB1 : N == 2 ? 0x4E : N == 4 ? 0x141 : 0x140;  // quad_perm, row_(half_)mirror
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, x, ctrl, 0xF, 0xF, false));
+  } else {
+    // swapping the odd halves of one copy with the even halves of another leaves each lane its own
+    // value in one of the two and the partner's in the other
+    const auto r = N == 16 ? __builtin_amdgcn_permlane16_swap(x, x, false, false)
+                           : __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    const bool odd = (threadIdx.x & N) != 0;
+    return __int_as_float(odd ? r[0] : r[1]);
+  }
+}
+template <int LPT, int N = 1>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  if constexpr (N < LPT) return group_sum<LPT, 2 * N>(v + other_half<N>(v));
   return v;
 }
-template <int LPT>
+template <int LPT, int N = 1>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) {
-    const float w = __shfl_xor(v, o, kWave);
-    v = (w > v || w != w) ? w : v;  // a NaN score wins, so it reaches lse
+  if constexpr (N < LPT) {
+    const float w = other_half<N>(v);
+    return group_max<LPT, 2 * N>((w > v || w != w) ? w : v);  // a NaN score wins, so it reaches lse
   }
   return v;
-}
-
-// lane j's value, of each group of LPT lanes
-template <int LPT>
-__device__ __forceinline__ float from_lane(float v, int j) {
-  if constexpr (LPT == kWave) return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
-  else return __shfl(v, j, LPT);
-}
-template <int LPT>
-__device__ __forceinline__ int from_lane(int v, int j) {
-  if constexpr (LPT == kWave) return __builtin_amdgcn_readlane(v, j);
-  else return __shfl(v, j, LPT);
 }
 
 // the 4 scores at columns e0 .. e0+3 of a row (columns past E: -inf)
@@ -331,8 +335,7 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(int E, int k, int G, 
   finish_loss(E, k, dot, s_z, s_n, inv_n, counts, loss);
 }
 
-// dlogits, written in full: the losses' gradient plus, with dgates, the gates' gradient of
-// route_backward (same arithmetic, so the two are equal when dloss is zero).
+// dlogits, written in full: the losses' gradient plus, with dgates, the gates' gradient.
 template <int LPT, int NV, bool VEC>
 __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int k, const float* __restrict__ logits,
                                                                const float* __restrict__ lse,
@@ -343,8 +346,15 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
                                                                const int32_t* __restrict__ topk_idx,
                                                                float* __restrict__ dlogits) {
   constexpr int TW = kWave / LPT;
+  // the gates' gradient of a group's token by column, zero outside its choices (and between tokens)
+  __shared__ __align__(16) float s_gate[kWaves][TW][4 * NV * LPT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int q = lane % LPT, sub = lane / LPT;
+  float* mine = s_gate[wave][sub];
+#pragma unroll
+  for (int i = 0; i < NV; i++)
+    *reinterpret_cast<float4*>(mine + 4 * (q + LPT * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
+  __builtin_amdgcn_wave_barrier();
   const int n = counts[E];
   const float inv_n = n > 0 ? 1.f / (float)n : 0.f;
   float share[NV][4];  // c_e / N
@@ -389,26 +399,22 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
     for (int i = 0; i < NV; i++)
 #pragma unroll
       for (int c = 0; c < 4; c++) p[i][c] = kept ? p[i][c] * fmaf(a, share[i][c] - inner, bl) : 0.f;
-    if (dgates) {  // lane j of the group holds choice j; each is passed round in order
-      float gsum = 0.f;
-      for (int j = 0; j < k; j++) gsum = fmaf(from_lane<LPT>(g, j), from_lane<LPT>(dg, j), gsum);
-      const float gv = g * (dg - gsum);
-      float gate[NV][4];
+    if (dgates) {
+      // lane j puts choice j's gradient where the lane that holds its column picks it up
+      const float gv = g * (dg - group_sum<LPT>(g * dg));
+      if (id >= 0 && id < E) atomicAdd(&mine[id], gv);
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int i = 0; i < NV; i++) gate[i][0] = gate[i][1] = gate[i][2] = gate[i][3] = 0.f;
-      for (int j = 0; j < k; j++) {
-        const float gj = from_lane<LPT>(gv, j);
-        const int r0 = from_lane<LPT>(id, j) - 4 * q;
-#pragma unroll
-        for (int i = 0; i < NV; i++)
-#pragma unroll
-          for (int c = 0; c < 4; c++)
-            if (r0 - 4 * LPT * i == c) gate[i][c] += gj;
+      for (int i = 0; i < NV; i++) {
+        const float4 gate = *reinterpret_cast<const float4*>(mine + 4 * (q + LPT * i));
+        p[i][0] += gate.x;
+        p[i][1] += gate.y;
+        p[i][2] += gate.z;
+        p[i][3] += gate.w;
       }
-#pragma unroll
-      for (int i = 0; i < NV; i++)
-#pragma unroll
-        for (int c = 0; c < 4; c++) p[i][c] += gate[i][c];
+      __builtin_amdgcn_wave_barrier();
+      if (id >= 0 && id < E) mine[id] = 0.f;
+      __builtin_amdgcn_wave_barrier();
     }
     if (!in) continue;
 #pragma unroll

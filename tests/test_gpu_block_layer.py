@@ -260,7 +260,7 @@ def test_layer_router_losses_without_a_block():
     assert normwise_err(host(L.dx), host(P.dx) + ax) <= TOL["bf16"]
     assert torch.equal(L.y, P.y) and torch.equal(L.dW1, P.dW1)
     L.backward(d["dy"], torch.zeros(2, device="cuda"))  # other weights than the layer's
-    assert torch.equal(L.dlogits, P.dlogits)
+    assert normwise_err(host(L.dlogits), host(P.dlogits)) <= 1e-6  # the gates' gradient alone, in another order
     steps = L.steps
     with pytest.raises(ValueError, match="learned routing"):
         L.forward(d["x"], d["W1"], d["W3"], d["W2"], topk_idx=L.topk_idx, gates=L.gates)
