@@ -315,45 +315,53 @@ def moe_ffn_dgrad1_mx(shape, dabq_rows, dabs_rows, W1, W3, offsets, dx_perm, ws,
 
 
 # ------------------------------------------------------------------ around the layer
-def _call_checked(name, shape, specs, args, stream=None):
-    """Call `name` after checking each tensor of `specs` (argument name, tensor or None, dtype,
-    number of elements): on one GPU, contiguous, of that type and size.  Launches on that GPU's
-    current stream if none is given, whichever device is the current one.  `args` are the call's
-    arguments in order, tensors as they came."""
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: a torch Stream object costs a microsecond
+
+
+def _call_checked(name, shape, args, stream=None):
+    """Call `name` with args in the C call's order: a tensor as (argument name, tensor or None, dtype,
+    number of elements), anything else as it is.  Tensors have to lie on one GPU, contiguous, of
+    that type and size (dtype None: a workspace of any type, whose size in bytes is passed on
+    behind it).  The call runs on that GPU's current stream if none is given, whichever device is
+    the current one."""
     dev = None
-    for arg, t, dtype, n in specs:
-        if t is None:
+    raw = []
+    for a in args:
+        if type(a) is not tuple:
+            raw.append(a)
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{name}: {arg} must live on the GPU")
-        if dtype is None:  # workspace: any type and size (the call checks its bytes)
-            if not t.is_contiguous():
-                raise ValueError(f"{name}: {arg} must be contiguous")
-        elif t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{name}: {arg} must be a contiguous {dtype} tensor of {n} elements, got {t.dtype} of "
-                             f"shape {tuple(t.shape)}, strides {t.stride()}")
+        arg, t, dtype, n = a
+        if t is None:
+            raw.append(None)
+            if dtype is None:
+                raw.append(0)
+            continue
         at = t.get_device()
-        if dev is None:
+        if at != dev:
+            if at < 0:
+                raise ValueError(f"{name}: {arg} must live on the GPU")
+            if dev is not None:
+                raise ValueError(f"{name}: {arg} lives on GPU {at}, the arguments before it on GPU {dev}")
             dev = at
-        elif at != dev:
-            raise ValueError(f"{name}: {arg} lives on GPU {at}, the arguments before it on GPU {dev}")
-    lib = load_library()
-    raw = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+        if not t.is_contiguous() or (dtype is not None and (t.dtype is not dtype or t.numel() != n)):
+            raise ValueError(f"{name}: {arg} must be contiguous" + ("" if dtype is None else
+                             f", {dtype}, of {n} elements; got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}"))
+        raw.append(t.data_ptr())
+        if dtype is None:
+            raw.append(t.numel() * t.element_size())
+    lib = _lib or load_library()
+    fn = getattr(lib, name)
     if dev is None or dev == torch.cuda.current_device():
-        st = getattr(lib, name)(ctypes.byref(shape), *raw, _stream(stream))
+        st = fn(shape, *raw, _stream(stream) if stream is not None or dev is None else _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = getattr(lib, name)(ctypes.byref(shape), *raw, _stream(stream))
+            st = fn(shape, *raw, _stream(stream) if stream is not None else _raw_stream(dev))
     if st != 0:
         raise MoeError(name, st, lib.moe_status_str(st).decode())
 
 
 def _act(shape):
-    return torch.float32 if shape.act == MOE_F32 else torch.bfloat16
-
-
-def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+    return _F32 if shape.act == MOE_F32 else torch.bfloat16
 
 
 _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
@@ -362,72 +370,67 @@ _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 def moe_balance_fwd(shape, logits, topk_idx, mask, lse, counts, prob_mean, loss, ws, stream=None):
     """Balance loss, z-loss and per-expert counts of the kept tokens (mask: uint8 [T] or None)."""
     T, E, k = shape.T, shape.E, shape.k
-    _call_checked("moe_balance_fwd", shape,
-                  (("logits", logits, _F32, T * E), ("topk_idx", topk_idx, _I32, T * k), ("mask", mask, _U8, T),
-                   ("lse", lse, _F32, T), ("counts", counts, _I32, E + 1), ("prob_mean", prob_mean, _F32, E),
-                   ("loss", loss, _F32, 2), ("ws", ws, None, 0)),
-                  (logits, topk_idx, mask, lse, counts, prob_mean, loss, ws, _nbytes(ws)), stream)
+    _call_checked("moe_balance_fwd", shape, (
+        ("logits", logits, _F32, T * E), ("topk_idx", topk_idx, _I32, T * k), ("mask", mask, _U8, T),
+        ("lse", lse, _F32, T), ("counts", counts, _I32, E + 1), ("prob_mean", prob_mean, _F32, E),
+        ("loss", loss, _F32, 2), ("ws", ws, None, 0)), stream)
 
 
 def moe_balance_bwd(shape, logits, lse, counts, dloss, dgates, gates, topk_idx, dlogits, stream=None):
     """dlogits of the losses (weights dloss, a float32 [2] on the GPU) and, with dgates, of the gates."""
     T, E, k = shape.T, shape.E, shape.k
-    _call_checked("moe_balance_bwd", shape,
-                  (("logits", logits, _F32, T * E), ("lse", lse, _F32, T), ("counts", counts, _I32, E + 1),
-                   ("dloss", dloss, _F32, 2), ("dgates", dgates, _F32, T * k), ("gates", gates, _F32, T * k),
-                   ("topk_idx", topk_idx, _I32, T * k), ("dlogits", dlogits, _F32, T * E)),
-                  (logits, lse, counts, dloss, dgates, gates, topk_idx, dlogits), stream)
+    _call_checked("moe_balance_bwd", shape, (
+        ("logits", logits, _F32, T * E), ("lse", lse, _F32, T), ("counts", counts, _I32, E + 1),
+        ("dloss", dloss, _F32, 2), ("dgates", dgates, _F32, T * k), ("gates", gates, _F32, T * k),
+        ("topk_idx", topk_idx, _I32, T * k), ("dlogits", dlogits, _F32, T * E)), stream)
 
 
 def moe_block_norm_fwd(shape, x, y, gate, w_post, w_pre, res_scale, eps, v, xn, rstd_post, rstd_pre, stream=None):
     """v = x + res_scale gate (norm(y) w_post), xn = norm(v) w_pre; None leaves a part out."""
     T, d, a = shape.T, shape.d, _act(shape)
-    _call_checked("moe_block_norm_fwd", shape,
-                  (("x", x, a, T * d), ("y", y, a, T * d), ("gate", gate, _F32, T), ("w_post", w_post, a, d),
-                   ("w_pre", w_pre, a, d), ("v", v, a, T * d), ("xn", xn, a, T * d), ("rstd_post", rstd_post, _F32, T),
-                   ("rstd_pre", rstd_pre, _F32, T)),
-                  (x, y, gate, w_post, w_pre, res_scale, eps, v, xn, rstd_post, rstd_pre), stream)
+    n = T * d
+    _call_checked("moe_block_norm_fwd", shape, (
+        ("x", x, a, n), ("y", y, a, n), ("gate", gate, _F32, T), ("w_post", w_post, a, d), ("w_pre", w_pre, a, d),
+        res_scale, eps, ("v", v, a, n), ("xn", xn, a, n), ("rstd_post", rstd_post, _F32, T),
+        ("rstd_pre", rstd_pre, _F32, T)), stream)
 
 
 def moe_block_norm_bwd(shape, dv, dxn, v, y, gate, w_post, w_pre, rstd_post, rstd_pre, res_scale, dx, dy, dgate,
                        dw_post, dw_pre, ws, stream=None):
+    """Gradients of moe_block_norm_fwd; None for what the forward left out or is not wanted."""
     T, d, a = shape.T, shape.d, _act(shape)
-    _call_checked("moe_block_norm_bwd", shape,
-                  (("dx", dx, a, T * d), ("dv", dv, a, T * d), ("dxn", dxn, a, T * d), ("v", v, a, T * d),
-                   ("y", y, a, T * d), ("gate", gate, _F32, T), ("w_post", w_post, a, d), ("w_pre", w_pre, a, d),
-                   ("rstd_post", rstd_post, _F32, T), ("rstd_pre", rstd_pre, _F32, T), ("dy", dy, a, T * d),
-                   ("dgate", dgate, _F32, T), ("dw_post", dw_post, _F32, d), ("dw_pre", dw_pre, _F32, d),
-                   ("ws", ws, None, 0)),
-                  (dv, dxn, v, y, gate, w_post, w_pre, rstd_post, rstd_pre, res_scale, dx, dy, dgate, dw_post, dw_pre,
-                   ws, _nbytes(ws)), stream)
+    n = T * d
+    _call_checked("moe_block_norm_bwd", shape, (
+        ("dv", dv, a, n), ("dxn", dxn, a, n), ("v", v, a, n), ("y", y, a, n), ("gate", gate, _F32, T),
+        ("w_post", w_post, a, d), ("w_pre", w_pre, a, d), ("rstd_post", rstd_post, _F32, T),
+        ("rstd_pre", rstd_pre, _F32, T), res_scale, ("dx", dx, a, n), ("dy", dy, a, n), ("dgate", dgate, _F32, T),
+        ("dw_post", dw_post, _F32, d), ("dw_pre", dw_pre, _F32, d), ("ws", ws, None, 0)), stream)
 
 
 def moe_combine_norm(shape, y_perm, gates, slot_row, y_add, x, gate, w_post, w_pre, res_scale, eps, v, xn, rstd_post,
                      rstd_pre, stream=None):
     """moe_block_norm_fwd of the gated sum of each token's k routed rows (moe_combine), in one pass."""
     T, d, k, a = shape.T, shape.d, shape.k, _act(shape)
-    _call_checked("moe_combine_norm", shape,
-                  (("x", x, a, T * d), ("y_perm", y_perm, a, T * k * d), ("gates", gates, _F32, T * k),
-                   ("slot_row", slot_row, _I32, T * k), ("y_add", y_add, a, T * d), ("gate", gate, _F32, T),
-                   ("w_post", w_post, a, d), ("w_pre", w_pre, a, d), ("v", v, a, T * d), ("xn", xn, a, T * d),
-                   ("rstd_post", rstd_post, _F32, T), ("rstd_pre", rstd_pre, _F32, T)),
-                  (y_perm, gates, slot_row, y_add, x, gate, w_post, w_pre, res_scale, eps, v, xn, rstd_post, rstd_pre),
-                  stream)
+    n = T * d
+    _call_checked("moe_combine_norm", shape, (
+        ("y_perm", y_perm, a, n * k), ("gates", gates, _F32, T * k), ("slot_row", slot_row, _I32, T * k),
+        ("y_add", y_add, a, n), ("x", x, a, n), ("gate", gate, _F32, T), ("w_post", w_post, a, d),
+        ("w_pre", w_pre, a, d), res_scale, eps, ("v", v, a, n), ("xn", xn, a, n), ("rstd_post", rstd_post, _F32, T),
+        ("rstd_pre", rstd_pre, _F32, T)), stream)
 
 
 def moe_combine_norm_bwd(shape, dv, dxn, v, y_perm, gates, slot_row, y_add, gate, w_post, w_pre, rstd_post, rstd_pre,
                          res_scale, dx, dy, dy_perm, dgates, dgate, dw_post, dw_pre, ws, stream=None):
+    """Gradients of moe_combine_norm; None for what the forward left out or is not wanted."""
     T, d, k, a = shape.T, shape.d, shape.k, _act(shape)
-    _call_checked("moe_combine_norm_bwd", shape,
-                  (("dx", dx, a, T * d), ("dv", dv, a, T * d), ("dxn", dxn, a, T * d), ("v", v, a, T * d),
-                   ("y_perm", y_perm, a, T * k * d), ("gates", gates, _F32, T * k), ("slot_row", slot_row, _I32, T * k),
-                   ("y_add", y_add, a, T * d), ("gate", gate, _F32, T), ("w_post", w_post, a, d),
-                   ("w_pre", w_pre, a, d), ("rstd_post", rstd_post, _F32, T), ("rstd_pre", rstd_pre, _F32, T),
-                   ("dy", dy, a, T * d), ("dy_perm", dy_perm, a, T * k * d), ("dgates", dgates, _F32, T * k),
-                   ("dgate", dgate, _F32, T), ("dw_post", dw_post, _F32, d), ("dw_pre", dw_pre, _F32, d),
-                   ("ws", ws, None, 0)),
-                  (dv, dxn, v, y_perm, gates, slot_row, y_add, gate, w_post, w_pre, rstd_post, rstd_pre, res_scale, dx,
-                   dy, dy_perm, dgates, dgate, dw_post, dw_pre, ws, _nbytes(ws)), stream)
+    n = T * d
+    _call_checked("moe_combine_norm_bwd", shape, (
+        ("dv", dv, a, n), ("dxn", dxn, a, n), ("v", v, a, n), ("y_perm", y_perm, a, n * k),
+        ("gates", gates, _F32, T * k), ("slot_row", slot_row, _I32, T * k), ("y_add", y_add, a, n),
+        ("gate", gate, _F32, T), ("w_post", w_post, a, d), ("w_pre", w_pre, a, d),
+        ("rstd_post", rstd_post, _F32, T), ("rstd_pre", rstd_pre, _F32, T), res_scale, ("dx", dx, a, n),
+        ("dy", dy, a, n), ("dy_perm", dy_perm, a, n * k), ("dgates", dgates, _F32, T * k), ("dgate", dgate, _F32, T),
+        ("dw_post", dw_post, _F32, d), ("dw_pre", dw_pre, _F32, d), ("ws", ws, None, 0)), stream)
 
 
 from .layer import MoEBlock, MoEExpertLayer  # noqa: E402  (re-export)

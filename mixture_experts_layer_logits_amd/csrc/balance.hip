@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(int T, int E, 
     __syncthreads();
     if (tid == 0) {
       double all = 0.0;
+#pragma unroll
       for (int w = 0; w < kFwdWaves; w++) all += s_dot[w];
       finish_loss(E, k, all, z, n, inv_n, counts, loss);
     }
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(int E, int k, int G, 
   double p = 0.0;
   int c = 0;
   if (col < E) {
-#pragma unroll 8
+#pragma unroll 16
     for (int g = run; g < G; g += RUNS) {
       p += part.prob[(int64_t)g * E + col];
       c += part.count[(int64_t)g * E + col];
@@ -457,13 +458,19 @@ hipError_t for_experts(int E, int k, F&& f) {
   return f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
 }
 
-// workgroups of `waves` waves that give each `passes` rounds of tokens, up to `most`
-int balance_grid(int T, int E, int k, int waves, int passes, int most) {
-  const int64_t per = (int64_t)waves * (kWave / lanes_per_token(E, k)) * passes;
+// workgroups of `waves` waves that hold all tokens at once, up to `most`
+int balance_grid(int T, int E, int k, int waves, int most) {
+  const int64_t per = (int64_t)waves * (kWave / lanes_per_token(E, k));
   const int64_t g = (T + per - 1) / per;
   return (int)(g < 1 ? 1 : (g > most ? most : g));
 }
-int balance_fwd_grid(int T, int E, int k) { return balance_grid(T, E, k, kFwdWaves, 4, kBalanceBlocks); }
+// Four rounds of tokens or fewer stay in one workgroup: that takes less than a second launch would.
+// More are spread as wide as they go (T = 8192, E = 128: 9.6 us with 256 workgroups of one round,
+// 11.4 with 128 of two, 12.2 with 64 of four).
+int balance_fwd_grid(int T, int E, int k) {
+  const int g = balance_grid(T, E, k, kFwdWaves, kBalanceBlocks);
+  return g <= 4 ? 1 : g;
+}
 
 }  // namespace
 
@@ -492,7 +499,7 @@ hipError_t balance_backward(int T, int E, int k, const float* logits, const floa
                             const float* dloss, const float* dgates, const float* gates, const int32_t* topk_idx,
                             float* dlogits, hipStream_t st) {
   if (T == 0) return hipSuccess;
-  const int G = balance_grid(T, E, k, kWaves, 1, device_cu_count() * 8);
+  const int G = balance_grid(T, E, k, kWaves, device_cu_count() * 8);
   const bool vec = vec_ok(E, logits, dlogits);
   return for_experts(E, k, [&](auto lpt, auto nv) {
     if (vec)
