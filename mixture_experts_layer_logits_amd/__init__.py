@@ -315,7 +315,8 @@ def moe_ffn_dgrad1_mx(shape, dabq_rows, dabs_rows, W1, W3, offsets, dx_perm, ws,
 
 
 # ------------------------------------------------------------------ around the layer
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: a torch Stream object costs a microsecond
+# the handle and the index alone: a torch Stream object costs a microsecond
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _call_checked(name, shape, args, stream=None):
@@ -351,7 +352,7 @@ def _call_checked(name, shape, args, stream=None):
             raw.append(t.numel() * t.element_size())
     lib = _lib or load_library()
     fn = getattr(lib, name)
-    if dev is None or dev == torch.cuda.current_device():
+    if dev is None or dev == _device():
         st = fn(shape, *raw, _stream(stream) if stream is not None or dev is None else _raw_stream(dev))
     else:
         with torch.cuda.device(dev):

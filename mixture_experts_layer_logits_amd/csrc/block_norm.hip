@@ -235,7 +235,8 @@ __global__ void __launch_bounds__(NWAVES * 64) norm_fwd_kernel(const NormFwd a) 
 // they get twice as many.
 template <typename T, int C, int SRC, int NWAVES>
 constexpr int bwd_waves_per_eu() {
-  return NWAVES < 16 && SRC == kGather && (sizeof(T) == 4 || C == 2) ? 2 : 4;
+  if (NWAVES > 8) return (NWAVES + 3) / 4;  // one workgroup a compute unit
+  return SRC == kGather && (sizeof(T) == 4 || C == 2) ? 2 : 4;
 }
 
 template <typename T, int WPR, int C, int NWAVES, int SRC>
@@ -463,7 +464,9 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(int d, int G, const float
 }
 
 // Calls f(WPR, C, NWAVES) with the waves per row, chunks per lane and waves per workgroup that
-// hold a row of d.
+// hold a row of d.  Rows between the steps leave lanes idle, which costs little: at 1.6 GB the
+// backward of combine and norm takes 382 us at d = 2560 on 8 waves a row (347 at 2048, 342 at 4096),
+// and 447 on 5, whose workgroups fill a compute unit worse.
 #define MOE_NORM_CASE(WPR, C, NWAVES) \
   if (d <= WPR * C * 512) \
     return f(std::integral_constant<int, WPR>{}, std::integral_constant<int, C>{}, std::integral_constant<int, NWAVES>{});
@@ -474,12 +477,13 @@ hipError_t for_width_fwd(int d, F&& f) {
   return hipErrorInvalidValue;
 }
 // Backward: one chunk a lane, so a row's accumulators and both sets of rows fit 128 registers.  A
-// gathering row of more than 4096 columns takes 8 waves at two chunks instead of 16 at one, whose
-// 128 registers it overflows (d = 8192, k = 4, T = 8192: 393 against 524 us); without a gather 16
-// waves are faster (54 against 59 us).
+// gathering row of more than 12 waves takes 8 at two chunks instead of 16 at one, whose 128
+// registers it overflows (d = 8192, k = 4, T = 8192: 393 against 524 us); without a gather 16
+// waves are faster (54 against 59 us).  12 waves keep 168 registers each (d = 5120: 396 us against
+// 508 on 8 waves of two chunks).
 template <int SRC, class F>
 hipError_t for_width_bwd(int d, F&& f) {
-  MOE_NORM_CASE(1, 1, 8) MOE_NORM_CASE(2, 1, 8) MOE_NORM_CASE(4, 1, 8) MOE_NORM_CASE(8, 1, 8)
+  MOE_NORM_CASE(1, 1, 8) MOE_NORM_CASE(2, 1, 8) MOE_NORM_CASE(4, 1, 8) MOE_NORM_CASE(8, 1, 8) MOE_NORM_CASE(12, 1, 12)
   if constexpr (SRC == kGather) { MOE_NORM_CASE(8, 2, 8) } else { MOE_NORM_CASE(16, 1, 16) }
   MOE_NORM_CASE(16, 2, 16)
   return hipErrorInvalidValue;
@@ -508,7 +512,8 @@ int bwd_grid(int T, int rpb, int resident) {
   const int64_t g = ((int64_t)T + rpb - 1) / rpb;
   if (g <= 2) return g > 0;
   const int most = resident < kNormBlocks ? resident : kNormBlocks;
-  return (int)(g < most ? g : most);
+  const int64_t passes = (g + most - 1) / most;
+  return (int)((g + passes - 1) / passes);  // as few workgroups as take that many passes: fewer partials
 }
 
 template <typename T, int SRC>
