@@ -19,6 +19,7 @@
 
 #include "block.h"
 #include "gemm.h"
+#include "lanes.h"
 
 namespace moe {
 namespace {
@@ -27,29 +28,6 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr float kNegInf = -INFINITY;
 
-// The other half's value at distance N (lane ^ N for N = 1, 2, 16, 32; for 4 and 8 a lane of the
-// other half, which does in a reduction whose halves are uniform).  Register exchanges: the LDS
-// crossbar behind shuffles is what bounded the backward (65521 tokens, E = 96: see below).
-template <int N>
-__device__ __forceinline__ float other_half(float v) {
-  const int x = __float_as_int(v);
-  if constexpr (N <= 8) {
-    constexpr int ctrl = N == 1 ? 0xB1 : N == 2 ? 0x4E : N == 4 ? 0x141 : 0x140;  // quad_perm, row_(half_)mirror
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, x, ctrl, 0xF, 0xF, false));
-  } else {
-    // swapping the odd halves of one copy with the even halves of another leaves each lane its own
-    // value in one of the two and the partner's in the other
-    const auto r = N == 16 ? __builtin_amdgcn_permlane16_swap(x, x, false, false)
-                           : __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    const bool odd = (threadIdx.x & N) != 0;
-    return __int_as_float(odd ? r[0] : r[1]);
-  }
-}
-template <int LPT, int N = 1>
-__device__ __forceinline__ float group_sum(float v) {
-  if constexpr (N < LPT) return group_sum<LPT, 2 * N>(v + other_half<N>(v));
-  return v;
-}
 template <int LPT, int N = 1>
 __device__ __forceinline__ float group_max(float v) {
   if constexpr (N < LPT) {
@@ -59,16 +37,26 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
-// the 4 scores at columns e0 .. e0+3 of a row (columns past E: -inf)
-template <bool VEC>
-__device__ __forceinline__ void load_scores(const float* row, int e0, int E, float (&v)[4]) {
+// Column of element c of lane q's load i: 4 consecutive ones where rows are 16-byte aligned (VEC),
+// else one of each LPT, so that a wave's 4-byte accesses still fall on whole lines.
+template <int LPT, bool VEC>
+__device__ __forceinline__ int column(int q, int i, int c) {
+  return VEC ? 4 * (q + LPT * i) + c : q + LPT * (4 * i + c);
+}
+// lane q's scores of load i (columns past E: -inf)
+template <int LPT, bool VEC>
+__device__ __forceinline__ void load_scores(const float* row, int q, int i, int E, float (&v)[4]) {
   if constexpr (VEC) {
-    float4 q = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
-    if (e0 < E) q = *reinterpret_cast<const float4*>(row + e0);
-    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    const int e0 = column<LPT, VEC>(q, i, 0);
+    float4 w = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+    if (e0 < E) w = *reinterpret_cast<const float4*>(row + e0);
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
   } else {
 #pragma unroll
-    for (int c = 0; c < 4; c++) v[c] = e0 + c < E ? row[e0 + c] : kNegInf;
+    for (int c = 0; c < 4; c++) {
+      const int e = column<LPT, VEC>(q, i, c);
+      v[c] = e < E ? row[e] : kNegInf;
+    }
   }
 }
 
@@ -157,7 +145,7 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(int T, int E, 
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       v[i][0] = v[i][1] = v[i][2] = v[i][3] = kNegInf;
-      if (live) load_scores<VEC>(logits + at * E, 4 * (q + LPT * i), E, v[i]);
+      if (live) load_scores<LPT, VEC>(logits + at * E, q, i, E, v[i]);
     }
   };
   float v[NV][4], ahead[NV][4];
@@ -225,7 +213,7 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(int T, int E, 
       for (int i = 0; i < NV; i++)
 #pragma unroll
         for (int c = 0; c < 4; c++) {
-          const int col = 4 * (q + LPT * i) + c;
+          const int col = column<LPT, VEC>(q, i, c);
           if (col < E) f(s_p[wave % HALF][col], acc[i][c]);
         }
     }
@@ -363,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
   for (int i = 0; i < NV; i++)
 #pragma unroll
     for (int c = 0; c < 4; c++) {
-      const int e = 4 * (q + LPT * i) + c;
+      const int e = column<LPT, VEC>(q, i, c);
       share[i][c] = e < E ? (float)counts[e] * inv_n : 0.f;
     }
   const float a = dloss[0] * ((float)E / (float)k) * inv_n;
@@ -386,7 +374,7 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
     for (int i = 0; i < NV; i++) {
       p[i][0] = p[i][1] = p[i][2] = p[i][3] = 0.f;
       if (kept) {
-        load_scores<VEC>(logits + t * E, 4 * (q + LPT * i), E, p[i]);
+        load_scores<LPT, VEC>(logits + t * E, q, i, E, p[i]);
 #pragma unroll
         for (int c = 0; c < 4; c++) {
           p[i][c] = expf(p[i][c] - l);
@@ -407,27 +395,34 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int i = 0; i < NV; i++) {
-        const float4 gate = *reinterpret_cast<const float4*>(mine + 4 * (q + LPT * i));
-        p[i][0] += gate.x;
-        p[i][1] += gate.y;
-        p[i][2] += gate.z;
-        p[i][3] += gate.w;
+        if constexpr (VEC) {
+          const float4 gate = *reinterpret_cast<const float4*>(mine + column<LPT, VEC>(q, i, 0));
+          p[i][0] += gate.x;
+          p[i][1] += gate.y;
+          p[i][2] += gate.z;
+          p[i][3] += gate.w;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; c++) p[i][c] += mine[column<LPT, VEC>(q, i, c)];
+        }
       }
       __builtin_amdgcn_wave_barrier();
       if (id >= 0 && id < E) mine[id] = 0.f;
       __builtin_amdgcn_wave_barrier();
     }
     if (!in) continue;
+    float* o = dlogits + t * E;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-      const int e0 = 4 * (q + LPT * i);
-      float* o = dlogits + t * E + e0;
       if constexpr (VEC) {
-        if (e0 < E) *reinterpret_cast<float4*>(o) = make_float4(p[i][0], p[i][1], p[i][2], p[i][3]);
+        const int e0 = column<LPT, VEC>(q, i, 0);
+        if (e0 < E) *reinterpret_cast<float4*>(o + e0) = make_float4(p[i][0], p[i][1], p[i][2], p[i][3]);
       } else {
 #pragma unroll
-        for (int c = 0; c < 4; c++)
-          if (e0 + c < E) o[c] = p[i][c];
+        for (int c = 0; c < 4; c++) {
+          const int e = column<LPT, VEC>(q, i, c);
+          if (e < E) o[e] = p[i][c];
+        }
       }
     }
   }

@@ -13,41 +13,31 @@
 // writes dy_perm[slot_row[t, j]] = gates[t, j] dy[t] and dgates[t, j] = <dy[t], y_perm[..]>.
 //
 // HBM-bound: every row is read once and written once.  A row is held in the registers of WPR
-// waves, 8 consecutive columns per 16-byte load and C such chunks per lane; row sums are float
-// butterflies over the wave, then over the WPR waves through LDS.  Rows and weights round to
+// waves, or for narrow rows of LPR lanes of one (WPR = 1, 64 / LPR rows a wave), 8 consecutive
+// columns per 16-byte load and C such chunks per lane; row sums are register exchanges over the
+// lanes, then over the WPR waves through LDS.  Rows and weights round to
 // the element type once, at the store: xn is taken from the unrounded v, dy from the unrounded D.
 // Weight gradients accumulate in registers over a workgroup's rows, meet across its waves in
 // LDS, go to one partial row per workgroup and are added by a second launch, all in a fixed
 // order (no atomics).
 #include "block.h"
 #include "gemm.h"
+#include "lanes.h"
 
 namespace moe {
 namespace {
 
-enum Src { kNone = 0, kLoad = 1, kGather = 2 };  // the branch y: absent, read, gathered from routed rows
+// The branch y: absent, read, or gathered from routed rows (in the backward, from at most kBatch rows
+// a token, all held in registers, or from any number).
+enum Src { kNone = 0, kLoad = 1, kGather = 2, kGatherMany = 3 };
+constexpr bool gathers(int src) { return src == kGather || src == kGatherMany; }
 
-// Sum over the wave, the same in every lane: four exchanges inside each row of 16 lanes, then
-// the rows' sums passed on to lane 63 and read from there.  Register exchanges (DPP) take a
-// fraction of the time of six shuffles through the LDS crossbar, and the row sums stand on the
-// critical path of every row.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp_add(float v) {
-  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
-}
-__device__ __forceinline__ float wave_total(float v) {
-  v = dpp_add<0xB1, 0xF>(v);   // quad_perm [1,0,3,2]
-  v = dpp_add<0x4E, 0xF>(v);   // quad_perm [2,3,0,1]
-  v = dpp_add<0x141, 0xF>(v);  // row_half_mirror: the other quad of each 8
-  v = dpp_add<0x140, 0xF>(v);  // row_mirror: the other 8 of each 16
-  v = dpp_add<0x142, 0xA>(v);  // row_bcast15 into rows 1 and 3
-  v = dpp_add<0x143, 0xC>(v);  // row_bcast31 into rows 2 and 3
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
+// The lanes that hold one row: LPR of a wave, or WPR whole waves.
+constexpr int rows_of(int lpr, int wpr, int nwaves) { return nwaves * (kWave / lpr) / wpr; }
 
-// Sums over the WPR waves of a row.  Consecutive sums alternate between two LDS buffers, so one
+// Sums over the lanes of a row.  Over several waves, consecutive sums alternate between two LDS buffers, so one
 // barrier each is enough: a buffer is written again only after a later barrier.
-template <int WPR, int NWAVES>
+template <int LPR, int WPR, int NWAVES>
 struct RowSum {
   float (*buf)[NWAVES][4];
   int wave;
@@ -56,7 +46,7 @@ struct RowSum {
   __device__ __forceinline__ void operator()(float (&v)[N]) {
     static_assert(N <= 4, "a buffer holds 4 sums a wave");
 #pragma unroll
-    for (int n = 0; n < N; n++) v[n] = wave_total(v[n]);
+    for (int n = 0; n < N; n++) v[n] = LPR == kWave ? wave_total(v[n]) : group_sum<LPR>(v[n]);
     if constexpr (WPR > 1) {
       if ((threadIdx.x & 63) == 0)
 #pragma unroll
@@ -131,12 +121,12 @@ struct Lane {
   }
 };
 
-// Routed rows are loaded kBatch at a time, all loads before the first use.  With k <= kBatch the
-// backward keeps them for the gate gradients instead of gathering them again.
+// Routed rows are loaded kBatch at a time, all loads before the first use; the backward keeps the
+// last batch (with k <= kBatch all of them) for the gate gradients.
 constexpr int kBatch = 4;
 // Rows past 8192 columns take 16 waves at two chunks a lane and at most 128 registers: there the
-// backward keeps one routed row and no weights (they are read again each row) and loads no row
-// ahead.
+// backward keeps no weights (they are read again each row), loads no row ahead, and at k > kBatch
+// gathers one routed row at a time.
 template <int C, int NWAVES> constexpr bool kTight = C == 2 && NWAVES == 16;
 
 template <typename T, int C>
@@ -162,18 +152,20 @@ struct Gather {
   }
 };
 
-template <typename T, int WPR, int C, int NWAVES, int SRC>
+template <typename T, int LPR, int WPR, int C, int NWAVES, int SRC>
 __global__ void __launch_bounds__(NWAVES * 64) norm_fwd_kernel(const NormFwd a) {
-  constexpr int RPB = NWAVES / WPR;
+  constexpr int RPB = rows_of(LPR, WPR, NWAVES);
   __shared__ float s_red[2][NWAVES][4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  RowSum<WPR, NWAVES> row_sum{s_red, wave};
-  const Lane<T, C> ln{(wave % WPR) * kWave + lane, WPR * kWave, a.d / 8};
+  RowSum<LPR, WPR, NWAVES> row_sum{s_red, wave};
+  const Lane<T, C> ln{(wave % WPR) * kWave + lane % LPR, WPR * LPR, a.d / 8};
+  // this lane's row of the workgroup's; the same for a whole wave (in scalar registers) at LPR = 64
+  const int mine = LPR == kWave ? wave / WPR : wave * (kWave / LPR) + lane / LPR;
   const float inv_d = 1.f / (float)a.d;
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.T; base += (int64_t)gridDim.x * RPB) {
     // waves past the last row repeat it without storing (row sums may hold barriers)
-    const bool in = base + wave / WPR < a.T;
-    const int64_t t = in ? base + wave / WPR : a.T - 1;
+    const bool in = base + mine < a.T;
+    const int64_t t = in ? base + mine : a.T - 1;
     const int64_t at = t * a.d;
     float v[C][8];
     Raw<T> x[C], w_post[C], w_pre[C];
@@ -236,19 +228,22 @@ __global__ void __launch_bounds__(NWAVES * 64) norm_fwd_kernel(const NormFwd a) 
 template <typename T, int C, int SRC, int NWAVES>
 constexpr int bwd_waves_per_eu() {
   if (NWAVES > 8) return (NWAVES + 3) / 4;  // one workgroup a compute unit
-  return SRC == kGather && (sizeof(T) == 4 || C == 2) ? 2 : 4;
+  return gathers(SRC) && (sizeof(T) == 4 || C == 2) ? 2 : 4;
 }
 
-template <typename T, int WPR, int C, int NWAVES, int SRC>
+template <typename T, int LPR, int WPR, int C, int NWAVES, int SRC>
 __global__ void __launch_bounds__(NWAVES * 64)
     __attribute__((amdgpu_waves_per_eu(bwd_waves_per_eu<T, C, SRC, NWAVES>()))) norm_bwd_kernel(const NormBwd a) {
-  constexpr int RPB = NWAVES / WPR;
+  constexpr int RPB = rows_of(LPR, WPR, NWAVES);
   constexpr int kKeep = kTight<C, NWAVES> ? 1 : kBatch;
   __shared__ float s_red[2][NWAVES][4];
-  __shared__ float s_acc[RPB > 1 ? NWAVES * kWave * 8 : 1];
+  constexpr int GROUPS = NWAVES / WPR;
+  __shared__ float s_acc[GROUPS > 1 ? NWAVES * kWave * 8 : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  RowSum<WPR, NWAVES> row_sum{s_red, wave};
-  const Lane<T, C> ln{(wave % WPR) * kWave + lane, WPR * kWave, a.d / 8};
+  RowSum<LPR, WPR, NWAVES> row_sum{s_red, wave};
+  const Lane<T, C> ln{(wave % WPR) * kWave + lane % LPR, WPR * LPR, a.d / 8};
+  // this lane's row of the workgroup's; the same for a whole wave (in scalar registers) at LPR = 64
+  const int mine = LPR == kWave ? wave / WPR : wave * (kWave / LPR) + lane / LPR;
   const float inv_d = 1.f / (float)a.d;
   float acc_pre[C][8], acc_post[C][8];
   MOE_EACH(i, c) acc_pre[i][c] = acc_post[i][c] = 0.f;
@@ -257,9 +252,9 @@ __global__ void __launch_bounds__(NWAVES * 64)
   // rows).  Each set's loads are issued before the other is worked on, the first one's a row
   // ahead, so memory stays busy across the row sums without registers for a second row.
   Raw<T> w_pre[C], w_post[C], dv[C], dxn[C], v[C], y_raw[C];
-  Raw<T> rows[SRC == kGather ? kKeep : 1][C];
+  Raw<T> rows[gathers(SRC) ? kKeep : 1][C];
   const int64_t stride = (int64_t)gridDim.x * RPB;
-  int64_t next = (int64_t)blockIdx.x * RPB + wave / WPR;
+  int64_t next = (int64_t)blockIdx.x * RPB + mine;
   // rows past the last one repeat it: nothing of them is stored or added to the weights' sums
   auto clamped = [&](int64_t t) { return t < a.T ? t : (int64_t)a.T - 1; };
   auto load_stream = [&](int64_t t) {
@@ -270,9 +265,9 @@ __global__ void __launch_bounds__(NWAVES * 64)
     }
     if (a.dv) ln.load(a.dv, at, dv);
   };
-  int32_t slot[SRC == kGather ? kKeep : 1];  // the first routed rows of the next token
+  int32_t slot[gathers(SRC) ? kKeep : 1];  // the first routed rows of the next token
   auto load_slots = [&](int64_t t) {
-    if constexpr (SRC == kGather) {
+    if constexpr (gathers(SRC)) {
 #pragma unroll
       for (int j = 0; j < kKeep; j++) slot[j] = j < a.k ? a.slot_row[clamped(t) * a.k + j] : 0;
     }
@@ -289,7 +284,7 @@ __global__ void __launch_bounds__(NWAVES * 64)
     const int32_t* slots = a.slot_row + t * a.k;
     if constexpr (kTight<C, NWAVES>) load_stream(next);
     next += stride;
-    if constexpr (SRC == kGather) {
+    if constexpr (gathers(SRC)) {
 #pragma unroll
       for (int j = 0; j < kKeep; j++)
         if (j < a.k) ln.load(a.y_perm, (int64_t)slot[j] * a.d, rows[j]);
@@ -329,25 +324,36 @@ __global__ void __launch_bounds__(NWAVES * 64)
     if (in) ln.store(a.dx, at, D);
     if constexpr (!kTight<C, NWAVES>) load_stream(next);
     if constexpr (SRC != kNone) {
+      // kGather: routed rows j0 .. j0 + kKeep - 1 into `rows`, all loads before the first use; those
+      // of the last batch (`held`) serve the gate gradients, the others are gathered again
+      int held = 0;
+      auto load_rows = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < kKeep; j++)
+          if (j0 + j < a.k) ln.load(a.y_perm, (int64_t)slots[j0 + j] * a.d, rows[j]);
+      };
+      auto add_rows = [&](int j0, float (&y)[C][8]) {  // j in order
+#pragma unroll
+        for (int j = 0; j < kKeep; j++)
+          if (j0 + j < a.k) {
+            const float gj = gates[j0 + j];
+            MOE_EACH(i, c) y[i][c] = fmaf(gj, rows[j][i][c], y[i][c]);
+#pragma unroll
+            for (int i = 0; i < C; i++) rows[j][i].repack();
+          }
+      };
       float y[C][8];
       if constexpr (SRC == kLoad) {
         MOE_EACH(i, c) y[i][c] = y_raw[i][c];
       } else {
         MOE_EACH(i, c) y[i][c] = a.y_add ? y_raw[i][c] : 0.f;
-#pragma unroll
-        for (int j = 0; j < kKeep; j++)
-          if (j < a.k) {
-            const float gj = gates[j];
-            MOE_EACH(i, c) y[i][c] = fmaf(gj, rows[j][i][c], y[i][c]);
-#pragma unroll
-            for (int i = 0; i < C; i++) rows[j][i].repack();
+        add_rows(0, y);
+        if constexpr (SRC == kGatherMany)
+          for (int j0 = kKeep; j0 < a.k; j0 += kKeep) {
+            load_rows(j0);
+            add_rows(j0, y);
+            held = j0;
           }
-        for (int j = kKeep; j < a.k; j++) {
-          Raw<T> row[C];
-          ln.load(a.y_perm, (int64_t)slots[j] * a.d, row);
-          const float gj = gates[j];
-          MOE_EACH(i, c) y[i][c] = fmaf(gj, row[i][c], y[i][c]);
-        }
       }
       if constexpr (kTight<C, NWAVES>)
         if (a.w_post) ln.load(a.w_post, 0, w_post);
@@ -379,59 +385,68 @@ __global__ void __launch_bounds__(NWAVES * 64)
         MOE_EACH(i, c) D[i][c] = open ? ag * D[i][c] : 0.f;
       }
       if (in && a.dy) ln.store(a.dy, at, D);
-      if constexpr (SRC == kGather) {
-        auto routed = [&](int j, const Raw<T>(&row)[C]) {  // one row of dy_perm; this lane's part of dgates
-          const float gj = gates[j];
-          float o[C][8];
-          float s = 0.f;
-          MOE_EACH(i, c) {
-            s = fmaf(D[i][c], row[i][c], s);
-            o[i][c] = gj * D[i][c];
+      if constexpr (gathers(SRC)) {
+        auto routed = [&](int j0) {  // the batch's rows of dy_perm, and its dgates
+          float s[kKeep];
+#pragma unroll
+          for (int j = 0; j < kKeep; j++) {
+            s[j] = 0.f;
+            if (j0 + j >= a.k) continue;
+            const float gj = gates[j0 + j];
+            float o[C][8];
+            MOE_EACH(i, c) {
+              s[j] = fmaf(D[i][c], rows[j][i][c], s[j]);
+              o[i][c] = gj * D[i][c];
+            }
+            if (in) ln.store(a.dy_perm, (int64_t)slots[j0 + j] * a.d, o);
           }
-          if (in) ln.store(a.dy_perm, (int64_t)slots[j] * a.d, o);
-          return s;
+          row_sum(s);
+          if (in && ln.first == 0)
+#pragma unroll
+            for (int j = 0; j < kKeep; j++)
+              if (j0 + j < a.k) a.dgates[t * a.k + j0 + j] = s[j];
         };
-        float s[kKeep];
-#pragma unroll
-        for (int j = 0; j < kKeep; j++) s[j] = j < a.k ? routed(j, rows[j]) : 0.f;
-        row_sum(s);
-        if (in && ln.first == 0)
-#pragma unroll
-          for (int j = 0; j < kKeep; j++)
-            if (j < a.k) a.dgates[t * a.k + j] = s[j];
-        for (int j = kKeep; j < a.k; j++) {
-          ln.load(a.y_perm, (int64_t)slots[j] * a.d, rows[0]);
-          const float sj = row_sum(routed(j, rows[0]));
-          if (in && ln.first == 0) a.dgates[t * a.k + j] = sj;
+        if constexpr (SRC == kGather) {
+          routed(0);
+        } else {
+          routed(held);
+          for (int j0 = 0; j0 < held; j0 += kKeep) {
+            load_rows(j0);
+            routed(j0);
+          }
         }
       }
     }
   }
-  // weight-gradient partials: the workgroup's RPB rows of waves in order, then one row per
+  // weight-gradient partials: a wave's rows, the workgroup's waves in order, then one row per
   // workgroup of part [2][G][d] (dw_post, dw_pre)
   auto reduce = [&](float (&acc)[C][8], float* out) {
 #pragma unroll
     for (int i = 0; i < C; i++) {
       float sum[8];
-      if constexpr (RPB > 1) {
-        __syncthreads();
-        float* mine = s_acc + (wave * kWave + lane) * 8;
 #pragma unroll
-        for (int c = 0; c < 8; c++) mine[c] = acc[i][c];
+      for (int c = 0; c < 8; c++) {
+        sum[c] = acc[i][c];
+        if constexpr (LPR <= 8) sum[c] += other_half<8>(sum[c]);
+        if constexpr (LPR <= 16) sum[c] += other_half<16>(sum[c]);
+        if constexpr (LPR <= 32) sum[c] += other_half<32>(sum[c]);
+      }
+      if constexpr (GROUPS > 1) {
+        __syncthreads();
+        float* at = s_acc + (wave * kWave + lane) * 8;
+#pragma unroll
+        for (int c = 0; c < 8; c++) at[c] = sum[c];
         __syncthreads();
         if (wave < WPR) {
 #pragma unroll
           for (int c = 0; c < 8; c++) sum[c] = 0.f;
-          for (int r = 0; r < RPB; r++)
+          for (int r = 0; r < GROUPS; r++)
 #pragma unroll
             for (int c = 0; c < 8; c++) sum[c] += s_acc[((r * WPR + wave) * kWave + lane) * 8 + c];
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 8; c++) sum[c] = acc[i][c];
       }
       const int chunk = ln.first + i * ln.step;
-      if (wave < WPR && chunk < ln.nchunk) store8<float>(out + chunk * 8, sum);
+      if (wave < WPR && lane < LPR && chunk < ln.nchunk) store8<float>(out + chunk * 8, sum);
     }
   };
   const bool alone = gridDim.x == 1;  // then the sums are whole
@@ -463,17 +478,24 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(int d, int G, const float
   if (run == 0) out[blockIdx.x * COLS + col] = s[0][col];
 }
 
-// Calls f(WPR, C, NWAVES) with the waves per row, chunks per lane and waves per workgroup that
-// hold a row of d.  Rows between the steps leave lanes idle, which costs little: at 1.6 GB the
+// Calls f(LPR, WPR, C, NWAVES) with the lanes and waves per row, chunks per lane and waves per
+// workgroup that hold a row of d.  Rows between the steps leave lanes idle, which costs little: at 1.6 GB the
 // backward of combine and norm takes 382 us at d = 2560 on 8 waves a row (347 at 2048, 342 at 4096),
 // and 447 on 5, whose workgroups fill a compute unit worse.
-#define MOE_NORM_CASE(WPR, C, NWAVES) \
-  if (d <= WPR * C * 512) \
-    return f(std::integral_constant<int, WPR>{}, std::integral_constant<int, C>{}, std::integral_constant<int, NWAVES>{});
+#define MOE_NORM_CASE(LPR, WPR, C, NWAVES)                                        \
+  if (d <= LPR * WPR * C * 8)                                                     \
+    return f(std::integral_constant<int, LPR>{}, std::integral_constant<int, WPR>{}, \
+             std::integral_constant<int, C>{}, std::integral_constant<int, NWAVES>{});
+// Several narrow rows to a wave (combine and norm forward at T = 57912, d = 64, k = 7: 17 us against
+// 56) once there are more rows than waves that run at once; fewer rows take a wave each, whose
+// slots, gates and row sums are scalars (backward at T = 3, d = 256, k = 5: 6.8 us against 9.5).
+constexpr int kPackRows = 2048;
 template <class F>
-hipError_t for_width_fwd(int d, F&& f) {
-  MOE_NORM_CASE(1, 1, 4) MOE_NORM_CASE(1, 2, 4) MOE_NORM_CASE(2, 2, 4) MOE_NORM_CASE(4, 2, 4) MOE_NORM_CASE(8, 2, 8)
-  MOE_NORM_CASE(16, 2, 16)
+hipError_t for_width_fwd(int T, int d, F&& f) {
+  if (T > kPackRows) { MOE_NORM_CASE(8, 1, 1, 4) MOE_NORM_CASE(16, 1, 1, 4) MOE_NORM_CASE(32, 1, 1, 4) }
+  MOE_NORM_CASE(64, 1, 1, 4)
+  MOE_NORM_CASE(64, 1, 2, 4) MOE_NORM_CASE(64, 2, 2, 4) MOE_NORM_CASE(64, 4, 2, 4) MOE_NORM_CASE(64, 8, 2, 8)
+  MOE_NORM_CASE(64, 16, 2, 16)
   return hipErrorInvalidValue;
 }
 // Backward: one chunk a lane, so a row's accumulators and both sets of rows fit 128 registers.  A
@@ -482,10 +504,12 @@ hipError_t for_width_fwd(int d, F&& f) {
 // waves are faster (54 against 59 us).  12 waves keep 168 registers each (d = 5120: 396 us against
 // 508 on 8 waves of two chunks).
 template <int SRC, class F>
-hipError_t for_width_bwd(int d, F&& f) {
-  MOE_NORM_CASE(1, 1, 8) MOE_NORM_CASE(2, 1, 8) MOE_NORM_CASE(4, 1, 8) MOE_NORM_CASE(8, 1, 8) MOE_NORM_CASE(12, 1, 12)
-  if constexpr (SRC == kGather) { MOE_NORM_CASE(8, 2, 8) } else { MOE_NORM_CASE(16, 1, 16) }
-  MOE_NORM_CASE(16, 2, 16)
+hipError_t for_width_bwd(int T, int d, F&& f) {
+  if (T > kPackRows) { MOE_NORM_CASE(8, 1, 1, 8) MOE_NORM_CASE(16, 1, 1, 8) MOE_NORM_CASE(32, 1, 1, 8) }
+  MOE_NORM_CASE(64, 1, 1, 8)
+  MOE_NORM_CASE(64, 2, 1, 8) MOE_NORM_CASE(64, 4, 1, 8) MOE_NORM_CASE(64, 8, 1, 8) MOE_NORM_CASE(64, 12, 1, 12)
+  if constexpr (gathers(SRC)) { MOE_NORM_CASE(64, 8, 2, 8) } else { MOE_NORM_CASE(64, 16, 1, 16) }
+  if constexpr (SRC != kGather) { MOE_NORM_CASE(64, 16, 2, 16) }  // kGather: at most 8192 columns
   return hipErrorInvalidValue;
 }
 #undef MOE_NORM_CASE
@@ -495,34 +519,36 @@ constexpr int64_t kNormFwdBlocks = 1 << 20;
 
 template <typename T>
 hipError_t fwd_t(const NormFwd& a, hipStream_t st) {
-  return for_width_fwd(a.d, [&](auto wpr, auto c, auto nw) {
-    constexpr int RPB = nw() / wpr();
+  return for_width_fwd(a.T, a.d, [&](auto lpr, auto wpr, auto c, auto nw) {
+    constexpr int RPB = rows_of(lpr(), wpr(), nw());
     const int64_t rows = ((int64_t)a.T + RPB - 1) / RPB;
     const dim3 grid((unsigned)(rows < kNormFwdBlocks ? rows : kNormFwdBlocks)), block(nw() * 64);
-    if (a.y_perm) hipLaunchKernelGGL((norm_fwd_kernel<T, wpr(), c(), nw(), kGather>), grid, block, 0, st, a);
-    else if (a.y) hipLaunchKernelGGL((norm_fwd_kernel<T, wpr(), c(), nw(), kLoad>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((norm_fwd_kernel<T, wpr(), c(), nw(), kNone>), grid, block, 0, st, a);
+    if (a.y_perm) hipLaunchKernelGGL((norm_fwd_kernel<T, lpr(), wpr(), c(), nw(), kGather>), grid, block, 0, st, a);
+    else if (a.y) hipLaunchKernelGGL((norm_fwd_kernel<T, lpr(), wpr(), c(), nw(), kLoad>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((norm_fwd_kernel<T, lpr(), wpr(), c(), nw(), kNone>), grid, block, 0, st, a);
     return hipGetLastError();
   });
 }
 
-// Up to 2 rows a wave in one workgroup, which then needs no second launch (2.4 us) to add up
-// weight gradients; more rows take every resident workgroup, kNormBlocks at most.
-int bwd_grid(int T, int rpb, int resident) {
+// One workgroup where that saves the second launch (2.4 us) that adds up weight gradients: two
+// passes of rows take less, two that gather (5 us each) do not.  More rows take every resident
+// workgroup, kNormBlocks at most, and as few as need that many passes, for fewer partials.
+int bwd_grid(int T, int rpb, int resident, bool gather) {
   const int64_t g = ((int64_t)T + rpb - 1) / rpb;
-  if (g <= 2) return g > 0;
+  if (g <= (gather ? 1 : 2)) return g > 0;
   const int most = resident < kNormBlocks ? resident : kNormBlocks;
   const int64_t passes = (g + most - 1) / most;
-  return (int)((g + passes - 1) / passes);  // as few workgroups as take that many passes: fewer partials
+  return (int)((g + passes - 1) / passes);
 }
 
 template <typename T, int SRC>
 hipError_t bwd_t(const NormBwd& a, hipStream_t st) {
   int G = 0;
-  const hipError_t err = for_width_bwd<SRC>(a.d, [&](auto wpr, auto c, auto nw) {
-    const auto kern = norm_bwd_kernel<T, wpr(), c(), nw(), SRC>;
-    G = bwd_grid(a.T, nw() / wpr(),
-                 device_cu_count() * kernel_occupancy(reinterpret_cast<const void*>(kern), nw() * 64, 0));
+  const hipError_t err = for_width_bwd<SRC>(a.T, a.d, [&](auto lpr, auto wpr, auto c, auto nw) {
+    const auto kern = norm_bwd_kernel<T, lpr(), wpr(), c(), nw(), SRC>;
+    G = bwd_grid(a.T, rows_of(lpr(), wpr(), nw()),
+                 device_cu_count() * kernel_occupancy(reinterpret_cast<const void*>(kern), nw() * 64, 0),
+                 gathers(SRC));
     if (G == 0) return hipSuccess;
     hipLaunchKernelGGL(kern, dim3(G), dim3(nw() * 64), 0, st, a);
     return hipGetLastError();
@@ -544,7 +570,9 @@ hipError_t block_norm_forward(int elem_bytes, const NormFwd& a, hipStream_t st) 
 }
 
 hipError_t block_norm_backward(int elem_bytes, const NormBwd& a, hipStream_t st) {
-  if (a.y_perm) return elem_bytes == 4 ? bwd_t<float, kGather>(a, st) : bwd_t<bf16_t, kGather>(a, st);
+  if (a.y_perm && a.k <= kBatch && a.d <= 8192)
+    return elem_bytes == 4 ? bwd_t<float, kGather>(a, st) : bwd_t<bf16_t, kGather>(a, st);
+  if (a.y_perm) return elem_bytes == 4 ? bwd_t<float, kGatherMany>(a, st) : bwd_t<bf16_t, kGatherMany>(a, st);
   if (a.y) return elem_bytes == 4 ? bwd_t<float, kLoad>(a, st) : bwd_t<bf16_t, kLoad>(a, st);
   return elem_bytes == 4 ? bwd_t<float, kNone>(a, st) : bwd_t<bf16_t, kNone>(a, st);
 }

@@ -380,10 +380,12 @@ def test_combine_norm_top_k(k, d):
 
 
 @pytest.mark.parametrize("branch", ["none", "y", "combine"])
-def test_norm_many_rows(branch):
-    """More rows than workgroups: several rows to every wave of the backward."""
-    say(f"[gpu] norm many rows {branch}")
-    n = Norm(9001, 64, "bf16", branch, seed=6)
+@pytest.mark.parametrize("T,d,k,act", [(9001, 64, 3, "bf16"), (2049, 128, 6, "bf16"), (5003, 192, 4, "f32"),
+                                       (2500, 256, 9, "bf16"), (3001, 320, 2, "bf16"), (2048, 64, 5, "f32")])
+def test_norm_many_rows(branch, T, d, k, act):
+    """More rows than workgroups: several rows to every wave, narrow ones side by side in it."""
+    say(f"[gpu] norm many rows {branch} T={T} d={d} k={k} {act}")
+    n = Norm(T, d, act, branch, k=k, seed=6)
     n.check(n.fwd(), n.ref_fwd())
     n.check(n.bwd(), n.ref_bwd())
 
