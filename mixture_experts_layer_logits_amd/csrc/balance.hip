@@ -28,6 +28,19 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr float kNegInf = -INFINITY;
 
+// e^x = 2^t (1 + r ln 2) with t = x log2 e rounded and r what that rounding and the constant's own
+// dropped: within 2 units in the last place for x <= 0, values below 2^-126 as 0, NaN as NaN.  The
+// backward issues some 140 vector instructions per lane and token, which bound it; expf's handling of
+// ranges that p = e^(score - lse) never has was 20 of them.
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kLog2E = 1.44269502f, kLog2ELow = 1.92596303e-08f, kLn2 = 0.693147182f;
+  x = x < -150.f ? -150.f : x;  // -inf: its r would be NaN
+  const float t = x * kLog2E;
+  const float r = fmaf(x, kLog2ELow, fmaf(x, kLog2E, -t));
+  const float p = __builtin_amdgcn_exp2f(t);
+  return fmaf(p, r * kLn2, p);
+}
+
 template <int LPT, int N = 1>
 __device__ __forceinline__ float group_max(float v) {
   if constexpr (N < LPT) {
@@ -167,7 +180,7 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(int T, int E, 
     for (int i = 0; i < NV; i++)
 #pragma unroll
       for (int c = 0; c < 4; c++) {
-        v[i][c] = kept ? expf(v[i][c] - top) : 0.f;
+        v[i][c] = kept ? exp_neg(v[i][c] - top) : 0.f;
         sum += v[i][c];
       }
     sum = group_sum<LPT>(sum);
@@ -377,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
         load_scores<LPT, VEC>(logits + t * E, q, i, E, p[i]);
 #pragma unroll
         for (int c = 0; c < 4; c++) {
-          p[i][c] = expf(p[i][c] - l);
+          p[i][c] = exp_neg(p[i][c] - l);
           inner = fmaf(p[i][c], share[i][c], inner);
         }
       }
