@@ -473,7 +473,7 @@ moe_status moe_combine_norm(const moe_shape* s, const void* y_perm, const float*
 
 /* Backward of moe_combine_norm: moe_block_norm_bwd's outputs, and moe_combine_bwd's from the
  * unrounded dy: dy_perm[slot_row[t, j]] = gates[t, j] dy[t], dgates[t, j] = <dy[t],
- * y_perm[slot_row[t, j]]>.  y is rebuilt from the gathered rows.  dy [T, d] (the gradient of
+ * y_perm[slot_row[t, j]]> (0 where the token's gate is 0).  y is rebuilt from the gathered rows.  dy [T, d] (the gradient of
  * y_add) may be NULL.  dy_perm must not be y_perm. */
 moe_status moe_combine_norm_bwd(const moe_shape* s, const void* dv, const void* dxn, const void* v,
                                 const void* y_perm, const float* gates, const int32_t* slot_row, const void* y_add,

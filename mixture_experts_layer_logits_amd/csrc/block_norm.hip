@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(NWAVES * 64)
           if (in && ln.first == 0)
 #pragma unroll
             for (int j = 0; j < kKeep; j++)
-              if (j0 + j < a.k) a.dgates[t * a.k + j0 + j] = s[j];
+              if (j0 + j < a.k) a.dgates[t * a.k + j0 + j] = open ? s[j] : 0.f;  // 0 whatever the rows hold
         };
         if constexpr (SRC == kGather) {
           routed(0);

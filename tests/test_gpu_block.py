@@ -350,7 +350,7 @@ FLAGS = [(True, True, True), (True, True, False), (True, False, True), (False, T
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("T,d", [(1, 64), (1, 2048), (2, 192), (7, 512), (65, 576), (257, 1088), (33, 2048), (9, 2112),
-                                 (40, 4096), (6, 8256), (5, 16384)])
+                                 (40, 4096), (30, 5120), (21, 7168), (6, 8256), (5, 16384)])
 def test_norm_widths(T, d, act):
     for branch in ("none", "y", "combine"):
         say(f"[gpu] norm T={T} d={d} {act} {branch}")
@@ -371,10 +371,11 @@ def test_norm_parts(branch, post, pre, gated):
 
 
 @pytest.mark.parametrize("k", [1, 2, 3, 4, 5, 8, 9, 32])
-@pytest.mark.parametrize("d", [256, 2048])
-def test_combine_norm_top_k(k, d):
-    say(f"[gpu] combine norm k={k} d={d}")
-    n = Norm(37, d, "bf16", "combine", k=k, add=k % 2 == 1, seed=k)
+@pytest.mark.parametrize("d,act", [(256, "bf16"), (2048, "bf16"), (2048, "f32"), (5120, "bf16"), (7168, "bf16"),
+                                   (16384, "bf16")])
+def test_combine_norm_top_k(k, d, act):
+    say(f"[gpu] combine norm k={k} d={d} {act}")
+    n = Norm(37 if d < 4096 else 7, d, act, "combine", k=k, add=k % 2 == 1, seed=k)
     n.check(n.fwd(), n.ref_fwd())
     n.check(n.bwd(), n.ref_bwd())
 
@@ -391,8 +392,9 @@ def test_norm_many_rows(branch, T, d, k, act):
 
 
 @pytest.mark.parametrize("branch", ["y", "combine"])
-def test_norm_closed_gates_drop_what_the_branch_holds(branch):
-    n = Norm(64, 256, "bf16", branch, k=2, seed=3)
+@pytest.mark.parametrize("T,k,post", [(64, 2, True), (64, 6, True), (2100, 3, True), (64, 2, False)])
+def test_norm_closed_gates_drop_what_the_branch_holds(branch, T, k, post):
+    n = Norm(T, 256, "bf16", branch, k=k, post=post, seed=3)
     shut = torch.nonzero(n.c["gate"] == 0)[:, 0]
     clean = {k: v.clone() for k, v in n.fwd().items()}
     cb = {k: v.clone() for k, v in n.bwd().items()}
@@ -404,11 +406,12 @@ def test_norm_closed_gates_drop_what_the_branch_holds(branch):
     assert torch.equal(f["v"], clean["v"]) and torch.equal(f["xn"], clean["xn"])
     assert torch.equal(f["v"][shut.cuda()], n.d["x"][shut.cuda()])
     b = n.bwd()
-    assert torch.equal(b["dw_post"], cb["dw_post"]) and torch.equal(b["dx"], cb["dx"])
+    assert torch.equal(b["dx"], cb["dx"]) and (not post or torch.equal(b["dw_post"], cb["dw_post"]))
     if branch == "y":
         assert torch.equal(b["dy"], cb["dy"]) and not host(b["dy"][shut.cuda()]).any()
     else:
-        assert torch.equal(b["dy_perm"], cb["dy_perm"])
+        assert torch.equal(b["dy_perm"], cb["dy_perm"]) and torch.equal(b["dgates"], cb["dgates"])
+        assert not host(b["dgates"][shut.cuda()]).any()
 
 
 def test_norm_rows_of_zeros():

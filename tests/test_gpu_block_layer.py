@@ -179,6 +179,19 @@ def test_a_stack_of_blocks_passes_its_norm_on():
         assert normwise_err(host(x), host(y)) <= TOL["bf16"] or moved, n
 
 
+def test_block_refuses_its_own_output_as_input():
+    import mixture_experts_layer_logits_amd as m
+    w = workloads.scaled(W["e8_k4_t8192"], T=32, d=128, f=64)
+    inp, e = workloads.make_inputs(w), _extra(w, 2, True, False, True)
+    block = m.MoEBlock(_layer(w, None), 0.5, EPS)
+    v, _ = _run(block, w, inp, e)
+    d, x = to_dev(inp), {k: None if t is None else t.cuda() for k, t in e.items()}
+    for kw in (dict(h=v, w_pre=x["w_pre"]), dict(h=d["x"], xn=block.xn_next), dict(h=d["x"]),
+               dict(h=d["x"], xn=d["x"], w_pre=x["w_pre"])):
+        with pytest.raises(ValueError):
+            block.forward(kw.pop("h"), d["W1"], d["W3"], d["W2"], Wr=d["Wr"], **kw)
+
+
 def test_block_step_graph_replays_match_eager():
     import mixture_experts_layer_logits_amd as m
     w = workloads.scaled(W["e128_k4_t8192_shared"], T=256, d=256, f=128, shared_f=64)
