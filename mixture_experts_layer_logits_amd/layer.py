@@ -249,11 +249,12 @@ class MoEExpertLayer:
                                self.dyq_rows, self.dys_rows, self.dyq_cols, self.dys_cols)
         else:
             moe_combine_bwd(s, dy, self.y_perm, g, self.slot_row, self.dy_perm, self.dgates)
-        return self._experts_backward(dy, dloss)
+        self._input_grads(dy, dloss)
+        return self._finish_backward()
 
-    def _experts_backward(self, dy, dloss=None):
-        """The backward behind the combine's: dy_perm and dgates are in place, dy is read by the
-        shared expert alone."""
+    def _input_grads(self, dy, dloss=None):
+        """The backward behind the combine's, up to dx: dy_perm and dgates are in place, dy is read
+        by the shared expert alone.  wgrad1 is left to _finish_backward."""
         s = self.shape
         x, W1, W3, W2, Wr, g = self._params
         if self.recompute:  # regenerate a, b and h from the kept routed rows
@@ -302,8 +303,13 @@ class MoEExpertLayer:
             moe_permute_bwd_router(s, self.dx_perm, self.slot_row, self.topk_idx, self.dlogits, Wr, dx_add, self.dx)
         else:
             moe_permute_bwd(s, self.dx_perm, self.slot_row, dx_r, dx_add, self.dx)
+        return self.dx
+
+    def _finish_backward(self):
         # wgrad1 goes last: its gradient writes, the largest output of the step, would
         # otherwise push dx_perm out of the memory-side cache before the un-permute reads it
+        # (and dx, before a block's first norm does)
+        s = self.shape
         if self.mx_dispatch:
             moe_ffn_wgrad1_mx(s, self.xq_cols, self.xs_cols, self.dab, self.offsets, self.dW1, self.dW3, self.ws)
         else:
@@ -345,8 +351,8 @@ class MoEBlock:
 
     forward   moe_block_norm_fwd (unless xn is given) -> the layer's calls up to y_perm
               -> moe_combine_norm
-    backward  moe_combine_norm_bwd -> the layer's calls from dy_perm on
-              -> moe_block_norm_bwd (unless xn was given)
+    backward  moe_combine_norm_bwd -> the layer's calls from dy_perm to dx
+              -> moe_block_norm_bwd (unless xn was given) -> wgrad1
 
     y is never stored: the combine's norm takes it from registers and the backward gathers it
     again.  A layer with the MXFP8 dispatch writes its routed gradient rows in E4M3 from dy, so
@@ -406,12 +412,12 @@ class MoEBlock:
         else:
             moe_combine_norm_bwd(s, dv, dxn_next, self.v, L.y_perm, g, L.slot_row, y_add, *mid,
                                  None if y_add is None else self.dy, L.dy_perm, L.dgates, *tail)
-        dxn = L._experts_backward(self.dy, dloss)
-        if not self._own_pre:
-            return self.dv, dxn
-        moe_block_norm_bwd(s, self.dv, dxn, h, None, None, None, w_pre, None, self.rstd_pre, 1.0, self.dh, None, None,
-                           None, self.dw_pre, L.ws)
-        return self.dh
+        dxn = L._input_grads(self.dy, dloss)
+        if self._own_pre:
+            moe_block_norm_bwd(s, self.dv, dxn, h, None, None, None, w_pre, None, self.rstd_pre, 1.0, self.dh, None,
+                               None, None, self.dw_pre, L.ws)
+        L._finish_backward()
+        return self.dh if self._own_pre else (self.dv, dxn)
 
 
 class MoEExpertFunction(torch.autograd.Function):
