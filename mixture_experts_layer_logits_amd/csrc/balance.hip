@@ -10,8 +10,8 @@
 // at large T and launch latency below about 4 MB of scores.
 //
 // A token's scores lie across LPT lanes (a power of two, at most a wave, and at least k), 4
-// consecutive experts per 16-byte load and NV loads per lane, so a wave holds 64 / LPT tokens, the
-// softmax takes log2(LPT) exchange steps, and lane j holds the token's choice j.  Column sums stay
+// consecutive experts per 16-byte load and NV <= 4 loads per lane, so a wave holds 64 / LPT tokens,
+// the softmax takes log2(LPT) exchange steps, and lane j holds the token's choice j.  Column sums stay
 // in registers over a wave's tokens and meet in a fixed order: across the wave's tokens, the
 // workgroup's waves, then the workgroups (a second launch, in double), so the result is the same
 // bits on every run.
@@ -445,53 +445,73 @@ bool vec_ok(int E, const void* a, const void* b) {
   return E % 4 == 0 && ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15) == 0;
 }
 
-int lanes_per_token(int E, int k) {
+// How a token's scores lie in a wave: lanes (a power of two, at least k) and loads a lane.
+struct Layout {
+  int lanes, loads;
+  int tokens() const { return kWave / lanes; }  // of a wave
+};
+// Wide: one load a lane where a wave holds the row.  Dense: up to four, so that the work per token
+// that does not depend on E (reductions, addresses, choices) is shared by more tokens of a wave and
+// fewer lanes stay idle.
+Layout layout_of(int E, int k, bool dense) {
+  const int quads = (E + 3) / 4;
   int l = 1;
-  while (l < kWave && (4 * l < E || l < k)) l *= 2;
-  return l;
+  while (l < kWave && (l * (dense ? 4 : 1) < quads || l < k)) l *= 2;
+  return Layout{l, (quads + l - 1) / l};
 }
 
-// Calls f(LPT, NV) with the lanes per token and loads per lane that hold E scores and k choices.
-template <class F>
-hipError_t for_experts(int E, int k, F&& f) {
+// Calls f(LPT, NV) with a layout's constants (DENSE: also those that only a dense layout has).
+template <bool DENSE, class F>
+hipError_t for_layout(const Layout& y, F&& f) {
   using std::integral_constant;
-  switch (lanes_per_token(E, k)) {
-#define MOE_BAL_CASE(LPT) \
-  case LPT: return f(integral_constant<int, LPT>{}, integral_constant<int, 1>{});
-    MOE_BAL_CASE(1) MOE_BAL_CASE(2) MOE_BAL_CASE(4) MOE_BAL_CASE(8) MOE_BAL_CASE(16) MOE_BAL_CASE(32)
-#undef MOE_BAL_CASE
+#define MOE_BAL_CASE(LPT, NV) \
+  if (y.lanes == LPT && y.loads == NV) return f(integral_constant<int, LPT>{}, integral_constant<int, NV>{});
+  MOE_BAL_CASE(1, 1) MOE_BAL_CASE(2, 1) MOE_BAL_CASE(4, 1) MOE_BAL_CASE(8, 1) MOE_BAL_CASE(16, 1) MOE_BAL_CASE(32, 1)
+  MOE_BAL_CASE(64, 1) MOE_BAL_CASE(64, 2) MOE_BAL_CASE(64, 3) MOE_BAL_CASE(64, 4)
+  if constexpr (DENSE) {
+#define MOE_BAL_DENSE(LPT) MOE_BAL_CASE(LPT, 2) MOE_BAL_CASE(LPT, 3) MOE_BAL_CASE(LPT, 4)
+    MOE_BAL_DENSE(1) MOE_BAL_DENSE(2) MOE_BAL_DENSE(4) MOE_BAL_DENSE(8) MOE_BAL_DENSE(16) MOE_BAL_DENSE(32)
+#undef MOE_BAL_DENSE
   }
-  if (E <= 256) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  if (E <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+#undef MOE_BAL_CASE
+  return hipErrorInvalidValue;
 }
 
 // workgroups of `waves` waves that hold all tokens at once, up to `most`
-int balance_grid(int T, int E, int k, int waves, int most) {
-  const int64_t per = (int64_t)waves * (kWave / lanes_per_token(E, k));
+int balance_grid(int T, const Layout& y, int waves, int most) {
+  const int64_t per = (int64_t)waves * y.tokens();
   const int64_t g = (T + per - 1) / per;
   return (int)(g < 1 ? 1 : (g > most ? most : g));
 }
 // Four rounds of tokens or fewer stay in one workgroup: that takes less than a second launch would.
 // More are spread as wide as they go (T = 8192, E = 128: 9.6 us with 256 workgroups of one round,
 // 11.4 with 128 of two, 12.2 with 64 of four).
-int balance_fwd_grid(int T, int E, int k) {
-  const int g = balance_grid(T, E, k, kFwdWaves, kBalanceBlocks);
+int balance_fwd_grid(int T, const Layout& y) {
+  const int g = balance_grid(T, y, kFwdWaves, kBalanceBlocks);
   return g <= 4 ? 1 : g;
+}
+// Dense once the wide layout takes more than three rounds: T = 63383, E = 134, k = 2 29.9 -> 21.2 us,
+// T = 65521, E = 96, k = 6 19.3 -> 16.6, E = 128 and 256 the same; at two rounds it loses (T = 16384,
+// E = 128: 10.9 against 14.6).  The backward stays wide: with four loads a lane it keeps too few in
+// flight (T = 65536, E = 128, k = 4: 15.8 us against 19.8).
+Layout balance_fwd_layout(int T, int E, int k) {
+  const Layout wide = layout_of(E, k, false);
+  return (int64_t)T > 3ll * kBalanceBlocks * kFwdWaves * wide.tokens() ? layout_of(E, k, true) : wide;
 }
 
 }  // namespace
 
 size_t balance_workspace_bytes(int T, int E, int k) {
-  return kPartHeader + (size_t)balance_fwd_grid(T, E, k) * ((size_t)E * 2 + 2) * sizeof(float);
+  return kPartHeader + (size_t)balance_fwd_grid(T, balance_fwd_layout(T, E, k)) * ((size_t)E * 2 + 2) * sizeof(float);
 }
 
 hipError_t balance_forward(int T, int E, int k, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
                            float* lse, int32_t* counts, float* prob_mean, float* loss, void* ws, hipStream_t st) {
-  const int G = balance_fwd_grid(T, E, k);
+  const Layout y = balance_fwd_layout(T, E, k);
+  const int G = balance_fwd_grid(T, y);
   const BalancePart part = carve(ws, G, E);
   const bool vec = vec_ok(E, logits, logits);
-  const hipError_t err = for_experts(E, k, [&](auto lpt, auto nv) {
+  const hipError_t err = for_layout<true>(y, [&](auto lpt, auto nv) {
     const auto kern = vec ? balance_fwd_kernel<lpt(), nv(), true> : balance_fwd_kernel<lpt(), nv(), false>;
     hipLaunchKernelGGL(kern, dim3(G), dim3(kFwdThreads), 0, st, T, E, k, logits, topk_idx, mask, lse, part, counts,
                        prob_mean, loss);
@@ -507,9 +527,10 @@ hipError_t balance_backward(int T, int E, int k, const float* logits, const floa
                             const float* dloss, const float* dgates, const float* gates, const int32_t* topk_idx,
                             float* dlogits, hipStream_t st) {
   if (T == 0) return hipSuccess;
-  const int G = balance_grid(T, E, k, kWaves, device_cu_count() * 8);
+  const Layout y = layout_of(E, k, false);
+  const int G = balance_grid(T, y, kWaves, device_cu_count() * 8);
   const bool vec = vec_ok(E, logits, dlogits);
-  return for_experts(E, k, [&](auto lpt, auto nv) {
+  return for_layout<false>(y, [&](auto lpt, auto nv) {
     if (vec)
       hipLaunchKernelGGL((balance_bwd_kernel<lpt(), nv(), true>), dim3(G), dim3(kThreads), 0, st, T, E, k, logits, lse,
                          counts, dloss, dgates, gates, topk_idx, dlogits);

@@ -104,7 +104,9 @@ def _check_balance(b, L, idx, gates, dgates, mask, with_gates=True):
 
 @pytest.mark.parametrize("T,E,k", [
     (1, 1, 1), (1, 128, 4), (5, 2, 1), (64, 3, 3), (300, 8, 2), (1025, 8, 8), (257, 33, 4), (64, 64, 32), (513, 96, 6),
-    (2000, 128, 4), (77, 130, 5), (100, 256, 8), (63, 257, 2), (130, 1000, 4), (65, 1024, 32), (9001, 16, 2)])
+    (2000, 128, 4), (77, 130, 5), (100, 256, 8), (63, 257, 2), (130, 1000, 4), (65, 1024, 32), (9001, 16, 2),
+    # past three rounds of the widest layout: several loads a lane
+    (13000, 134, 2), (25001, 96, 6), (12500, 513, 8), (50003, 40, 1)])
 @pytest.mark.parametrize("masked", [False, True])
 def test_balance_against_oracle(T, E, k, masked):
     say(f"[gpu] balance T={T} E={E} k={k} masked={masked}")
