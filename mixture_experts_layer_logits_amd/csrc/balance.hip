@@ -6,8 +6,13 @@
 //   loss[0] = E / (k N) sum_e c_e mean_t p_e     (1 when choices and probabilities are even)
 //   loss[1] = mean_t lse(logits[t])^2
 //   dlogits[t, e] = p_e (g0 E / (k N) (c_e / N - sum_e' p_e' c_e' / N) + 2 g1 lse_t / N)
-// c_e is a count and has no gradient.  Both passes read the scores once; what bounds them is HBM
-// at large T and launch latency below about 4 MB of scores.
+// c_e is a count and has no gradient.  Both passes read the scores once.
+//
+// Measured on an MI355X, inputs in the memory-side cache: forward 4.8 us at T = 256, E = 8, k = 2
+// (one launch), 10.1 us at T = 8192, E = 128, k = 4 (two dependent launches, each latency), 19.1 us at
+// T = 65536 (1.8 TB/s; the choices' atomics are none of it and the exponentials 1.2 us, and twice the
+// workgroups take 20.3); backward 4.4 us at T = 8192 and 13.5 us (4.1 TB/s) at T = 65521, E = 96, k = 6,
+// where issuing its vector instructions alone takes about 8.
 //
 // A token's scores lie across LPT lanes (a power of two, at most a wave, and at least k), 4
 // consecutive experts per 16-byte load and NV <= 4 loads per lane, so a wave holds 64 / LPT tokens,

@@ -20,6 +20,12 @@
 // Weight gradients accumulate in registers over a workgroup's rows, meet across its waves in
 // LDS, go to one partial row per workgroup and are added by a second launch, all in a fixed
 // order (no atomics).
+//
+// Measured on an MI355X (a 2 + 2 GiB copy runs at 4.97 TB/s, 134 + 134 MB at 7.2 out of the
+// memory-side cache), bf16: forward with both norms 22.4 us at T = 8192, d = 2048 (6.0 TB/s), 2.4 us
+// for one row; backward 47.8 us (4.2 TB/s; 42 and the second launch); backward of the norm
+// before a block 103 us at T = 16384, d = 4096 (5.2 TB/s); combine with both norms at k = 4 58.4 us
+// at T = 8192, d = 2048 (4.6 TB/s), backward 336 us at T = 16384, d = 4096 (4.8 TB/s).
 #include "block.h"
 #include "gemm.h"
 #include "lanes.h"
@@ -35,8 +41,8 @@ constexpr bool gathers(int src) { return src == kGather || src == kGatherMany; }
 // The lanes that hold one row: LPR of a wave, or WPR whole waves.
 constexpr int rows_of(int lpr, int wpr, int nwaves) { return nwaves * (kWave / lpr) / wpr; }
 
-// Sums over the lanes of a row.  Over several waves, consecutive sums alternate between two LDS buffers, so one
-// barrier each is enough: a buffer is written again only after a later barrier.
+// Sums over the lanes of a row.  Over several waves, consecutive sums alternate between two LDS
+// buffers, so one barrier each is enough: a buffer is written again only after a later barrier.
 template <int LPR, int WPR, int NWAVES>
 struct RowSum {
   float (*buf)[NWAVES][4];
