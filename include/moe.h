@@ -442,7 +442,7 @@ moe_status moe_balance_bwd(const moe_shape* s, const float* logits, const float*
  * of exactly 0 drops the branch whatever y holds.  x, y, w_post [d], w_pre [d], v, xn act; gate
  * [T] float; rstd_post, rstd_pre [T] float: r(y) and r(v) for the backward (with w_post, w_pre).
  * v may be x (in place).  Each stored row is rounded once; xn is taken from the unrounded v.
- * Needs d <= 16384, eps > 0 and finite res_scale; a pointer that the call has no use for (xn
+ * Needs d <= 16384, eps > 0 (no denormal) and finite res_scale; a pointer that the call has no use for (xn
  * without w_pre, gate without y, ...) is MOE_EINVAL. */
 moe_status moe_block_norm_fwd(const moe_shape* s, const void* x, const void* y, const float* gate,
                               const void* w_post, const void* w_pre, float res_scale, float eps, void* v, void* xn,

@@ -134,12 +134,12 @@ moe_status check_rows(const moe_shape* s, std::initializer_list<const void*> ps)
 
 bool rows_ok(const moe_shape* s, const void* p) { return p || s->T == 0; }
 
-// Block-norm arguments that do not depend on the batch: the width the kernels hold, a positive
-// eps (forward) and a finite residual scale.
+// Block-norm arguments that do not depend on the batch: the width the kernels hold, a positive eps
+// that is no denormal (forward; a row of zeros has rsqrt(eps) as its rstd) and a finite residual scale.
 moe_status check_norm(const moe_shape* s, float res_scale, float eps) {
   MOE_TRY(check_shape(s));
   if (s->d > kNormMaxWidth) return MOE_EINVAL;
-  if (!std::isfinite(res_scale) || !std::isfinite(eps) || !(eps > 0.f)) return MOE_EINVAL;
+  if (!std::isfinite(res_scale) || !std::isnormal(eps) || eps < 0.f) return MOE_EINVAL;
   return MOE_OK;
 }
 

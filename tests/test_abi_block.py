@@ -52,7 +52,7 @@ REFUSED = (
     [("moe_balance_bwd", {n: 0}, MOE_ENULL) for n in BAL_BWD if n != "dgates"] +
     [("moe_block_norm_fwd", {n: 0}, MOE_ENULL) for n in ("x", "v", "xn", "rstd_post", "rstd_pre")] +
     [("moe_block_norm_fwd", {n: A + 8}, MOE_EALIGN) for n in ("x", "y", "w_post", "w_pre", "v", "xn")] +
-    [("moe_block_norm_fwd", dict(eps=e), MOE_EINVAL) for e in (0.0, -1e-6, math.nan, math.inf)] +
+    [("moe_block_norm_fwd", dict(eps=e), MOE_EINVAL) for e in (0.0, -1e-6, 1e-40, math.nan, math.inf)] +
     [("moe_block_norm_fwd", dict(res_scale=e), MOE_EINVAL) for e in (math.nan, -math.inf)] +
     # pointers the call has no use for
     [("moe_block_norm_fwd", dict(y=0), MOE_EINVAL), ("moe_block_norm_fwd", dict(w_pre=0), MOE_EINVAL),
