@@ -375,7 +375,8 @@ class MoEBlock:
         as MoEExpertLayer.forward.  Returns v; xn_next is left in the block."""
         if (xn is None) == (w_pre is None):
             raise ValueError("a block takes w_pre, or the xn of the block before")
-        if h.data_ptr() == self.v.data_ptr() or (xn is not None and xn.data_ptr() == self.xn_next.data_ptr()):
+        if h.numel() and (h.data_ptr() == self.v.data_ptr() or
+                          (xn is not None and xn.data_ptr() == self.xn_next.data_ptr())):
             raise ValueError("a block cannot read its own output: its backward needs what this forward overwrites")
         L, s = self.layer, self.layer.shape
         self._own_pre = xn is None

@@ -179,6 +179,22 @@ def test_a_stack_of_blocks_passes_its_norm_on():
         assert normwise_err(host(x), host(y)) <= TOL["bf16"] or moved, n
 
 
+def test_block_of_no_tokens():
+    """An empty batch: zero losses, counts and weight gradients."""
+    import mixture_experts_layer_logits_amd as m
+    w = workloads.scaled(W["e8_k4_t8192"], T=0, d=128, f=64)
+    say("[gpu] block of no tokens")
+    inp, e = workloads.make_inputs(w), _extra(w, 2, True, True, True)
+    block = m.MoEBlock(_layer(w, (0.5, 0.1)), 0.5, EPS)
+    L = block.layer
+    for t in (block.dw_pre, block.dw_post, block.dw_next, L.dWr, L.dW1, L.loss):
+        t.fill_(7)
+    v, dh = _run(block, w, inp, e)
+    assert v.shape == dh.shape == (0, 128)
+    for t in (block.dw_pre, block.dw_post, block.dw_next, L.dWr, L.dW1, L.loss, L.bal_counts):
+        assert not host(t).any()
+
+
 def test_block_refuses_its_own_output_as_input():
     import mixture_experts_layer_logits_amd as m
     w = workloads.scaled(W["e8_k4_t8192"], T=32, d=128, f=64)
