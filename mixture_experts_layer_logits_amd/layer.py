@@ -471,7 +471,7 @@ class MoEBlockFunction(torch.autograd.Function):
                                "activations are gone (one block object per in-flight forward)")
         dh = B.backward(dv.contiguous(), dloss=dloss.contiguous())
         _, gate, w_pre, w_post, _, _ = B._saved
-        dt = L.dtype
-        return (dh.clone(), B.dw_pre.to(dt), None if w_post is None else B.dw_post.to(dt),
-                None if gate is None else B.dgate.clone(), L.dWr.to(dt), L.dW1.clone(), L.dW3.clone(), L.dW2.clone(),
+        own = lambda t: t.to(L.dtype, copy=True)  # noqa: E731  (the buffers are the next backward's too)
+        return (own(dh), own(B.dw_pre), None if w_post is None else own(B.dw_post),
+                None if gate is None else B.dgate.clone(), own(L.dWr), own(L.dW1), own(L.dW3), own(L.dW2),
                 None, None, None)

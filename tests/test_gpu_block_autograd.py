@@ -1,0 +1,66 @@
+"""The autograd functions of the layer and of the block: what the caller holds afterwards, what the
+backward notices, and what is refused.  Values are the whole steps' (test_gpu_block_layer.py,
+test_gpu_parity.py); here two runs of the same calls are compared bit for bit."""
+import pytest
+import torch
+
+import workloads
+from gpu_common import say, to_dev
+
+pytestmark = pytest.mark.gpu
+
+W = workloads.WORKLOADS
+SMALL = {"f32": workloads.scaled(W["tiny_fp32"], T=48, d=64, f=64, E=8, k=2),
+         "bf16": workloads.scaled(W["e8_k4_t8192"], T=48, d=64, f=64)}
+BLOCK_LEAVES = ("h", "w_pre", "w_post", "gate", "Wr", "W1", "W3", "W2")
+
+
+class Block:
+    """Leaves, gradients to come in, and the block of one case."""
+    names = BLOCK_LEAVES
+
+    def __init__(self, act="bf16", seed=3, **kw):
+        import mixture_experts_layer_logits_amd as m
+        from mixture_experts_layer_logits_amd.layer import MoEBlockFunction
+        w = SMALL[act]
+        d = to_dev(workloads.make_inputs(w))
+        g = torch.Generator().manual_seed(seed)
+        dt = w.torch_dtype()
+        rnd = lambda *n: torch.randn(*n, generator=g)  # noqa: E731
+        L = m.MoEExpertLayer(w.T, w.d, w.f, w.E, w.k, act=m.MOE_F32 if act == "f32" else m.MOE_BF16,
+                             balance=(0.0, 0.0), **kw)
+        self.block, self.layer, self.fn = m.MoEBlock(L, 0.7), L, MoEBlockFunction
+        make = dict(h=d["x"], w_pre=(1 + 0.1 * rnd(w.d)).to(dt).cuda(), w_post=(1 + 0.1 * rnd(w.d)).to(dt).cuda(),
+                    gate=torch.sigmoid(rnd(w.T)).cuda(), Wr=d["Wr"], W1=d["W1"], W3=d["W3"], W2=d["W2"])
+        self.leaves = [make[n].clone().requires_grad_() for n in self.names]
+        self.dy = [(rnd(w.T, w.d).to(dt) * 0.1).cuda() for _ in range(2)]
+        self.owner = self.block
+
+    def loss(self, i=0):
+        v, loss = self.fn.apply(*self.leaves, self.owner)
+        return (v.float() * self.dy[i].float()).sum() + 0.5 * loss[0] + 0.1 * loss[1]
+
+    def grads(self, i=0):
+        return torch.autograd.grad(self.loss(i), self.leaves)
+
+    def buffers(self):
+        return [t for o in (self.layer, self.owner) for t in vars(o).values() if torch.is_tensor(t)]
+
+
+def _own_gradients(c):
+    """The gradients are the caller's own: no buffer of the layer or block among them, and a second
+    step leaves the first one's as they were."""
+    first = c.grads(0)
+    kept = [t.clone() for t in first]
+    owned = {t.untyped_storage().data_ptr() for t in c.buffers()}
+    second = c.grads(1)
+    torch.cuda.synchronize()
+    for n, a, k, b in zip(c.names, first, kept, second):
+        assert a.untyped_storage().data_ptr() not in owned, n
+        assert torch.equal(a, k) and not torch.equal(a, b), n
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_block_gradients_are_the_callers_own(act):
+    say(f"[gpu] block gradients kept over two steps {act}")
+    _own_gradients(Block(act))
