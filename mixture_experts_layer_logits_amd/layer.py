@@ -443,7 +443,7 @@ class MoEExpertFunction(torch.autograd.Function):
             raise RuntimeError("MoEExpertFunction: the layer ran another forward since this one; its saved "
                                "activations are gone (one layer object per in-flight forward)")
         L.backward(dy.contiguous())
-        return L.dx.clone(), L.dWr.to(L.dtype), L.dW1.clone(), L.dW3.clone(), L.dW2.clone(), None, None
+        return L.dx.clone(), L.dWr.to(L.dtype, copy=True), L.dW1.clone(), L.dW3.clone(), L.dW2.clone(), None, None
 
 
 class MoEBlockFunction(torch.autograd.Function):

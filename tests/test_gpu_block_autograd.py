@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import workloads
-from gpu_common import say, to_dev
+from gpu_common import make_layer, say, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -13,6 +13,7 @@ W = workloads.WORKLOADS
 SMALL = {"f32": workloads.scaled(W["tiny_fp32"], T=48, d=64, f=64, E=8, k=2),
          "bf16": workloads.scaled(W["e8_k4_t8192"], T=48, d=64, f=64)}
 BLOCK_LEAVES = ("h", "w_pre", "w_post", "gate", "Wr", "W1", "W3", "W2")
+LAYER_LEAVES = ("x", "Wr", "W1", "W3", "W2")
 
 
 class Block:
@@ -47,6 +48,23 @@ class Block:
         return [t for o in (self.layer, self.owner) for t in vars(o).values() if torch.is_tensor(t)]
 
 
+class Layer(Block):
+    names = LAYER_LEAVES
+
+    def __init__(self, act="bf16", seed=3, **kw):
+        from mixture_experts_layer_logits_amd.layer import MoEExpertFunction
+        w = SMALL[act]
+        d = to_dev(workloads.make_inputs(w))
+        self.layer = self.owner = make_layer(w, **kw)
+        self.fn = MoEExpertFunction
+        self.leaves = [d[n].clone().requires_grad_() for n in self.names]
+        g = torch.Generator().manual_seed(seed)
+        self.dy = [(torch.randn(w.T, w.d, generator=g).to(w.torch_dtype()) * 0.1).cuda() for _ in range(2)]
+
+    def loss(self, i=0):
+        return (self.fn.apply(*self.leaves, self.owner).float() * self.dy[i].float()).sum()
+
+
 def _own_gradients(c):
     """The gradients are the caller's own: no buffer of the layer or block among them, and a second
     step leaves the first one's as they were."""
@@ -64,3 +82,9 @@ def _own_gradients(c):
 def test_block_gradients_are_the_callers_own(act):
     say(f"[gpu] block gradients kept over two steps {act}")
     _own_gradients(Block(act))
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_layer_gradients_are_the_callers_own(act):
+    say(f"[gpu] layer gradients kept over two steps {act}")
+    _own_gradients(Layer(act))
