@@ -450,7 +450,8 @@ class MoEBlockFunction(torch.autograd.Function):
     """v, loss = block(h) with learned routing; gradients for h, w_pre, w_post, gate (float32 [T]
     or None), Wr, W1, W3, W2.  loss is the layer's float32 [2] of router losses (balance, z), to
     be weighted into the objective like any other value; its weights in the layer are not used.
-    The layer must have been made with ``balance``.  One forward at a time, as MoEExpertFunction."""
+    The layer must have been made with ``balance``.  One forward at a time, as MoEExpertFunction.
+    The inputs are autograd's saved tensors: one changed in place before the backward raises."""
 
     @staticmethod
     def forward(ctx, h, w_pre, w_post, gate, Wr, W1, W3, W2, block: MoEBlock, bias=None, mask=None):
@@ -458,8 +459,9 @@ class MoEBlockFunction(torch.autograd.Function):
         if L.balance is None:
             raise ValueError("MoEBlockFunction needs a layer with router losses (balance=(w_balance, w_z))")
         c = lambda t: None if t is None else t.contiguous()  # noqa: E731
-        v = block.forward(c(h), c(W1), c(W3), c(W2), w_pre=c(w_pre), w_post=c(w_post), gate=c(gate), Wr=c(Wr),
-                          bias=c(bias), mask=c(mask))
+        h, w_pre, w_post, gate, Wr, W1, W3, W2 = (c(t) for t in (h, w_pre, w_post, gate, Wr, W1, W3, W2))
+        v = block.forward(h, W1, W3, W2, w_pre=w_pre, w_post=w_post, gate=gate, Wr=Wr, bias=c(bias), mask=c(mask))
+        ctx.save_for_backward(h, w_pre, w_post, gate, Wr, W1, W3, W2)
         ctx.block, ctx.step = block, L.steps
         return v.clone(), L.loss.clone()
 
@@ -469,8 +471,11 @@ class MoEBlockFunction(torch.autograd.Function):
         if L.steps != ctx.step:
             raise RuntimeError("MoEBlockFunction: the layer ran another forward since this one; its saved "
                                "activations are gone (one block object per in-flight forward)")
+        # raises if one of them was changed in place since; under saved-tensor hooks, what these returned
+        h, w_pre, w_post, gate, Wr, W1, W3, W2 = ctx.saved_tensors
+        B._saved = (h, gate, w_pre, w_post, *B._saved[4:])
+        L._params = (L._params[0], W1, W3, W2, Wr, L._params[-1])
         dh = B.backward(dv.contiguous(), dloss=dloss.contiguous())
-        _, gate, w_pre, w_post, _, _ = B._saved
         own = lambda t: t.to(L.dtype, copy=True)  # noqa: E731  (the buffers are the next backward's too)
         return (own(dh), own(B.dw_pre), None if w_post is None else own(B.dw_post),
                 None if gate is None else B.dgate.clone(), own(L.dWr), own(L.dW1), own(L.dW3), own(L.dW2),

@@ -78,6 +78,28 @@ def _own_gradients(c):
         assert torch.equal(a, k) and not torch.equal(a, b), n
 
 
+def _notices(c, at):
+    """An input changed in place between the passes: the backward says so instead of computing with it."""
+    out = c.loss()
+    with torch.no_grad():
+        c.leaves[at].mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.backward()
+
+
+def _reads_what_was_saved(c):
+    """Tensors that saved-tensor hooks put elsewhere are what the backward computes with."""
+    want = c.grads()
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(), lambda t: t):
+        out = c.loss()
+    with torch.no_grad():
+        for t in c.leaves:
+            t.mul_(2)
+    got = torch.autograd.grad(out, c.leaves)
+    for n, a, b in zip(c.names, got, want):
+        assert torch.equal(a, b), n
+
+
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 def test_block_gradients_are_the_callers_own(act):
     say(f"[gpu] block gradients kept over two steps {act}")
@@ -88,3 +110,15 @@ def test_block_gradients_are_the_callers_own(act):
 def test_layer_gradients_are_the_callers_own(act):
     say(f"[gpu] layer gradients kept over two steps {act}")
     _own_gradients(Layer(act))
+
+
+@pytest.mark.parametrize("name", BLOCK_LEAVES)
+def test_block_backward_notices_an_input_changed_in_place(name):
+    say(f"[gpu] block, {name} changed in place")
+    _notices(Block(), BLOCK_LEAVES.index(name))
+
+
+@pytest.mark.parametrize("recompute", [False, True])
+def test_block_backward_reads_what_was_saved(recompute):
+    say(f"[gpu] block under saved-tensor hooks recompute={recompute}")
+    _reads_what_was_saved(Block(recompute=recompute))
