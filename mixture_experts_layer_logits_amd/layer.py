@@ -426,12 +426,14 @@ class MoEExpertFunction(torch.autograd.Function):
     gradients for x, Wr, W1, W3, W2.  The layer's buffers hold one forward at a time, so
     each backward must follow its own forward: a second forward through the same layer
     before the first one's backward makes that backward raise instead of returning the
-    second forward's gradients."""
+    second forward's gradients.  The inputs are autograd's saved tensors: one changed in place
+    before the backward makes it raise too."""
 
     @staticmethod
     def forward(ctx, x, Wr, W1, W3, W2, layer: MoEExpertLayer, bias=None):
-        y = layer.forward(x.contiguous(), W1.contiguous(), W3.contiguous(), W2.contiguous(), Wr=Wr.contiguous(),
-                          bias=None if bias is None else bias.contiguous())
+        x, Wr, W1, W3, W2 = (t.contiguous() for t in (x, Wr, W1, W3, W2))
+        y = layer.forward(x, W1, W3, W2, Wr=Wr, bias=None if bias is None else bias.contiguous())
+        ctx.save_for_backward(x, Wr, W1, W3, W2)
         ctx.layer = layer
         ctx.step = layer.steps
         return y.clone()
@@ -442,6 +444,9 @@ class MoEExpertFunction(torch.autograd.Function):
         if L.steps != ctx.step:
             raise RuntimeError("MoEExpertFunction: the layer ran another forward since this one; its saved "
                                "activations are gone (one layer object per in-flight forward)")
+        # raises if one of them was changed in place since; under saved-tensor hooks, what these returned
+        x, Wr, W1, W3, W2 = ctx.saved_tensors
+        L._params = (x, W1, W3, W2, Wr, L._params[-1])
         L.backward(dy.contiguous())
         return L.dx.clone(), L.dWr.to(L.dtype, copy=True), L.dW1.clone(), L.dW3.clone(), L.dW2.clone(), None, None
 

@@ -122,3 +122,15 @@ def test_block_backward_notices_an_input_changed_in_place(name):
 def test_block_backward_reads_what_was_saved(recompute):
     say(f"[gpu] block under saved-tensor hooks recompute={recompute}")
     _reads_what_was_saved(Block(recompute=recompute))
+
+
+@pytest.mark.parametrize("name", LAYER_LEAVES)
+def test_layer_backward_notices_an_input_changed_in_place(name):
+    say(f"[gpu] layer, {name} changed in place")
+    _notices(Layer(), LAYER_LEAVES.index(name))
+
+
+@pytest.mark.parametrize("recompute", [False, True])
+def test_layer_backward_reads_what_was_saved(recompute):
+    say(f"[gpu] layer under saved-tensor hooks recompute={recompute}")
+    _reads_what_was_saved(Layer(recompute=recompute))
