@@ -455,14 +455,17 @@ class MoEBlockFunction(torch.autograd.Function):
     """v, loss = block(h) with learned routing; gradients for h, w_pre, w_post, gate (float32 [T]
     or None), Wr, W1, W3, W2.  loss is the layer's float32 [2] of router losses (balance, z), to
     be weighted into the objective like any other value; its weights in the layer are not used.
-    The layer must have been made with ``balance``.  One forward at a time, as MoEExpertFunction.
-    The inputs are autograd's saved tensors: one changed in place before the backward raises."""
+    The layer must have been made with ``balance`` and without a shared expert.  One forward at
+    a time, as MoEExpertFunction.  The inputs are autograd's saved tensors: one changed in place
+    before the backward makes it raise."""
 
     @staticmethod
     def forward(ctx, h, w_pre, w_post, gate, Wr, W1, W3, W2, block: MoEBlock, bias=None, mask=None):
         L = block.layer
         if L.balance is None:
             raise ValueError("MoEBlockFunction needs a layer with router losses (balance=(w_balance, w_z))")
+        if L.shared_f:
+            raise ValueError("MoEBlockFunction takes no shared expert's weights: its layer must have none")
         c = lambda t: None if t is None else t.contiguous()  # noqa: E731
         h, w_pre, w_post, gate, Wr, W1, W3, W2 = (c(t) for t in (h, w_pre, w_post, gate, Wr, W1, W3, W2))
         v = block.forward(h, W1, W3, W2, w_pre=w_pre, w_post=w_post, gate=gate, Wr=Wr, bias=c(bias), mask=c(mask))

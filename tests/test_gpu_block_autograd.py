@@ -134,3 +134,12 @@ def test_layer_backward_notices_an_input_changed_in_place(name):
 def test_layer_backward_reads_what_was_saved(recompute):
     say(f"[gpu] layer under saved-tensor hooks recompute={recompute}")
     _reads_what_was_saved(Layer(recompute=recompute))
+
+
+def test_block_function_refuses_a_layer_with_a_shared_expert():
+    """It takes no shared weights, and v without the shared expert's part is another function."""
+    say("[gpu] block autograd with a shared expert's layer")
+    c = Block(shared_f=64)
+    with pytest.raises(ValueError, match="shared expert"):
+        c.loss()
+    assert c.layer.steps == 0
