@@ -421,6 +421,23 @@ class MoEBlock:
         return self.dh if self._own_pre else (self.dv, dxn)
 
 
+class _FirstOrder(torch.autograd.Function):
+    """Passes gradients on under create_graph.  They depend on `inputs`, but the kernels have no
+    derivative of the backward: going back through them raises, instead of leaving that part out."""
+
+    @staticmethod
+    def forward(ctx, n, *grads_and_inputs):
+        return grads_and_inputs[:n]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the expert layer's and the block's gradients have no second derivative")
+
+    @classmethod
+    def of(cls, grads, *inputs):
+        return cls.apply(len(grads), *grads, *inputs) if torch.is_grad_enabled() else grads
+
+
 class MoEExpertFunction(torch.autograd.Function):
     """y = MoE(x) with learned routing (optional constant per-expert router bias);
     gradients for x, Wr, W1, W3, W2.  The layer's buffers hold one forward at a time, so
@@ -448,7 +465,8 @@ class MoEExpertFunction(torch.autograd.Function):
         x, Wr, W1, W3, W2 = ctx.saved_tensors
         L._params = (x, W1, W3, W2, Wr, L._params[-1])
         L.backward(dy.contiguous())
-        return L.dx.clone(), L.dWr.to(L.dtype, copy=True), L.dW1.clone(), L.dW3.clone(), L.dW2.clone(), None, None
+        grads = L.dx.clone(), L.dWr.to(L.dtype, copy=True), L.dW1.clone(), L.dW3.clone(), L.dW2.clone()
+        return (*_FirstOrder.of(grads, dy, x, Wr, W1, W3, W2), None, None)
 
 
 class MoEBlockFunction(torch.autograd.Function):
@@ -485,6 +503,6 @@ class MoEBlockFunction(torch.autograd.Function):
         L._params = (L._params[0], W1, W3, W2, Wr, L._params[-1])
         dh = B.backward(dv.contiguous(), dloss=dloss.contiguous())
         own = lambda t: t.to(L.dtype, copy=True)  # noqa: E731  (the buffers are the next backward's too)
-        return (own(dh), own(B.dw_pre), None if w_post is None else own(B.dw_post),
-                None if gate is None else B.dgate.clone(), own(L.dWr), own(L.dW1), own(L.dW3), own(L.dW2),
-                None, None, None)
+        grads = (own(dh), own(B.dw_pre), None if w_post is None else own(B.dw_post),
+                 None if gate is None else B.dgate.clone(), own(L.dWr), own(L.dW1), own(L.dW3), own(L.dW2))
+        return (*_FirstOrder.of(grads, dv, dloss, h, w_pre, w_post, gate, Wr, W1, W3, W2), None, None, None)

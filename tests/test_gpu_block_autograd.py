@@ -100,6 +100,17 @@ def _reads_what_was_saved(c):
         assert torch.equal(a, b), n
 
 
+def _no_second_derivative(c):
+    """The kernels have no derivative of the backward: asking for one raises, it is not left out.  The
+    first derivatives are the same either way."""
+    want = c.grads()
+    got = torch.autograd.grad(c.loss(), c.leaves, create_graph=True)
+    for n, a, b in zip(c.names, got, want):
+        assert torch.equal(a, b), n
+        with pytest.raises(RuntimeError, match="second derivative"):
+            (a.float().square().sum() + c.leaves[0].float().sum()).backward(retain_graph=True)
+
+
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 def test_block_gradients_are_the_callers_own(act):
     say(f"[gpu] block gradients kept over two steps {act}")
@@ -143,3 +154,9 @@ def test_block_function_refuses_a_layer_with_a_shared_expert():
     with pytest.raises(ValueError, match="shared expert"):
         c.loss()
     assert c.layer.steps == 0
+
+
+@pytest.mark.parametrize("make", [Block, Layer])
+def test_second_derivatives_raise(make):
+    say(f"[gpu] second derivative of {make.__name__}")
+    _no_second_derivative(make())
