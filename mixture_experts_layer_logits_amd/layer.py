@@ -361,6 +361,7 @@ class MoEBlock:
 
     def __init__(self, layer: MoEExpertLayer, res_scale=1.0, eps=1e-6):
         self.layer, self.res_scale, self.eps = layer, float(res_scale), float(eps)
+        self._saved = None
         e, T, d, f32 = layer._e, layer.T, layer.d, torch.float32
         self.xn, self.v, self.xn_next = e(T, d), e(T, d), e(T, d)
         self.rstd_pre, self.rstd_post, self.rstd_next = e(T, dtype=f32), e(T, dtype=f32), e(T, dtype=f32)
@@ -379,13 +380,14 @@ class MoEBlock:
                           (xn is not None and xn.data_ptr() == self.xn_next.data_ptr())):
             raise ValueError("a block cannot read its own output: its backward needs what this forward overwrites")
         L, s = self.layer, self.layer.shape
-        self._own_pre = xn is None
-        if self._own_pre:
+        L._check_losses(topk_idx, mask)
+        if xn is None:
             xn = self.xn
             moe_block_norm_fwd(s, h, None, None, None, w_pre, 1.0, self.eps, None, xn, None, self.rstd_pre)
+        # from here on the forward before this one is overwritten, also if a later call is refused
+        self._saved, self._own_pre = None, w_pre is not None
         y_add = L._experts_forward(xn, W1, W3, W2, Wr, bias, topk_idx, gates, shared, mask)
         g = L._params[-1]
-        self._saved = (h, gate, w_pre, w_post, w_next, y_add)
         out = (gate, w_post, w_next, self.res_scale, self.eps, self.v, None if w_next is None else self.xn_next,
                None if w_post is None else self.rstd_post, None if w_next is None else self.rstd_next)
         if L.mx_dispatch:
@@ -393,12 +395,15 @@ class MoEBlock:
             moe_block_norm_fwd(s, h, L.y, *out)
         else:
             moe_combine_norm(s, L.y_perm, g, L.slot_row, y_add, h, *out)
+        self._saved = (h, gate, w_pre, w_post, w_next, y_add)
         return self.v
 
     def backward(self, dv, dxn_next=None, dloss=None):
         """dv [T, d] (None: v was used through xn_next only), dxn_next [T, d] with w_next, dloss as
         MoEExpertLayer.backward.  Returns dh; with a given xn, (dh, dxn) for the block before.
         dw_pre, dw_post, dw_next, dgate and the layer's gradients are left in their buffers."""
+        if self._saved is None:
+            raise RuntimeError("the block has no forward to go back through (none ran, or the last one was refused)")
         L, s = self.layer, self.layer.shape
         h, gate, w_pre, w_post, w_next, y_add = self._saved
         mid = (gate, w_post, w_next, None if w_post is None else self.rstd_post,

@@ -160,3 +160,34 @@ def test_block_function_refuses_a_layer_with_a_shared_expert():
 def test_second_derivatives_raise(make):
     say(f"[gpu] second derivative of {make.__name__}")
     _no_second_derivative(make())
+
+
+def test_block_refused_forward_leaves_the_one_before():
+    """A forward refused for its routing arguments writes nothing: the backward of the one before it is
+    the undisturbed one's.  One refused later has overwritten part of it: then the backward raises."""
+    say("[gpu] block forward refused between a forward and its backward")
+    c = Block()
+    B, L = c.block, c.layer
+    h, w_pre, w_post, gate, Wr, W1, W3, W2 = (t.detach() for t in c.leaves)
+    outs = lambda: [t.clone() for t in (B.dh, B.dw_pre, B.dw_post, L.dWr, L.dW1, L.dx)]  # noqa: E731
+    kw = dict(w_pre=w_pre, w_post=w_post, gate=gate)
+    B.forward(h, W1, W3, W2, Wr=Wr, **kw)
+    B.backward(c.dy[0])
+    want = outs()
+    B.forward(h, W1, W3, W2, Wr=Wr, **kw)
+    with pytest.raises(ValueError, match="learned routing"):
+        B.forward(h * 3, W1, W3, W2, topk_idx=L.topk_idx, gates=L.gates, **kw)
+    with pytest.raises(ValueError, match="learned routing"):
+        B.forward(h * 3, W1, W3, W2, xn=h, w_post=w_post, topk_idx=L.topk_idx, gates=L.gates)
+    B.backward(c.dy[0])
+    assert all(torch.equal(a, b) for a, b in zip(outs(), want))
+    out = c.loss()
+    with pytest.raises(ValueError, match="gate"):
+        B.forward(h * 3, W1, W3, W2, Wr=Wr, w_pre=w_pre, w_post=w_post, gate=gate.double())
+    with pytest.raises(RuntimeError, match="no forward"):
+        B.backward(c.dy[0])
+    with pytest.raises(RuntimeError, match="another forward"):
+        out.backward()
+    B.forward(h, W1, W3, W2, Wr=Wr, **kw)
+    B.backward(c.dy[0])
+    assert all(torch.equal(a, b) for a, b in zip(outs(), want))
