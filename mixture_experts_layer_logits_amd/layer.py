@@ -343,6 +343,12 @@ class MoEExpertLayer:
         return n
 
 
+def _shares(t, *others):
+    """Does t lie in the memory of one of `others`?"""
+    at = t.untyped_storage().data_ptr()
+    return t.numel() > 0 and any(at == o.untyped_storage().data_ptr() for o in others)
+
+
 class MoEBlock:
     """An expert layer between its norms (RMS norms over d, learned scales w_pre and w_post):
 
@@ -376,10 +382,12 @@ class MoEBlock:
         as MoEExpertLayer.forward.  Returns v; xn_next is left in the block."""
         if (xn is None) == (w_pre is None):
             raise ValueError("a block takes w_pre, or the xn of the block before")
-        if h.numel() and (h.data_ptr() == self.v.data_ptr() or
-                          (xn is not None and xn.data_ptr() == self.xn_next.data_ptr())):
-            raise ValueError("a block cannot read its own output: its backward needs what this forward overwrites")
         L, s = self.layer, self.layer.shape
+        # written before h or xn is read for the last time: by the norm, the combine, or the backward
+        work = (self.v, self.xn_next, self.dv, self.dy, L.dx, *((L.y,) if L.mx_dispatch else ()))
+        if _shares(h, *work, *((self.xn,) if xn is None else ())) or (xn is not None and _shares(xn, *work)):
+            raise ValueError("a block cannot read its own output or working buffers: this forward or its backward "
+                             "overwrites them")
         L._check_losses(topk_idx, mask)
         if xn is None:
             xn = self.xn

@@ -191,3 +191,37 @@ def test_block_refused_forward_leaves_the_one_before():
     B.forward(h, W1, W3, W2, Wr=Wr, **kw)
     B.backward(c.dy[0])
     assert all(torch.equal(a, b) for a, b in zip(outs(), want))
+
+
+def test_block_refuses_its_working_buffers_as_inputs():
+    """What the forward or the backward writes before it reads h or xn for the last time."""
+    say("[gpu] block on its own buffers")
+    c = Block()
+    B, L = c.block, c.layer
+    h, w_pre, w_post, _, Wr, W1, W3, W2 = (t.detach() for t in c.leaves)
+    B.forward(h, W1, W3, W2, w_pre=w_pre, w_post=w_post, w_next=w_pre, Wr=Wr)
+    for own in (B.xn, B.v, B.xn_next, B.dv, B.dy, L.dx):
+        with pytest.raises(ValueError, match="its own"):
+            B.forward(own, W1, W3, W2, w_pre=w_pre, Wr=Wr)
+        if own is not B.xn:
+            with pytest.raises(ValueError, match="its own"):
+                B.forward(h, W1, W3, W2, xn=own, Wr=Wr)
+    # its own norm's output is not written when it is given
+    B.forward(h, W1, W3, W2, w_pre=w_pre, w_post=w_post, Wr=Wr)
+    B.backward(c.dy[0])
+    want = [t.clone() for t in (B.v, B.dv, L.dWr)]
+    B.forward(h, W1, W3, W2, xn=B.xn, w_post=w_post, Wr=Wr)
+    B.backward(c.dy[0])
+    assert all(torch.equal(a, b) for a, b in zip((B.v, B.dv, L.dWr), want))
+
+
+def test_block_on_the_mxfp8_dispatch_refuses_the_layers_output():
+    """There the combine writes y before the norm reads h; elsewhere y is the layer's own forward's."""
+    import mixture_experts_layer_logits_amd as m
+    say("[gpu] block on its layer's y, MXFP8 dispatch")
+    L = m.MoEExpertLayer(16, 128, 128, 8, 2, gemm=m.MOE_MXFP8, mx_scope=m.MOE_MX_ALL)
+    B, w = m.MoEBlock(L), torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    idx = torch.arange(2, dtype=torch.int32, device="cuda").repeat(16, 1)
+    with pytest.raises(ValueError, match="its own"):
+        B.forward(L.y, None, None, None, w_pre=w, topk_idx=idx, gates=torch.ones(16, 2, device="cuda"))
+    assert L.steps == 0
