@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
 #pragma unroll
   for (int i = 0; i < NV; i++)
     *reinterpret_cast<float4*>(mine + 4 * (q + LPT * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_fence();
   const int n = counts[E];
   const float inv_n = n > 0 ? 1.f / (float)n : 0.f;
   float share[NV][4];  // c_e / N
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
       // lane j puts choice j's gradient where the lane that holds its column picks it up
       const float gv = g * (dg - group_sum<LPT>(g * dg));
       if (id >= 0 && id < E) atomicAdd(&mine[id], gv);
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_fence();
 #pragma unroll
       for (int i = 0; i < NV; i++) {
         if constexpr (VEC) {
@@ -424,9 +424,9 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(int T, int E, int
           for (int c = 0; c < 4; c++) p[i][c] += mine[column<LPT, VEC>(q, i, c)];
         }
       }
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_fence();
       if (id >= 0 && id < E) mine[id] = 0.f;
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_fence();
     }
     if (!in) continue;
     float* o = dlogits + t * E;

@@ -49,4 +49,12 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
+// Between a wave's own writes to LDS and its other lanes' reads: orders them for the compiler (the
+// hardware runs a wave's LDS accesses in order, so it costs no instruction).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 }  // namespace moe
