@@ -19,6 +19,7 @@
 
 #include "common.h"
 #include "gemm.h"
+#include "lanes.h"
 #include "route.h"
 
 // Fixed scratch of the allocation-free routing entry point: the per-chunk expert histograms
@@ -130,10 +131,10 @@ __global__ void __launch_bounds__(kThreads) route_chunk_kernel(int T, int E, int
       const uint64_t lower = mask & ((1ull << lane) - 1ull);
       int rank = 0;
       if (valid) rank = s_cnt[e] + __popcll(lower);
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_fence();
       const bool last = valid && ((mask >> lane) >> 1) == 0;  // highest lane of its expert group
       if (last) s_cnt[e] = rank + 1;
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_fence();
       if (valid) local_rank[(int64_t)t0 * k + s] = rank;
     }
   }

@@ -8,7 +8,7 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "csrc")
 
 
-@pytest.mark.parametrize("name", ["balance.hip"])
+@pytest.mark.parametrize("name", ["balance.hip", "route.hip"])
 def test_lds_exchanges_inside_a_wave_are_fenced(name):
     """A wave barrier alone orders scheduling, not memory: lanes that hand values on through LDS
     without a workgroup barrier use lanes.h's wave_lds_fence."""
