@@ -402,17 +402,17 @@ moe_status moe_ffn_dgrad1_mx(const moe_shape* s, const uint8_t* dabq_rows, const
  * --------------------------------------------------------------------------------------- */
 
 /* Balance loss, router z-loss and per-expert counts of a batch's routing.
- * A token t is kept unless mask[t] is 0 (a padded batch; mask NULL keeps all) or none of its
- * scores is above -inf; a token left out enters nothing, whatever its scores hold (inf, NaN).
+ * A token t is kept unless mask[t] is 0 (a padded batch; mask NULL keeps all) or each of its
+ * scores is -inf; a token left out enters nothing, whatever its scores hold (inf, NaN).
  * Over the N kept tokens, with p = softmax(logits[t]) over all E experts:
  *   counts[e] = c_e, how often topk_idx of a kept token names expert e;  counts[E] = N
  *   prob_mean[e] = mean p_e;  lse[t] = log sum_e exp(logits[t, e]) (-inf for a token left out)
  *   loss[0] = E / (k N) sum_e c_e prob_mean[e]  (1 when choices and probabilities are even)
  *   loss[1] = mean lse[t]^2
- * N = 0 gives zero losses and means.  Scores may be -inf (an expert out of use: p = 0).  Ids
- * outside [0, E) are clamped.  logits [T, E] float, topk_idx [T, k], mask [T] u8 or NULL; lse [T]
- * float, counts [E + 1] int32, prob_mean [E] and loss [2] float written.  Sums over tokens are
- * float inside a workgroup and double across workgroups. */
+ * N = 0 gives zero losses and means.  Scores may be -inf (an expert out of use: p = 0).  An id
+ * outside [0, E) is counted as the nearest expert.  logits [T, E] float, topk_idx [T, k], mask
+ * [T] u8 or NULL; lse [T] float, counts [E + 1] int32, prob_mean [E] and loss [2] float written.
+ * Sums over tokens are float inside a workgroup and double across workgroups. */
 moe_status moe_balance_fwd(const moe_shape* s, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
                            float* lse, int32_t* counts, float* prob_mean, float* loss, void* ws, size_t ws_bytes,
                            void* stream);
@@ -422,7 +422,8 @@ moe_status moe_balance_fwd(const moe_shape* s, const float* logits, const int32_
  *   dlogits[t, e] = p_e (dloss[0] E / (k N) (c_e / N - sum_e' p_e' c_e' / N) + 2 dloss[1] lse[t] / N)
  *                   + (e chosen by t: g_e (dgates_e - sum_j g_j dgates_j), as moe_route_bwd)
  * dgates, gates, topk_idx [T, k]: all three, or dgates NULL for the losses' gradient alone.  A
- * token left out (lse -inf) keeps its gates' gradient.  dlogits [T, E] float written in full; with
+ * token left out (lse -inf) keeps its gates' gradient; a choice whose id is outside [0, E) has
+ * none (as in moe_route_bwd, it enters sum_j alone).  dlogits [T, E] float written in full; with
  * dloss zero it is moe_route_bwd's but for the order in which sum_j is added.  dloss [2] float, on
  * the device.
  * Ranks of a data-parallel job that add up counts (all E + 1 of them) between the two calls get
