@@ -369,8 +369,10 @@ _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 
 
 def moe_balance_fwd(shape, logits, topk_idx, mask, lse, counts, prob_mean, loss, ws, stream=None):
-    """Balance loss, z-loss and per-expert counts of the kept tokens (mask: uint8 [T] or None)."""
+    """Balance loss, z-loss and per-expert counts of the kept tokens (mask: bool or uint8 [T], or None)."""
     T, E, k = shape.T, shape.E, shape.k
+    if mask is not None and mask.dtype is torch.bool:
+        mask = mask.view(_U8)  # the same bytes
     _call_checked("moe_balance_fwd", shape, (
         ("logits", logits, _F32, T * E), ("topk_idx", topk_idx, _I32, T * k), ("mask", mask, _U8, T),
         ("lse", lse, _F32, T), ("counts", counts, _I32, E + 1), ("prob_mean", prob_mean, _F32, E),

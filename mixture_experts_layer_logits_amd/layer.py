@@ -60,8 +60,8 @@ section "Παραλληλισμός, Ακρίβεια και Τεχνικές Μ
 
 Router losses (``balance=(w_balance, w_z)``, learned routing): the forward also runs
 moe_balance_fwd, which leaves the balance loss and the z-loss in ``loss``, the kept tokens'
-per-expert counts in ``bal_counts`` and the mean probabilities in ``prob_mean``; ``mask`` (uint8
-[T], 0 = padding) leaves tokens out of all of them.  The backward then takes the gradient of
+per-expert counts in ``bal_counts`` and the mean probabilities in ``prob_mean``; ``mask`` (bool or
+uint8 [T], 0 = padding) leaves tokens out of all of them.  The backward then takes the gradient of
 w_balance loss[0] + w_z loss[1] with the gates' (moe_balance_bwd instead of moe_route_bwd).  That
 gradient reaches every expert's score, so the router's input gradient is the dense
 dlogits Wr (``router_dx_fused`` is off).
@@ -199,7 +199,7 @@ class MoEExpertLayer:
 
     def forward(self, x, W1, W3, W2, Wr=None, bias=None, topk_idx=None, gates=None, shared=None, mask=None):
         """shared: (W1s [1, fs, d], W3s [1, fs, d], W2s [1, d, fs]) of the shared expert.
-        mask: uint8 [T], 0 for a token the router losses leave out."""
+        mask: bool or uint8 [T], 0 for a token the router losses leave out."""
         y_add = self._experts_forward(x, W1, W3, W2, Wr, bias, topk_idx, gates, shared, mask)
         moe_combine(self.shape, self.y_perm, self._params[-1], self.slot_row, y_add, self.y)
         return self.y

@@ -29,3 +29,21 @@ def test_ids_out_of_range_have_no_gate_gradient():
     mag = (g * (np.abs(dg) + (g * np.abs(dg)).sum(1, keepdims=True))).max(1, keepdims=True)
     assert np.all(np.abs(got - host(want)) <= 8 * F32 * mag)
     assert not got[4].any() and not got[9].any() and np.count_nonzero(got[11]) == 1
+
+
+def test_masks_of_truth_values():
+    """A bool mask is the same bytes as the uint8 one, in the calls and through the layer."""
+    import mixture_experts_layer_logits_amd as m
+    say("[gpu] balance forward, bool mask")
+    L, idx, gates, dgates = _balance_inputs(300, 8, 2, 3)
+    keep = torch.arange(300) % 3 != 1
+    a = Balance(L, idx, gates, dgates, keep.to(torch.uint8)).fwd()
+    b = Balance(L, idx, gates, dgates, keep).fwd()
+    for n in ("lse", "counts", "prob", "loss"):
+        assert torch.equal(getattr(a, n), getattr(b, n)), n
+    layer = m.MoEExpertLayer(300, 64, 64, 8, 2, balance=(1.0, 1.0))
+    x, Wr = torch.randn(300, 64, device="cuda").bfloat16(), torch.randn(8, 64, device="cuda").bfloat16()
+    layer.route(x, Wr, mask=keep.cuda())
+    assert int(layer.bal_counts[8]) == 200
+    with pytest.raises(ValueError, match="mask"):
+        Balance(L, idx, gates, dgates, keep.float()).fwd()
