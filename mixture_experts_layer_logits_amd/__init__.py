@@ -148,16 +148,37 @@ def _p(t):
     return t.data_ptr()
 
 
+# the handle and the index alone: a torch Stream object costs a microsecond
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream=None):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _launch(fn, dev, stream, *args):
+    """fn(*args, stream handle) on GPU `dev` (None: the current one), on that GPU's current stream if
+    none is given, whichever GPU is the current one."""
+    if dev is None or dev == _device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(stream))
+
+
+def _gpu_of(args):
+    """The GPU that the first tensor among the arguments lies on (None: raw pointers alone)."""
+    for a in args:
+        if a is not None and not isinstance(a, (int, ctypes.c_size_t)):
+            return a.get_device()
+    return None
 
 
 def _call(name, shape, *args, stream=None):
     lib = load_library()
-    st = getattr(lib, name)(ctypes.byref(shape), *[_p(a) if not isinstance(a, ctypes.c_size_t) else a for a in args],
-                            _stream(stream))
+    st = _launch(getattr(lib, name), _gpu_of(args), stream, ctypes.byref(shape),
+                 *[_p(a) if not isinstance(a, ctypes.c_size_t) else a for a in args])
     if st != 0:
         raise MoeError(name, st, lib.moe_status_str(st).decode())
 
@@ -267,7 +288,8 @@ def moe_tuning_reload():
 # ------------------------------------------------------------------ MXFP8
 def moe_mx_quantize(rows, cols, axis, seg_offsets, nseg, src, q, scales, stream=None):
     lib = load_library()
-    st = lib.moe_mx_quantize(rows, cols, axis, _p(seg_offsets), nseg, _p(src), _p(q), _p(scales), _stream(stream))
+    st = _launch(lib.moe_mx_quantize, _gpu_of((src, q)), stream, rows, cols, axis, _p(seg_offsets), nseg, _p(src),
+                 _p(q), _p(scales))
     if st != 0:
         raise MoeError("moe_mx_quantize", st, lib.moe_status_str(st).decode())
 
@@ -315,10 +337,6 @@ def moe_ffn_dgrad1_mx(shape, dabq_rows, dabs_rows, W1, W3, offsets, dx_perm, ws,
 
 
 # ------------------------------------------------------------------ around the layer
-# the handle and the index alone: a torch Stream object costs a microsecond
-_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-
 def _call_checked(name, shape, args, stream=None):
     """Call `name` with args in the C call's order: a tensor as (argument name, tensor or None, dtype,
     number of elements), anything else as it is.  Tensors have to lie on one GPU, contiguous, of
@@ -351,12 +369,7 @@ def _call_checked(name, shape, args, stream=None):
         if dtype is None:
             raw.append(t.numel() * t.element_size())
     lib = _lib or load_library()
-    fn = getattr(lib, name)
-    if dev is None or dev == _device():
-        st = fn(shape, *raw, _stream(stream) if stream is not None or dev is None else _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(shape, *raw, _stream(stream) if stream is not None else _raw_stream(dev))
+    st = _launch(getattr(lib, name), dev, stream, shape, *raw)
     if st != 0:
         raise MoeError(name, st, lib.moe_status_str(st).decode())
 
