@@ -158,11 +158,13 @@ def _stream(stream=None):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _launch(fn, dev, stream, *args):
+def _launch(fn, dev, stream, args):
     """fn(*args, stream handle) on GPU `dev` (None: the current one), on that GPU's current stream if
-    none is given, whichever GPU is the current one."""
-    if dev is None or dev == _device():
-        return fn(*args, _stream(stream))
+    none is given, whichever GPU is the current one.  args: a list, used up."""
+    here = _device()
+    if dev is None or dev == here:
+        args.append(_raw_stream(here) if stream is None else _stream(stream))
+        return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args, _stream(stream))
 
@@ -177,8 +179,8 @@ def _gpu_of(args):
 
 def _call(name, shape, *args, stream=None):
     lib = load_library()
-    st = _launch(getattr(lib, name), _gpu_of(args), stream, ctypes.byref(shape),
-                 *[_p(a) if not isinstance(a, ctypes.c_size_t) else a for a in args])
+    st = _launch(getattr(lib, name), _gpu_of(args), stream,
+                 [shape, *[_p(a) if not isinstance(a, ctypes.c_size_t) else a for a in args]])
     if st != 0:
         raise MoeError(name, st, lib.moe_status_str(st).decode())
 
@@ -288,8 +290,8 @@ def moe_tuning_reload():
 # ------------------------------------------------------------------ MXFP8
 def moe_mx_quantize(rows, cols, axis, seg_offsets, nseg, src, q, scales, stream=None):
     lib = load_library()
-    st = _launch(lib.moe_mx_quantize, _gpu_of((src, q)), stream, rows, cols, axis, _p(seg_offsets), nseg, _p(src),
-                 _p(q), _p(scales))
+    st = _launch(lib.moe_mx_quantize, _gpu_of((src, q)), stream,
+                 [rows, cols, axis, _p(seg_offsets), nseg, _p(src), _p(q), _p(scales)])
     if st != 0:
         raise MoeError("moe_mx_quantize", st, lib.moe_status_str(st).decode())
 
@@ -344,7 +346,7 @@ def _call_checked(name, shape, args, stream=None):
     behind it).  The call runs on that GPU's current stream if none is given, whichever device is
     the current one."""
     dev = None
-    raw = []
+    raw = [shape]
     for a in args:
         if type(a) is not tuple:
             raw.append(a)
@@ -369,7 +371,7 @@ def _call_checked(name, shape, args, stream=None):
         if dtype is None:
             raw.append(t.numel() * t.element_size())
     lib = _lib or load_library()
-    st = _launch(getattr(lib, name), dev, stream, shape, *raw)
+    st = _launch(getattr(lib, name), dev, stream, raw)
     if st != 0:
         raise MoeError(name, st, lib.moe_status_str(st).decode())
 
