@@ -131,8 +131,9 @@ struct Lane {
 // last batch (with k <= kBatch all of them) for the gate gradients.
 constexpr int kBatch = 4;
 // Rows past 8192 columns take 16 waves at two chunks a lane and at most 128 registers: there the
-// backward keeps no weights (they are read again each row), loads no row ahead, and at k > kBatch
-// gathers one routed row at a time.
+// backward keeps no weights (they are read again each row), loads no row ahead, and gathers one
+// routed row at a time.  With a branch that still spills (registers, bf16 / float: 77 / 188 with y, 99 /
+// 248 with routed rows; 2 / 6 without a branch; the float gathering forward 75).
 template <int C, int NWAVES> constexpr bool kTight = C == 2 && NWAVES == 16;
 
 template <typename T, int C>
@@ -228,9 +229,11 @@ __global__ void __launch_bounds__(NWAVES * 64) norm_fwd_kernel(const NormFwd a) 
   }
 }
 
-// Waves per SIMD the registers are held to: 4 (128 registers), which the bf16 kernels meet; float
-// rows that gather would spill there (44 to 53 registers), and so would two chunks a lane, so
-// they get twice as many.
+// Waves per SIMD the registers are held to: 4 (128 registers).  Up to 8192 columns the kernels without
+// a gather meet that, the bf16 gathering ones nearly (several rows a wave spill 7 to 10, 4 waves a row
+// with k > kBatch 2).  Float rows that gather would spill 44 to 53 registers there, and bf16 ones of
+// two chunks a lane too, so those get up to 256: the bf16 ones take 206, float 164 to 178, and float of
+// two chunks spills 83 to 95 even so.  12 waves a row have 168 (float gathers spill 4 to 11).
 template <typename T, int C, int SRC, int NWAVES>
 constexpr int bwd_waves_per_eu() {
   if (NWAVES > 8) return (NWAVES + 3) / 4;  // one workgroup a compute unit
@@ -485,16 +488,20 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(int d, int G, const float
 }
 
 // Calls f(LPR, WPR, C, NWAVES) with the lanes and waves per row, chunks per lane and waves per
-// workgroup that hold a row of d.  Rows between the steps leave lanes idle, which costs little: at 1.6 GB the
-// backward of combine and norm takes 382 us at d = 2560 on 8 waves a row (347 at 2048, 342 at 4096),
-// and 447 on 5, whose workgroups fill a compute unit worse.
+// workgroup that hold a row of d.  Rows between the steps leave lanes idle: at 1.6 GB the backward of combine
+// and norm takes 382 us at d = 2560 on 8 waves a row (347 at 2048, 342 at 4096), and 447 on 5, whose
+// workgroups fill a compute unit worse; just past a step, with nearly half of the lanes idle, bf16 rows
+// take a quarter more (d = 1088: 447 us against 359 at 1024; float 390 against 343).
 #define MOE_NORM_CASE(LPR, WPR, C, NWAVES)                                        \
   if (d <= LPR * WPR * C * 8)                                                     \
     return f(std::integral_constant<int, LPR>{}, std::integral_constant<int, WPR>{}, \
              std::integral_constant<int, C>{}, std::integral_constant<int, NWAVES>{});
 // Several narrow rows to a wave (combine and norm forward at T = 57912, d = 64, k = 7: 17 us against
-// 56) once there are more rows than waves that run at once; fewer rows take a wave each, whose
-// slots, gates and row sums are scalars (backward at T = 3, d = 256, k = 5: 6.8 us against 9.5).
+// 56) or, for fewer rows, a wave each, whose slots, gates and row sums are scalars (backward at T = 3,
+// d = 256, k = 5: 6.8 us against 9.5).  The backward decides the step: with both norms at d = 128, a wave
+// each against several takes 7.2 / 9.2 us against 7.6 / 8.1 at T = 2048 / 4096, and gathering k = 4 rows
+// 9.8 / 12.4 against 11.2 / 12.0 (d = 64 and 256 cross there too).  The forward gains from packing at any T
+// (4.2 against 3.7 us at T = 2048, d = 128, k = 4; 3.7 against 3.5 at 256) and shares the rule.
 constexpr int kPackRows = 2048;
 template <class F>
 hipError_t for_width_fwd(int T, int d, F&& f) {

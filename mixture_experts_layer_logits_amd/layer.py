@@ -452,12 +452,12 @@ class _FirstOrder(torch.autograd.Function):
 
 
 class MoEExpertFunction(torch.autograd.Function):
-    """y = MoE(x) with learned routing (optional constant per-expert router bias);
-    gradients for x, Wr, W1, W3, W2.  The layer's buffers hold one forward at a time, so
-    each backward must follow its own forward: a second forward through the same layer
-    before the first one's backward makes that backward raise instead of returning the
-    second forward's gradients.  The inputs are autograd's saved tensors: one changed in place
-    before the backward makes it raise too."""
+    """y = MoE(x) with learned routing (optional constant per-expert router bias), by the routed
+    experts alone (a layer's shared expert takes no part); gradients for x, Wr, W1, W3, W2.  The
+    layer's buffers hold one forward at a time, so each backward must follow its own forward: a
+    second forward through the same layer before the first one's backward makes that backward
+    raise instead of returning the second forward's gradients.  The inputs are autograd's saved
+    tensors: one changed in place before the backward makes it raise too."""
 
     @staticmethod
     def forward(ctx, x, Wr, W1, W3, W2, layer: MoEExpertLayer, bias=None):
