@@ -9,7 +9,7 @@
 // c_e is a count and has no gradient.  Both passes read the scores once.
 //
 // Measured on an MI355X, inputs in the memory-side cache: forward 4.8 us at T = 256, E = 8, k = 2
-// (one launch), 9.6 us at T = 8192, E = 128, k = 4 (two dependent launches, each latency), 19.2 us at
+// (one launch), 10.0 us at T = 8192, E = 128, k = 4 (two dependent launches, each latency), 19.2 us at
 // T = 65536: 14.6 (2.4 TB/s; its 4.2 M vector instructions issue in 7, and the waves wait through half
 // of their cycles, 16 of them a compute unit) and 4.7 of the second launch.  There the choices' atomics
 // are none of it and the exponentials 1.2 us, and twice the workgroups take 20.3.  Backward 4.4 us at T = 8192 and 13.5 us (4.1 TB/s) at T = 65521, E = 96, k = 6,
@@ -493,8 +493,8 @@ int balance_grid(int T, const Layout& y, int waves, int most) {
 // against two launches at 3, 4 and 5 rounds: 6.9 / 7.8 / 8.8 us against 8.0 / 8.2 / 8.0 at E = 128, 6.6 /
 // 7.2 / 8.0 against 7.2 / 7.3 / 7.3 at E = 8; at E = 64 and 1024 the fourth round is the second launch's
 // already (7.6 against 6.9, 14.3 against 12.6), the third is even.
-// More are spread as wide as they go (T = 8192, E = 128: 9.6 us with 256 workgroups of one round,
-// 11.4 with 128 of two, 12.2 with 64 of four).
+// More are spread as wide as they go (T = 8192, E = 128, side by side: 9.6 us with 256 workgroups of
+// one round, 11.4 with 128 of two, 12.2 with 64 of four).
 int balance_fwd_grid(int T, const Layout& y) {
   const int g = balance_grid(T, y, kFwdWaves, kBalanceBlocks);
   return g <= 4 ? 1 : g;

@@ -225,3 +225,32 @@ def test_block_on_the_mxfp8_dispatch_refuses_the_layers_output():
     with pytest.raises(ValueError, match="its own"):
         B.forward(L.y, None, None, None, w_pre=w, topk_idx=idx, gates=torch.ones(16, 2, device="cuda"))
     assert L.steps == 0
+
+
+@pytest.mark.parametrize("create_graph", [False, True])
+def test_block_function_without_the_norm_behind_and_the_gate(create_graph):
+    """None for w_post and gate: the gradients of the others are the block's own backward's."""
+    say(f"[gpu] block autograd, no w_post, no gate, create_graph={create_graph}")
+    c = Block("f32")
+    c.leaves[2] = c.leaves[3] = None
+    given = [t for t in c.leaves if t is not None]
+    v, loss = c.fn.apply(*c.leaves, c.block)
+    got = torch.autograd.grad([v, loss], given, [c.dy[0], torch.tensor([0.5, 0.1], device="cuda")],
+                              create_graph=create_graph)
+    h, w_pre, _, _, Wr, W1, W3, W2 = (None if t is None else t.detach() for t in c.leaves)
+    B, L = c.block, c.layer
+    assert torch.equal(B.forward(h, W1, W3, W2, w_pre=w_pre, Wr=Wr), v.detach())
+    B.backward(c.dy[0], dloss=torch.tensor([0.5, 0.1], device="cuda"))
+    for a, b in zip(got, (B.dh, B.dw_pre, L.dWr, L.dW1, L.dW3, L.dW2)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("make", [Block, Layer])
+def test_functions_under_inference_mode(make):
+    say(f"[gpu] {make.__name__} under inference_mode")
+    c = make()
+    want = c.fn.apply(*c.leaves, c.owner)
+    with torch.inference_mode():
+        got = c.fn.apply(*c.leaves, c.owner)
+    for a, b in zip(want, got):
+        assert torch.equal(a.detach(), b)
