@@ -8,12 +8,12 @@
 //   dlogits[t, e] = p_e (g0 E / (k N) (c_e / N - sum_e' p_e' c_e' / N) + 2 g1 lse_t / N)
 // c_e is a count and has no gradient.  Both passes read the scores once.
 //
-// Measured on an MI355X, inputs in the memory-side cache: forward 4.8 us at T = 256, E = 8, k = 2
-// (one launch), 10.0 us at T = 8192, E = 128, k = 4 (two dependent launches, each latency), 19.2 us at
-// T = 65536: 14.6 (2.4 TB/s; its 4.2 M vector instructions issue in 7, and the waves wait through half
-// of their cycles, 16 of them a compute unit) and 4.7 of the second launch.  There the choices' atomics
-// are none of it and the exponentials 1.2 us, and twice the workgroups take 20.3.  Backward 4.4 us at T = 8192 and 13.5 us (4.1 TB/s) at T = 65521, E = 96, k = 6,
-// where issuing its vector instructions alone takes about 8.
+// Measured on an MI355X, inputs in the memory-side cache.  Forward: 4.8 us at T = 256, E = 8, k = 2 (one
+// launch), 10.0 us at T = 8192, E = 128, k = 4 (two dependent launches, each latency), 19.2 us at T = 65536:
+// 14.6 (2.4 TB/s; its 4.2 M vector instructions issue in 7, and the waves, 16 a compute unit, wait
+// through half of their cycles) and 4.7 of the second launch; there the choices' atomics are none of it,
+// the exponentials 1.2 us, and twice the workgroups take 20.3.  Backward: 4.4 us at T = 8192 and 13.5 us
+// (4.1 TB/s) at T = 65521, E = 96, k = 6, where issuing its vector instructions alone takes about 8.
 //
 // A token's scores lie across LPT lanes (a power of two, at most a wave, and at least k), 4
 // consecutive experts per 16-byte load and NV <= 4 loads per lane, so a wave holds 64 / LPT tokens,
