@@ -484,6 +484,81 @@ moe_status moe_combine_norm_bwd(const moe_shape* s, const void* dv, const void* 
                                 size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Expert products with 4-bit weights (serving: forward only).  A decode batch reads every
+ * chosen expert's weights for a row or two, so their bytes are its cost (E experts with k
+ * chosen per token: ettayeb.fr, "Olmo-core 3 ouvre l'entraînement des MoE…", section "Le
+ * problème que les MoE n'ont jamais tout à fait résolu"; the 4-bit format is this library's
+ * reading, the block scales are those of its MXFP8).
+ *
+ * MXFP4 rows: E2M1 codes (bit 3 the sign, bits 0-2 an index into 0, .5, 1, 1.5, 2, 3, 4, 6),
+ * element 2i in the low half of byte i and 2i + 1 in the high half, and one scale byte b per
+ * 32 elements along the row: value = code 2^(b - 127).  255 stands for a block of NaN.
+ *   W1q, W3q [E, f, d/2], W1s, W3s [E, f, d/32];  W2q [E, d, f/2], W2s [E, d, f/32]
+ * Every buffer is 16-byte aligned.
+ * --------------------------------------------------------------------------------------- */
+
+/* rows x cols elements of `act` (MOE_F32 or MOE_BF16) -> MXFP4 rows, q [rows, cols/2], scales
+ * [rows, cols/32]; cols a multiple of 32.  2^(b - 127) is the smallest power of two with
+ * amax <= 6 2^(b - 127), not below 2^-126; elements are rounded to the nearest code, ties to the
+ * even one.  A block with an infinity or NaN becomes NaN. */
+moe_status moe_mx4_quantize(int32_t rows, int32_t cols, int32_t act, const void* src, uint8_t* q, uint8_t* scales,
+                            void* stream);
+
+/* h = silu(a) b with a = X_e W1_e^T, b = X_e W3_e^T in one kernel (a and b are not stored).
+ * x_perm [R, d] act, h [R, f] act written.  The rows are not quantised: the weights widen
+ * without a rounding and the sums are float (act MOE_BF16: bf16 products; MOE_F32: float).
+ * moe_shape.gemm plays no part.  Any R; laid out for few rows per expert. */
+moe_status moe_ffn_gemm1_fwd_w4(const moe_shape* s, const void* x_perm, const uint8_t* W1q, const uint8_t* W1s,
+                                const uint8_t* W3q, const uint8_t* W3s, const int32_t* offsets, void* h,
+                                void* stream);
+
+/* y_perm = h W2_e^T: h [R, f], y_perm [R, d] act (written).  As above. */
+moe_status moe_ffn_gemm2_fwd_w4(const moe_shape* s, const void* h, const uint8_t* W2q, const uint8_t* W2s,
+                                const int32_t* offsets, void* y_perm, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * 8-bit activation checkpoints: what the training step keeps between its passes in 8 bits
+ * instead of 16, or instead of computing it again (activation memory against throughput:
+ * unite.ai, "Ai2 κυκλοφορεί το Olmo-Core 3…", section "Παραλληλισμός, Ακρίβεια και Τεχνικές
+ * Μνήμης"; the 8-bit form is this library's reading).
+ *
+ * MXINT8 rows: codes q in [-127, 127] (int8) and one scale byte b per 32 elements along the
+ * row: value = q 2^(b - 133).  2^(b - 127) is the smallest power of two with
+ * amax <= 127/64 2^(b - 127), not below 2^-120; q is rounded to nearest, ties to even.  255
+ * stands for a block of NaN (a block with an infinity or NaN becomes one).  An element is off by
+ * at most amax / 127 of its block.  Every buffer is 16-byte aligned.
+ * --------------------------------------------------------------------------------------- */
+
+/* rows x cols elements of `act` (MOE_F32 or MOE_BF16) <-> MXINT8 rows, q [rows, cols], scales
+ * [rows, cols/32]; cols a multiple of 32.  unpack: with h (else NULL) the rows are [a | b] with
+ * cols = 2f, f a multiple of 32, and h [rows, f] = silu(a) b is written beside dst. */
+moe_status moe_ckpt8_pack(int32_t rows, int32_t cols, int32_t act, const void* src, int8_t* q, uint8_t* scales,
+                          void* stream);
+moe_status moe_ckpt8_unpack(int32_t rows, int32_t cols, int32_t act, const int8_t* q, const uint8_t* scales,
+                            void* dst, void* h, void* stream);
+
+/* moe_ffn_gemm1_fwd (bf16) with [a | b] written as MXINT8 rows by the epilogue, from the float
+ * sums: abq [R, 2f], ab_s [R, 2f/32]; h as there.  MOE_EUNSUPPORTED for act MOE_F32 or GEMM1 in
+ * the MXFP8 scope. */
+moe_status moe_ffn_gemm1_fwd_c8(const moe_shape* s, const void* x_perm, const void* W1, const void* W3,
+                                const int32_t* offsets, void* h, int8_t* abq, uint8_t* ab_s, void* stream);
+
+/* moe_ffn_dgrad2 (bf16) with a and b taken from those rows; h [R, f] = silu(a) b is written again
+ * for moe_ffn_wgrad2.  MOE_EUNSUPPORTED for act MOE_F32 or dgrad2 in the MXFP8 scope. */
+moe_status moe_ffn_dgrad2_c8(const moe_shape* s, const void* dy_perm, const void* W2, const int8_t* abq,
+                             const uint8_t* ab_s, const int32_t* offsets, void* dab, void* h, void* stream);
+
+/* moe_combine (the same y, bit for bit) with the routed rows it gathers also written as MXINT8
+ * rows: yq [R, d], ys [R, d/32].  y_perm is not needed afterwards. */
+moe_status moe_combine_c8(const moe_shape* s, const void* y_perm, const float* gates, const int32_t* slot_row,
+                          const void* y_add, void* y, int8_t* yq, uint8_t* ys, void* stream);
+
+/* moe_combine_bwd with y_perm taken from those rows. */
+moe_status moe_combine_bwd_c8(const moe_shape* s, const void* dy, const int8_t* yq, const uint8_t* ys,
+                              const float* gates, const int32_t* slot_row, void* dy_perm, float* dgates,
+                              void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * moe_tuning_reload: forget the tuning overrides read so far (see the file header), so each
  * is read from the environment again at its next use.  For tuning sweeps and tests that
  * change them within one process; it must not run while another host thread launches

@@ -102,9 +102,24 @@ _SIGS = {
     "moe_block_norm_bwd": [_VP] * 9 + [_F] + [_VP] * 6 + [_SZ, _VP],
     "moe_combine_norm": [_VP] * 8 + [_F, _F] + [_VP] * 5,
     "moe_combine_norm_bwd": [_VP] * 12 + [_F] + [_VP] * 8 + [_SZ, _VP],
+    # expert products with 4-bit weights
+    "moe_ffn_gemm1_fwd_w4": [_VP] * 8,
+    "moe_ffn_gemm2_fwd_w4": [_VP] * 6,
+    # 8-bit activation checkpoints
+    "moe_ffn_gemm1_fwd_c8": [_VP] * 8,
+    "moe_ffn_dgrad2_c8": [_VP] * 8,
+    "moe_combine_c8": [_VP] * 8,
+    "moe_combine_bwd_c8": [_VP] * 8,
 }
-EXPORTED = sorted(list(_SIGS) + ["moe_mx_quantize", "moe_workspace_size", "moe_mx_cols_ld", "moe_status_str",
-                                  "moe_tuning_reload"])
+# entry points without a shape argument
+_I32T = ctypes.c_int32
+_BLOCK_SIGS = {
+    "moe_mx4_quantize": [_I32T] * 3 + [_VP] * 4,
+    "moe_ckpt8_pack": [_I32T] * 3 + [_VP] * 4,
+    "moe_ckpt8_unpack": [_I32T] * 3 + [_VP] * 5,
+}
+EXPORTED = sorted(list(_SIGS) + list(_BLOCK_SIGS) + ["moe_mx_quantize", "moe_workspace_size", "moe_mx_cols_ld",
+                                                     "moe_status_str", "moe_tuning_reload"])
 
 _lib = None
 
@@ -120,6 +135,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     for name, args in _SIGS.items():
         fn = getattr(lib, name)
         fn.argtypes = [_SHP] + args
+        fn.restype = ctypes.c_int
+    for name, args in _BLOCK_SIGS.items():
+        fn = getattr(lib, name)
+        fn.argtypes = args
         fn.restype = ctypes.c_int
     lib.moe_mx_quantize.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP, ctypes.c_int32, _VP, _VP,
                                     _VP, _VP]
@@ -340,13 +359,13 @@ def moe_ffn_dgrad1_mx(shape, dabq_rows, dabs_rows, W1, W3, offsets, dx_perm, ws,
 
 # ------------------------------------------------------------------ around the layer
 def _call_checked(name, shape, args, stream=None):
-    """Call `name` with args in the C call's order: a tensor as (argument name, tensor or None, dtype,
+    """Call `name` with shape (None: the call takes none) and args in the C call's order: a tensor as (argument name, tensor or None, dtype,
     number of elements), anything else as it is.  Tensors have to lie on one GPU, contiguous, of
     that type and size (dtype None: a workspace of any type, whose size in bytes is passed on
     behind it).  The call runs on that GPU's current stream if none is given, whichever device is
     the current one."""
     dev = None
-    raw = [shape]
+    raw = [] if shape is None else [shape]
     for a in args:
         if type(a) is not tuple:
             raw.append(a)
@@ -451,4 +470,98 @@ def moe_combine_norm_bwd(shape, dv, dxn, v, y_perm, gates, slot_row, y_add, gate
         ("dw_post", dw_post, _F32, d), ("dw_pre", dw_pre, _F32, d), ("ws", ws, None, 0)), stream)
 
 
-from .layer import MoEBlock, MoEExpertLayer  # noqa: E402  (re-export)
+# ------------------------------------------------------------------ 4-bit weights
+_I8 = torch.int8
+
+
+def _act_of(name, t):
+    """The `act` argument of a call on rows of blocks: the rows' own type."""
+    if t.dtype is not _F32 and t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name}: rows must be float32 or bfloat16, got {t.dtype}")
+    return MOE_F32 if t.dtype is _F32 else MOE_BF16
+
+
+def moe_mx4_quantize(rows, cols, src, q, scales, stream=None):
+    """MXFP4 of src [rows, cols] (float32 or bfloat16): q uint8 [rows, cols/2], scales uint8 [rows, cols/32]."""
+    n = rows * cols
+    _call_checked("moe_mx4_quantize", None, (
+        rows, cols, _act_of("moe_mx4_quantize", src), ("src", src, src.dtype, n), ("q", q, _U8, n // 2),
+        ("scales", scales, _U8, n // 32)), stream)
+
+
+def moe_ffn_gemm1_fwd_w4(shape, x_perm, W1q, W1s, W3q, W3s, offsets, h, stream=None):
+    """h = silu(X_e W1_e^T) (X_e W3_e^T) with MXFP4 weights."""
+    d, f, E, a = shape.d, shape.f, shape.E, _act(shape)
+    R = shape.T * shape.k
+    _call_checked("moe_ffn_gemm1_fwd_w4", shape, (
+        ("x_perm", x_perm, a, R * d), ("W1q", W1q, _U8, E * f * d // 2), ("W1s", W1s, _U8, E * f * d // 32),
+        ("W3q", W3q, _U8, E * f * d // 2), ("W3s", W3s, _U8, E * f * d // 32), ("offsets", offsets, _I32, E + 1),
+        ("h", h, a, R * f)), stream)
+
+
+def moe_ffn_gemm2_fwd_w4(shape, h, W2q, W2s, offsets, y_perm, stream=None):
+    """y_perm = h W2_e^T with MXFP4 weights."""
+    d, f, E, a = shape.d, shape.f, shape.E, _act(shape)
+    R = shape.T * shape.k
+    _call_checked("moe_ffn_gemm2_fwd_w4", shape, (
+        ("h", h, a, R * f), ("W2q", W2q, _U8, E * d * f // 2), ("W2s", W2s, _U8, E * d * f // 32),
+        ("offsets", offsets, _I32, E + 1), ("y_perm", y_perm, a, R * d)), stream)
+
+
+# ------------------------------------------------------------------ 8-bit activation checkpoints
+def moe_ckpt8_pack(rows, cols, src, q, scales, stream=None):
+    """MXINT8 of src [rows, cols] (float32 or bfloat16): q int8 [rows, cols], scales uint8 [rows, cols/32]."""
+    n = rows * cols
+    _call_checked("moe_ckpt8_pack", None, (
+        rows, cols, _act_of("moe_ckpt8_pack", src), ("src", src, src.dtype, n), ("q", q, _I8, n),
+        ("scales", scales, _U8, n // 32)), stream)
+
+
+def moe_ckpt8_unpack(rows, cols, q, scales, dst, h=None, stream=None):
+    """The values of MXINT8 rows, in dst's type; with h [rows, cols/2] also silu of each row's first half
+    times its second."""
+    n = rows * cols
+    _call_checked("moe_ckpt8_unpack", None, (
+        rows, cols, _act_of("moe_ckpt8_unpack", dst), ("q", q, _I8, n), ("scales", scales, _U8, n // 32),
+        ("dst", dst, dst.dtype, n), ("h", h, dst.dtype, n // 2)), stream)
+
+
+def moe_ffn_gemm1_fwd_c8(shape, x_perm, W1, W3, offsets, h, abq, ab_s, stream=None):
+    """moe_ffn_gemm1_fwd (bf16) with [a | b] kept as MXINT8 rows."""
+    d, f, E, a = shape.d, shape.f, shape.E, _act(shape)
+    R = shape.T * shape.k
+    _call_checked("moe_ffn_gemm1_fwd_c8", shape, (
+        ("x_perm", x_perm, a, R * d), ("W1", W1, a, E * f * d), ("W3", W3, a, E * f * d),
+        ("offsets", offsets, _I32, E + 1), ("h", h, a, R * f), ("abq", abq, _I8, R * 2 * f),
+        ("ab_s", ab_s, _U8, R * 2 * f // 32)), stream)
+
+
+def moe_ffn_dgrad2_c8(shape, dy_perm, W2, abq, ab_s, offsets, dab, h, stream=None):
+    """moe_ffn_dgrad2 (bf16) with a and b from MXINT8 rows; writes h again."""
+    d, f, E, a = shape.d, shape.f, shape.E, _act(shape)
+    R = shape.T * shape.k
+    _call_checked("moe_ffn_dgrad2_c8", shape, (
+        ("dy_perm", dy_perm, a, R * d), ("W2", W2, a, E * d * f), ("abq", abq, _I8, R * 2 * f),
+        ("ab_s", ab_s, _U8, R * 2 * f // 32), ("offsets", offsets, _I32, E + 1), ("dab", dab, a, R * 2 * f),
+        ("h", h, a, R * f)), stream)
+
+
+def moe_combine_c8(shape, y_perm, gates, slot_row, y_add, y, yq, ys, stream=None):
+    """moe_combine, with the routed rows also written as MXINT8 rows."""
+    T, d, k, a = shape.T, shape.d, shape.k, _act(shape)
+    n = T * d
+    _call_checked("moe_combine_c8", shape, (
+        ("y_perm", y_perm, a, n * k), ("gates", gates, _F32, T * k), ("slot_row", slot_row, _I32, T * k),
+        ("y_add", y_add, a, n), ("y", y, a, n), ("yq", yq, _I8, n * k), ("ys", ys, _U8, n * k // 32)), stream)
+
+
+def moe_combine_bwd_c8(shape, dy, yq, ys, gates, slot_row, dy_perm, dgates, stream=None):
+    """moe_combine_bwd with the routed rows read as MXINT8 rows."""
+    T, d, k, a = shape.T, shape.d, shape.k, _act(shape)
+    n = T * d
+    _call_checked("moe_combine_bwd_c8", shape, (
+        ("dy", dy, a, n), ("yq", yq, _I8, n * k), ("ys", ys, _U8, n * k // 32), ("gates", gates, _F32, T * k),
+        ("slot_row", slot_row, _I32, T * k), ("dy_perm", dy_perm, a, n * k), ("dgates", dgates, _F32, T * k)), stream)
+
+
+from .layer import MoEBlock, MoEExpertLayer, quantize_weights  # noqa: E402  (re-export)

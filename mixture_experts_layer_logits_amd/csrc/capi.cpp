@@ -15,9 +15,11 @@
 
 #include "../../include/moe.h"
 #include "block.h"
+#include "ckpt8.h"
 #include "gemm.h"
 #include "mx.h"
 #include "route.h"
+#include "w4.h"
 
 namespace moe {
 
@@ -189,6 +191,13 @@ moe_status norm_bwd(const moe_shape* s, bool branch, const NormBwd& a, size_t ws
     MOE_TRY(check_opt({a.dv, a.v, a.y, a.w_post, a.w_pre, a.y_add, a.dy}));
   }
   return launched(block_norm_backward(elem_bytes(s), a, st));
+}
+
+// rows of whole 32-element blocks in a supported type
+moe_status check_blocks(int32_t rows, int32_t cols, int32_t act) {
+  if (rows < 0 || cols <= 0 || cols % 32 != 0) return MOE_EINVAL;
+  if (act != MOE_F32 && act != MOE_BF16) return MOE_EUNSUPPORTED;
+  return MOE_OK;
 }
 
 GemmShape gshape(const moe_shape* s) { return GemmShape{s->T * s->k, s->d, s->f, s->E}; }
@@ -642,6 +651,96 @@ moe_status moe_ffn_dgrad1_mx(const moe_shape* s, const uint8_t* dabq_rows, const
   if (ws_bytes < mx_workspace_bytes(g.R, g.d, g.f, g.E)) return MOE_EWORKSPACE;
   return launched(dgrad1_mx(g, offsets, nullptr, (const bf16_t*)W1, (const bf16_t*)W3, (bf16_t*)dx_perm, ws, S(st),
                             MxIn{dabq_rows, dabs_rows}));
+}
+
+// ---------------------------------------------------------------------------------------
+// Expert products with 4-bit weights
+// ---------------------------------------------------------------------------------------
+moe_status moe_mx4_quantize(int32_t rows, int32_t cols, int32_t act, const void* src, uint8_t* q, uint8_t* scales,
+                            void* st) {
+  MOE_TRY(check_blocks(rows, cols, act));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(check_ptrs({src, q, scales}));
+  return launched(mx4_quantize_rows(act == MOE_F32 ? 4 : 2, rows, cols, src, q, scales, S(st)));
+}
+
+moe_status moe_ffn_gemm1_fwd_w4(const moe_shape* s, const void* x_perm, const uint8_t* W1q, const uint8_t* W1s,
+                                const uint8_t* W3q, const uint8_t* W3s, const int32_t* offsets, void* h, void* st) {
+  MOE_TRY(check_shape(s));
+  MOE_TRY(check_ptrs({W1q, W1s, W3q, W3s}));
+  MOE_TRY(check_rows(s, {x_perm, h}));
+  if (!offsets) return MOE_ENULL;
+  return launched(gemm1_fwd_w4(elem_bytes(s), gshape(s), offsets, x_perm, W1q, W1s, W3q, W3s, h, S(st)));
+}
+
+moe_status moe_ffn_gemm2_fwd_w4(const moe_shape* s, const void* h, const uint8_t* W2q, const uint8_t* W2s,
+                                const int32_t* offsets, void* y_perm, void* st) {
+  MOE_TRY(check_shape(s));
+  MOE_TRY(check_ptrs({W2q, W2s}));
+  MOE_TRY(check_rows(s, {h, y_perm}));
+  if (!offsets) return MOE_ENULL;
+  return launched(gemm2_fwd_w4(elem_bytes(s), gshape(s), offsets, h, W2q, W2s, y_perm, S(st)));
+}
+
+// ---------------------------------------------------------------------------------------
+// 8-bit activation checkpoints
+// ---------------------------------------------------------------------------------------
+moe_status moe_ckpt8_pack(int32_t rows, int32_t cols, int32_t act, const void* src, int8_t* q, uint8_t* scales,
+                          void* st) {
+  MOE_TRY(check_blocks(rows, cols, act));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(check_ptrs({src, q, scales}));
+  return launched(ck8_pack_rows(act == MOE_F32 ? 4 : 2, rows, cols, src, q, scales, S(st)));
+}
+
+moe_status moe_ckpt8_unpack(int32_t rows, int32_t cols, int32_t act, const int8_t* q, const uint8_t* scales, void* dst,
+                            void* h, void* st) {
+  MOE_TRY(check_blocks(rows, cols, act));
+  if (h && cols % (2 * kCk8Block) != 0) return MOE_EINVAL;
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(check_ptrs({q, scales, dst}));
+  MOE_TRY(check_opt({h}));
+  return launched(ck8_unpack_rows(act == MOE_F32 ? 4 : 2, rows, cols, q, scales, dst, h, S(st)));
+}
+
+moe_status moe_ffn_gemm1_fwd_c8(const moe_shape* s, const void* x_perm, const void* W1, const void* W3,
+                                const int32_t* offsets, void* h, int8_t* abq, uint8_t* ab_s, void* st) {
+  MOE_TRY(check_shape(s));
+  if (s->act != MOE_BF16 || mx_on(s, MOE_MX_GEMM1)) return MOE_EUNSUPPORTED;
+  MOE_TRY(check_ptrs({W1, W3}));
+  MOE_TRY(check_rows(s, {x_perm, h, abq, ab_s}));
+  if (!offsets) return MOE_ENULL;
+  return launched(gemm1_fwd_c8_bf16(gshape(s), offsets, (const bf16_t*)x_perm, (const bf16_t*)W1, (const bf16_t*)W3,
+                                    (bf16_t*)h, abq, ab_s, S(st)));
+}
+
+moe_status moe_ffn_dgrad2_c8(const moe_shape* s, const void* dy_perm, const void* W2, const int8_t* abq,
+                             const uint8_t* ab_s, const int32_t* offsets, void* dab, void* h, void* st) {
+  MOE_TRY(check_shape(s));
+  if (s->act != MOE_BF16 || mx_on(s, MOE_MX_DGRAD2)) return MOE_EUNSUPPORTED;
+  MOE_TRY(check_ptrs({W2}));
+  MOE_TRY(check_rows(s, {dy_perm, abq, ab_s, dab, h}));
+  if (!offsets) return MOE_ENULL;
+  return launched(dgrad2_c8_bf16(gshape(s), offsets, (const bf16_t*)dy_perm, (const bf16_t*)W2, abq, ab_s, (bf16_t*)dab,
+                                 (bf16_t*)h, S(st)));
+}
+
+moe_status moe_combine_c8(const moe_shape* s, const void* y_perm, const float* gates, const int32_t* slot_row,
+                          const void* y_add, void* y, int8_t* yq, uint8_t* ys, void* st) {
+  MOE_TRY(check_shape(s));
+  MOE_TRY(check_rows(s, {y_perm, y, yq, ys}));
+  if (!rows_ok(s, gates) || !rows_ok(s, slot_row)) return MOE_ENULL;
+  MOE_TRY(check_opt({y_add}));
+  return launched(combine_rows_c8(elem_bytes(s), s->T, s->d, s->k, y_perm, gates, slot_row, y_add, y, yq, ys, S(st)));
+}
+
+moe_status moe_combine_bwd_c8(const moe_shape* s, const void* dy, const int8_t* yq, const uint8_t* ys,
+                              const float* gates, const int32_t* slot_row, void* dy_perm, float* dgates, void* st) {
+  MOE_TRY(check_shape(s));
+  MOE_TRY(check_rows(s, {dy, yq, ys, dy_perm}));
+  if (!rows_ok(s, gates) || !rows_ok(s, slot_row) || !rows_ok(s, dgates)) return MOE_ENULL;
+  return launched(
+      combine_rows_bwd_c8(elem_bytes(s), s->T, s->d, s->k, dy, yq, ys, gates, slot_row, dy_perm, dgates, S(st)));
 }
 
 // ---------------------------------------------------------------------------------------

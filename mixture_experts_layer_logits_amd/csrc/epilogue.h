@@ -29,6 +29,11 @@
 // over the 8 lanes of the block) with `valid` gating the stores:
 //   Epi::SwiGLU                p.epilogue_swiglu4_q(m, hcol, a[4], b[4], valid, quad)
 //   Epi::DSwiGLU               p.epilogue4_pre_q(e, m, n, v[4], pair, valid, quad)
+// A STORE16 problem with CK8 = true keeps a and b between the passes as MXINT8 blocks instead of
+// bf16: Epi::SwiGLU encodes the fp32 a and b (one rounding) and stores them with h through
+// p.store_swiglu_c8 and p.store_scales_c8; Epi::DSwiGLU loads the codes of every output position
+// (p.prefetch_c8), and stores [da | db] and h = silu(a) b again through p.store_dswiglu16 and
+// p.store_h16.
 // The SwiGLU gradient reads the saved a, b of every output position.  Those loads are issued
 // for a whole 32-row block of the wave before any of its stores: memory operations complete
 // in order on one counter, so a load issued after a store (or after the operand loads still
@@ -36,7 +41,9 @@
 #pragma once
 #include "common.h"
 #include "gemm.h"
+#include "lanes.h"
 #include "mxcode.h"
+#include "mxint8.h"
 #include "tilemap.h"
 
 namespace moe {
@@ -178,6 +185,46 @@ __device__ __forceinline__ void mx_block_store8(const uint4& pk, bool valid, uin
   }
 }
 
+// The value of lane ^ 4 (all lanes of a quad differ): the other quad of each 8 mirrored, then the quad.
+__device__ __forceinline__ float lane_xor4(float v) { return dpp_f<0x1B>(dpp_f<0x141>(v)); }
+
+// Scale byte of the MXINT8 block that the lane's 4 values belong to: 32 columns of one row, held by
+// the 8 lanes that share (lane & 3, lane >> 5).  Every lane must call it.
+__device__ __forceinline__ int ck8_row_byte(const float (&v)[4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; c++) m = ck8_max(m, v[c]);
+  m = ck8_max(m, lane_xor4(m));
+  m = ck8_max(m, other_half<8>(m));
+  return ck8_scale_byte(ck8_max(m, other_half<16>(m)));
+}
+
+// pair_row16 for one word of four 1-byte columns per row group: 8 consecutive columns of the lane's own
+__device__ __forceinline__ uint2 pair_row8(const uint32_t (&w)[2], bool odd) {
+  const uint32_t r = __float_as_uint(lane_xor4(__uint_as_float(odd ? w[0] : w[1])));
+  return odd ? make_uint2(r, w[1]) : make_uint2(w[0], r);
+}
+
+// Codes and scale bytes of four consecutive hidden columns of one row of an MXINT8 [a | b]
+struct Ck8Pair {
+  uint32_t a, b;
+  int sa, sb;
+};
+// da, db in the arithmetic of dswiglu4, h in that of the forward epilogue
+__device__ __forceinline__ void dswiglu_h4(const float (&dh)[4], const Ck8Pair& pr, float (&da)[4], float (&db)[4],
+                                           float (&h)[4]) {
+  float a[4], b[4];
+  ck8_values4(pr.a, ck8_scale(pr.sa), a);
+  ck8_values4(pr.b, ck8_scale(pr.sb), b);
+#pragma unroll
+  for (int c = 0; c < 4; c++) {
+    const float s = sigmoidf_(a[c]);
+    da[c] = dh[c] * b[c] * s * (1.f + a[c] * (1.f - s));
+    db[c] = dh[c] * a[c] * s;
+    h[c] = a[c] * s * b[c];
+  }
+}
+
 // Writes the tile of wave (wave_m, wave_n) whose accumulators are acc.
 template <class Prob, int WTM, int WTN>
 __device__ __forceinline__ void tile_epilogue(const Prob& p, const f32x16 (&acc)[WTM][WTN], const TileRange& tr,
@@ -185,7 +232,89 @@ __device__ __forceinline__ void tile_epilogue(const Prob& p, const f32x16 (&acc)
   const int sub = lane & 3, quad = (lane & 31) >> 2, half = lane >> 5;
 #pragma unroll
   for (int i = 0; i < WTM; i++) {
-    if constexpr (Prob::EPI == Epi::DSwiGLU) {
+    if constexpr (Prob::EPI == Epi::DSwiGLU && Prob::CK8) {
+      // as the bf16 form below, with the codes of the block loaded first
+      Ck8Pair pre[4][WTN];
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        int m = tr.m0 + (wave_m * WTM + i) * 32 + 8 * q + 4 * half + sub;
+        m = m < tr.m_end ? m : tr.m_end - 1;
+#pragma unroll
+        for (int j = 0; j < WTN; j++) {
+          int n = tr.n0 + (wave_n * WTN + j) * 32 + 4 * quad;
+          n = n < p.N ? n : p.N - 4;
+          pre[q][j] = p.prefetch_c8(m, n);
+        }
+      }
+      const bool odd = quad & 1;
+#pragma unroll
+      for (int pq = 0; pq < 2; pq++) {
+        const int m = tr.m0 + (wave_m * WTM + i) * 32 + 8 * (2 * pq + (odd ? 1 : 0)) + 4 * half + sub;
+#pragma unroll
+        for (int j = 0; j < WTN; j++) {
+          uint32_t wa[2][2], wb[2][2], wh[2][2];
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            float v[4], da[4], db[4], hv[4];
+#pragma unroll
+            for (int c = 0; c < 4; c++) v[c] = acc[i][j][4 * (2 * pq + h) + c];
+            quad_transpose(v, lane);
+            dswiglu_h4(v, pre[2 * pq + h][j], da, db, hv);
+            wa[h][0] = pack_bf16x2(da[0], da[1]);
+            wa[h][1] = pack_bf16x2(da[2], da[3]);
+            wb[h][0] = pack_bf16x2(db[0], db[1]);
+            wb[h][1] = pack_bf16x2(db[2], db[3]);
+            wh[h][0] = pack_bf16x2(hv[0], hv[1]);
+            wh[h][1] = pack_bf16x2(hv[2], hv[3]);
+          }
+          const uint4 ua = pair_row16(wa, odd), ub = pair_row16(wb, odd), uh = pair_row16(wh, odd);
+          const int n = tr.n0 + (wave_n * WTN + j) * 32 + 8 * (quad >> 1);
+          if (m < tr.m_end && n < p.N) {
+            p.store_dswiglu16(m, n, ua, ub);
+            p.store_h16(m, n, uh);
+          }
+        }
+      }
+    } else if constexpr (Prob::EPI == Epi::SwiGLU && Prob::CK8) {
+      // a and b of the lane's own 4 columns and h from them in fp32; a and b leave as MXINT8 codes,
+      // completed to 8 columns of one row by the quad-pair exchange (8-byte stores), h as bf16
+      const bool odd = quad & 1;
+#pragma unroll
+      for (int pq = 0; pq < 2; pq++) {
+        const int m = tr.m0 + (wave_m * WTM + i) * 32 + 8 * (2 * pq + (odd ? 1 : 0)) + 4 * half + sub;
+#pragma unroll
+        for (int j = 0; j < WTN; j += 2) {
+          uint32_t wa[2], wb[2], wh[2][2];
+          int sa[2], sb[2];
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            float a[4], b[4], hv[4];
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+              a[c] = acc[i][j][4 * (2 * pq + h) + c];
+              b[c] = acc[i][j + 1][4 * (2 * pq + h) + c];
+            }
+            quad_transpose(a, lane);
+            quad_transpose(b, lane);
+            p.swiglu4(a, b, hv);
+            sa[h] = ck8_row_byte(a);
+            sb[h] = ck8_row_byte(b);
+            wa[h] = ck8_codes4(a[0], a[1], a[2], a[3], ck8_inv_scale(sa[h]));
+            wb[h] = ck8_codes4(b[0], b[1], b[2], b[3], ck8_inv_scale(sb[h]));
+            wh[h][0] = pack_bf16x2(hv[0], hv[1]);
+            wh[h][1] = pack_bf16x2(hv[2], hv[3]);
+          }
+          const uint2 ua = pair_row8(wa, odd), ub = pair_row8(wb, odd);
+          const uint4 uh = pair_row16(wh, odd);
+          const int hcol = tr.n0 / 2 + ((wave_n * WTN + j) >> 1) * 32 + 8 * (quad >> 1);
+          if (m < tr.m_end && hcol < p.N / 2) {
+            p.store_swiglu_c8(m, hcol, ua, ub, uh);
+            // the scale bytes are the block's in all its lanes: quads 0 and 1 store one row group's each
+            if (quad < 2) p.store_scales_c8(m, hcol, odd ? sa[1] : sa[0], odd ? sb[1] : sb[0]);
+          }
+        }
+      }
+    } else if constexpr (Prob::EPI == Epi::DSwiGLU) {
       // every saved (a, b) of the block first (rows and columns clamped into the tile, so no
       // load is out of range or under a branch), then the gradients and their stores
       AbPair pre[4][WTN];

@@ -851,6 +851,7 @@ mx_gemm_kernel(const Prob p) {
 // ---------------------------------------------------------------------------------------
 struct MxBase {
   static constexpr bool MXQ = false;  // no MXFP8 copy of the output
+  static constexpr bool CK8 = false;  // a, b kept as bf16
   static constexpr bool N_MAJOR = true;  // Group::M tile order within an expert
   static constexpr bool STORE16 = false;  // bf16 output rows through out_row (Epi::Store)
   int M = 0, N = 0, K = 0, E = 1;

@@ -58,6 +58,18 @@ extra GEMM1 per step for R * 3f activation elements held between the passes, the
 memory / throughput trade the pages report for recomputing activations (unite.ai,
 section "Παραλληλισμός, Ακρίβεια και Τεχνικές Μνήμης").
 
+8-bit checkpoints (``ckpt8=True``): what the backward needs of the expert FFN is kept in 8 bits.
+[a | b] leaves GEMM1's epilogue as MXINT8 (moe_ffn_gemm1_fwd_c8) and the dgrad2 epilogue reads it
+and writes h again for wgrad2 (moe_ffn_dgrad2_c8); the combine keeps the routed outputs as MXINT8
+(moe_combine_c8) and its backward reads them (moe_combine_bwd_c8); x_perm is gathered again from
+the layer's input before wgrad1.  Next to ``recompute`` this holds less and runs no GEMM twice, at
+the price of the checkpoint's 8 bits in the gradients (the forward is the same, bit for bit).  Where
+GEMM1 or dgrad2 does not run bf16 the rows go through moe_ckpt8_pack and moe_ckpt8_unpack instead.
+
+4-bit weights (``weights4=True``, serving: no backward): W1, W3, W2 are given as the (codes, scales)
+pairs that ``quantize_weights`` makes, and the expert products are moe_ffn_gemm1_fwd_w4 and
+moe_ffn_gemm2_fwd_w4 on the unquantised rows.
+
 Router losses (``balance=(w_balance, w_z)``, learned routing): the forward also runs
 moe_balance_fwd, which leaves the balance loss and the z-loss in ``loss``, the kept tokens'
 per-expert counts in ``bal_counts`` and the mean probabilities in ``prob_mean``; ``mask`` (bool or
@@ -80,27 +92,51 @@ from . import (MOE_BF16, MOE_F32, MOE_MX_DGRAD1, MOE_MX_DGRAD2, MOE_MX_GEMM1, MO
                moe_ffn_gemm2_fwd, moe_ffn_wgrad1, moe_ffn_wgrad1_mx, moe_ffn_wgrad2, moe_ffn_wgrad2_mx, moe_mx_cols_ld,
                moe_permute, moe_permute_bwd, moe_permute_bwd_router, moe_permute_mx, moe_route, moe_route_bwd,
                moe_route_given, moe_router_bwd, moe_balance_bwd, moe_balance_fwd, moe_block_norm_bwd,
-               moe_block_norm_fwd, moe_combine_norm, moe_combine_norm_bwd,
-               moe_router_fwd, moe_workspace_size, mx_scope_bits)
+               moe_block_norm_fwd, moe_combine_norm, moe_combine_norm_bwd, moe_ckpt8_pack, moe_ckpt8_unpack,
+               moe_combine_bwd_c8, moe_combine_c8, moe_ffn_dgrad2_c8, moe_ffn_gemm1_fwd_c8, moe_ffn_gemm1_fwd_w4,
+               moe_ffn_gemm2_fwd_w4, moe_mx4_quantize, moe_router_fwd, moe_workspace_size, mx_scope_bits)
 
 # the GEMMs that read the dispatched rows: all four must run MXFP8 for the MXFP8 dispatch
 _DISPATCH_READERS = MOE_MX_GEMM1 | MOE_MX_WGRAD1 | MOE_MX_DGRAD2 | MOE_MX_WGRAD2
 
 
+def quantize_weights(*weights):
+    """The MXFP4 form of expert weights [.., n, K] (float32 or bfloat16, contiguous, on the GPU): for each a
+    pair (codes uint8 [.., n, K/2], scales uint8 [.., n, K/32]), as a layer with ``weights4`` takes them."""
+    out = []
+    for w in weights:
+        rows, K = w.numel() // w.shape[-1], w.shape[-1]
+        q = torch.empty(*w.shape[:-1], K // 2, dtype=torch.uint8, device=w.device)
+        s = torch.empty(*w.shape[:-1], K // 32, dtype=torch.uint8, device=w.device)
+        moe_mx4_quantize(rows, K, w, q, s)
+        out.append((q, s))
+    return tuple(out)
+
+
 class MoEExpertLayer:
     def __init__(self, T, d, f, E, k, act=MOE_BF16, gemm=None, device="cuda", recompute=False, shared_f=0,
-                 mx_dispatch=None, mx_scope=0, mx_fused_quant=True, router_dx_fused=True, balance=None):
+                 mx_dispatch=None, mx_scope=0, mx_fused_quant=True, router_dx_fused=True, balance=None, ckpt8=False,
+                 weights4=False):
         self.shape = make_shape(T, d, f, E, k, act, gemm, mx_scope)
-        self.recompute = recompute
+        self.recompute, self.ckpt8, self.weights4 = recompute, bool(ckpt8), bool(weights4)
+        if self.ckpt8 and recompute:
+            raise ValueError("a layer recomputes its activations or keeps them in 8 bits, not both")
+        if self.weights4 and (recompute or ckpt8 or balance is not None or self.shape.gemm == MOE_MXFP8):
+            raise ValueError("a layer with 4-bit weights has no backward (no recompute, ckpt8 or router losses), and "
+                             "its products are not MXFP8")
         # the router's input gradient folded into the un-permute (k rows of Wr per token)
         # instead of a dense dlogits Wr GEMM written to dx_r and read back
         # (the router losses' gradient is not zero outside the k chosen experts)
         self.router_dx_fused = bool(router_dx_fused) and balance is None
         self.balance = balance
         bits = mx_scope_bits(self.shape)
-        # MXFP8 operands written by the producing bf16 GEMM's epilogue
-        self.fq_h = bool(mx_fused_quant) and bool(bits & MOE_MX_GEMM2) and not bits & MOE_MX_GEMM1
-        self.fq_dab = bool(mx_fused_quant) and bool(bits & MOE_MX_DGRAD1) and not bits & MOE_MX_DGRAD2
+        # MXFP8 operands written by the producing bf16 GEMM's epilogue (which writes the checkpoint instead)
+        fq = bool(mx_fused_quant) and not self.ckpt8
+        self.fq_h = fq and bool(bits & MOE_MX_GEMM2) and not bits & MOE_MX_GEMM1
+        self.fq_dab = fq and bool(bits & MOE_MX_DGRAD1) and not bits & MOE_MX_DGRAD2
+        # the checkpoint written and read by the GEMMs' own epilogues
+        self.c8_fwd = self.ckpt8 and act == MOE_BF16 and not bits & MOE_MX_GEMM1
+        self.c8_bwd = self.ckpt8 and act == MOE_BF16 and not bits & MOE_MX_DGRAD2
         covers = (bits & _DISPATCH_READERS) == _DISPATCH_READERS
         self.mx_dispatch = covers if mx_dispatch is None else bool(mx_dispatch)
         if self.mx_dispatch and not covers:
@@ -134,17 +170,34 @@ class MoEExpertLayer:
             self.dyq_rows, self.dys_rows = e(R, d, dtype=u8), e(R, d // 32, dtype=u8)
             self.dyq_cols, self.dys_cols = e(d, L, dtype=u8), e(d, L // 32, dtype=u8)
         else:
-            self.x_perm = e(R, d)
-            self.dy_perm = e(R, d)
-        self.ab = None if recompute else e(R, 2 * f)
-        self.h = None if recompute else e(R, f)
+            self.x_perm = None if self.ckpt8 else e(R, d)
+            self.dy_perm = None if self.weights4 else e(R, d)
+        held = not (recompute or self.ckpt8)
+        self.ab = e(R, 2 * f) if held and not self.weights4 else None
+        self.h = e(R, f) if held else None
+        if self.ckpt8:
+            i8 = torch.int8
+            self.ab_bits = e(R, 2 * f, dtype=i8), e(R, 2 * f // 32, dtype=u8)  # codes and scales
+            self.y_bits = e(R, d, dtype=i8), e(R, d // 32, dtype=u8)
         self.hq_rows = self.hs_rows = self.dabq_rows = self.dabs_rows = None
         if self.fq_h:
             self.hq_rows, self.hs_rows = e(R, f, dtype=u8), e(R, f // 32, dtype=u8)
         if self.fq_dab:
             self.dabq_rows, self.dabs_rows = e(R, 2 * f, dtype=u8), e(R, 2 * f // 32, dtype=u8)
-        self.y_perm = e(R, d)
+        self.y_perm = None if self.ckpt8 else e(R, d)
         self.y = e(T, d)
+        self.ws = torch.empty(moe_workspace_size(self.shape), dtype=torch.uint8, device=dev)
+        self.learned = True
+        self._params = None
+        self._shared = None
+        if shared_f:
+            fs = shared_f
+            self.shape_s = make_shape(T, d, fs, 1, 1, act, gemm, mx_scope)
+            self.offsets_s = torch.tensor([0, T], dtype=i32, device=dev)
+            self.h_s, self.y_s = None if self.ckpt8 else e(T, fs), e(T, d)
+        if self.weights4:
+            self.dx = None
+            return
         # backward buffers
         self.dgates = e(T, k, dtype=f32)
         self.dab = e(R, 2 * f)
@@ -161,15 +214,9 @@ class MoEExpertLayer:
             self.lse, self.prob_mean, self.loss = e(T, dtype=f32), e(E, dtype=f32), e(2, dtype=f32)
             self.bal_counts = e(E + 1, dtype=i32)
         self.dx = e(T, d)
-        self.ws = torch.empty(moe_workspace_size(self.shape), dtype=torch.uint8, device=dev)
-        self.learned = True
-        self._params = None
-        self._shared = None
         if shared_f:
-            fs = shared_f
-            self.shape_s = make_shape(T, d, fs, 1, 1, act, gemm, mx_scope)
-            self.offsets_s = torch.tensor([0, T], dtype=i32, device=dev)
-            self.ab_s, self.h_s, self.y_s = e(T, 2 * fs), e(T, fs), e(T, d)
+            self.ab_s = None if self.ckpt8 else e(T, 2 * fs)
+            self.ab_bits_s = (e(T, 2 * fs, dtype=i8), e(T, 2 * fs // 32, dtype=u8)) if self.ckpt8 else None
             self.dab_s, self.dx_s = e(T, 2 * fs), e(T, d)
             if self.fq_h:
                 self.hq_s, self.hs_s = e(T, fs, dtype=u8), e(T, fs // 32, dtype=u8)
@@ -182,6 +229,13 @@ class MoEExpertLayer:
     def _check_losses(self, topk_idx, mask):
         if (self.balance is not None and topk_idx is not None) or (self.balance is None and mask is not None):
             raise ValueError("the router losses need learned routing, and a mask needs the router losses")
+
+    def _check_inputs(self, x, weights):
+        if any(isinstance(w, (tuple, list)) != self.weights4 for w in weights):
+            raise ValueError("a layer with weights4 takes every weight as a (codes, scales) pair, another none")
+        if self.ckpt8 and _shares(x, self.y, self.dx):
+            raise ValueError("a layer with ckpt8 reads its input again in the backward: it cannot lie in the layer's "
+                             "y or dx")
 
     def route(self, x=None, Wr=None, bias=None, topk_idx=None, mask=None):
         s = self.shape
@@ -199,15 +253,26 @@ class MoEExpertLayer:
 
     def forward(self, x, W1, W3, W2, Wr=None, bias=None, topk_idx=None, gates=None, shared=None, mask=None):
         """shared: (W1s [1, fs, d], W3s [1, fs, d], W2s [1, d, fs]) of the shared expert.
-        mask: bool or uint8 [T], 0 for a token the router losses leave out."""
+        mask: bool or uint8 [T], 0 for a token the router losses leave out.
+        With weights4 every weight is a (codes, scales) pair.  x and the weights have to stay as they are
+        until the backward."""
         y_add = self._experts_forward(x, W1, W3, W2, Wr, bias, topk_idx, gates, shared, mask)
-        moe_combine(self.shape, self.y_perm, self._params[-1], self.slot_row, y_add, self.y)
+        return self._combine(y_add)
+
+    def _combine(self, y_add):
+        s, g = self.shape, self._params[-1]
+        if self.ckpt8:  # y_perm itself is not kept for the backward
+            moe_combine_c8(s, self.y_perm, g, self.slot_row, y_add, self.y, *self.y_bits)
+            self.y_perm = None
+        else:
+            moe_combine(s, self.y_perm, g, self.slot_row, y_add, self.y)
         return self.y
 
     def _experts_forward(self, x, W1, W3, W2, Wr, bias, topk_idx, gates, shared, mask):
         """The forward up to the routed rows y_perm; returns the shared expert's output or None."""
         s = self.shape
         self._check_losses(topk_idx, mask)
+        self._check_inputs(x, (W1, W3, W2, *(shared or ())))
         self.steps += 1
         self.route(x, Wr, bias, topk_idx, mask)
         g = self.gates if topk_idx is None else gates
@@ -217,18 +282,38 @@ class MoEExpertLayer:
         if shared is not None:
             W1s, W3s, W2s = shared
             ss = self.shape_s
-            if self.fq_h:
+            if self.weights4:
+                self._ffn_w4(ss, x, *shared, self.offsets_s, self.h_s, self.y_s)
+            elif self.ckpt8:
+                h = self._e(self.T, self.shared_f)
+                self._gemm1_c8(ss, x, W1s, W3s, self.offsets_s, h, self.ab_bits_s, self.ws_s)
+                moe_ffn_gemm2_fwd(ss, h, W2s, self.offsets_s, self.y_s, self.ws_s)
+            elif self.fq_h:
                 moe_ffn_gemm1_fwd_q(ss, x, W1s, W3s, self.offsets_s, self.ab_s, self.h_s, self.hq_s, self.hs_s)
                 moe_ffn_gemm2_fwd_mx(ss, self.hq_s, self.hs_s, W2s, self.offsets_s, self.y_s, self.ws_s)
             else:
                 moe_ffn_gemm1_fwd(ss, x, W1s, W3s, self.offsets_s, self.ab_s, self.h_s, self.ws_s)
                 moe_ffn_gemm2_fwd(ss, self.h_s, W2s, self.offsets_s, self.y_s, self.ws_s)
             y_add = self.y_s
+        if self.ckpt8:
+            self.y_perm = self._e(self.R, self.d)
         if self.mx_dispatch:
             moe_permute_mx(s, x, self.slot_row, self.offsets, self.row_src, self.xq_rows, self.xs_rows, self.xq_cols,
                            self.xs_cols)
         else:
+            if self.ckpt8:
+                self.x_perm = self._e(self.R, self.d)
             moe_permute(s, x, self.slot_row, self.row_src, self.x_perm)
+        if self.weights4:
+            self._ffn_w4(s, self.x_perm, W1, W3, W2, self.offsets, self.h, self.y_perm)
+            return y_add
+        if self.ckpt8:
+            self.h = self._e(self.R, self.f)
+            self._gemm1_c8(s, self.x_perm, W1, W3, self.offsets, self.h, self.ab_bits, self.ws)
+            self.x_perm = None  # gathered again where the backward needs it
+            moe_ffn_gemm2_fwd(s, self.h, W2, self.offsets, self.y_perm, self.ws)
+            self.h = None
+            return y_add
         if self.recompute:
             self.ab, self.h = self._e(self.R, 2 * self.f), self._e(self.R, self.f)
         self._gemm1(W1, W3, with_q=True)
@@ -240,17 +325,66 @@ class MoEExpertLayer:
             self.ab = self.h = None
         return y_add
 
+    @staticmethod
+    def _ffn_w4(s, x, W1, W3, W2, offsets, h, y):
+        moe_ffn_gemm1_fwd_w4(s, x, *W1, *W3, offsets, h)
+        moe_ffn_gemm2_fwd_w4(s, h, *W2, offsets, y)
+
+    def _gemm1_c8(self, s, x, W1, W3, offsets, h, bits, ws):
+        """GEMM1 with [a | b] left in `bits` (codes, scales) instead of bf16 or fp32 rows."""
+        if self.c8_fwd:
+            moe_ffn_gemm1_fwd_c8(s, x, W1, W3, offsets, h, *bits)
+            return
+        n = s.T * s.k
+        ab = self._e(n, 2 * s.f)
+        if self.mx_dispatch and s is self.shape:
+            moe_ffn_gemm1_fwd_mx(s, self.xq_rows, self.xs_rows, W1, W3, offsets, ab, h, ws)
+        else:
+            moe_ffn_gemm1_fwd(s, x, W1, W3, offsets, ab, h, ws)
+        moe_ckpt8_pack(n, 2 * s.f, ab, *bits)
+
+    def _dgrad2_c8(self, s, dy, W2, offsets, bits, dab, ws):
+        """[da | db] from the 8-bit [a | b]; returns h of the same a and b."""
+        n = s.T * s.k
+        h = self._e(n, s.f)
+        if self.c8_bwd:
+            moe_ffn_dgrad2_c8(s, dy, W2, *bits, offsets, dab, h)
+            return h
+        ab = self._e(n, 2 * s.f)
+        moe_ckpt8_unpack(n, 2 * s.f, *bits, ab, h)
+        if self.mx_dispatch and s is self.shape:
+            moe_ffn_dgrad2_mx(s, self.dyq_rows, self.dys_rows, W2, ab, offsets, dab, ws)
+        else:
+            moe_ffn_dgrad2(s, dy, W2, ab, offsets, dab, ws)
+        return h
+
+    def _check_backward(self):
+        if self.weights4:
+            raise RuntimeError("a layer with 4-bit weights has no backward")
+
     # -------------------------------------------------------------- backward
     def backward(self, dy, dloss=None):
         """dloss: float32 [2] on the GPU, the weights of the router losses in place of the layer's."""
-        s, g = self.shape, self._params[-1]
-        if self.mx_dispatch:
-            moe_combine_bwd_mx(s, dy, self.y_perm, g, self.slot_row, self.row_src, self.offsets, self.dgates,
-                               self.dyq_rows, self.dys_rows, self.dyq_cols, self.dys_cols)
-        else:
-            moe_combine_bwd(s, dy, self.y_perm, g, self.slot_row, self.dy_perm, self.dgates)
+        self._check_backward()
+        self._combine_bwd(dy)
         self._input_grads(dy, dloss)
         return self._finish_backward()
+
+    def _combine_bwd(self, dy):
+        s, g = self.shape, self._params[-1]
+        if self.ckpt8 and self.mx_dispatch:
+            y_perm = self._e(self.R, self.d)
+            moe_ckpt8_unpack(self.R, self.d, *self.y_bits, y_perm)
+        elif self.ckpt8:
+            moe_combine_bwd_c8(s, dy, *self.y_bits, g, self.slot_row, self.dy_perm, self.dgates)
+            return
+        else:
+            y_perm = self.y_perm
+        if self.mx_dispatch:
+            moe_combine_bwd_mx(s, dy, y_perm, g, self.slot_row, self.row_src, self.offsets, self.dgates, self.dyq_rows,
+                               self.dys_rows, self.dyq_cols, self.dys_cols)
+        else:
+            moe_combine_bwd(s, dy, y_perm, g, self.slot_row, self.dy_perm, self.dgates)
 
     def _input_grads(self, dy, dloss=None):
         """The backward behind the combine's, up to dx: dy_perm and dgates are in place, dy is read
@@ -260,7 +394,15 @@ class MoEExpertLayer:
         if self.recompute:  # regenerate a, b and h from the kept routed rows
             self.ab, self.h = self._e(self.R, 2 * self.f), self._e(self.R, self.f)
             self._gemm1(W1, W3)
-        if self.mx_dispatch:
+        if self.ckpt8:
+            h = self._dgrad2_c8(s, self.dy_perm, W2, self.offsets, self.ab_bits, self.dab, self.ws)
+            if self.mx_dispatch:
+                moe_ffn_wgrad2_mx(s, h, self.dyq_cols, self.dys_cols, self.offsets, self.dW2, self.ws)
+            else:
+                moe_ffn_wgrad2(s, h, self.dy_perm, self.offsets, self.dW2, self.ws)
+            del h
+            moe_ffn_dgrad1(s, self.dab, W1, W3, self.offsets, self.dx_perm, self.ws)
+        elif self.mx_dispatch:
             moe_ffn_dgrad2_mx(s, self.dyq_rows, self.dys_rows, W2, self.ab, self.offsets, self.dab, self.ws)
             moe_ffn_wgrad2_mx(s, self.h, self.dyq_cols, self.dys_cols, self.offsets, self.dW2, self.ws)
             moe_ffn_dgrad1(s, self.dab, W1, W3, self.offsets, self.dx_perm, self.ws)
@@ -288,11 +430,15 @@ class MoEExpertLayer:
         if self._shared is not None:
             W1s, W3s, W2s = self._shared
             ss, off = self.shape_s, self.offsets_s
-            if self.fq_dab:
+            h_s = self.h_s
+            if self.ckpt8:
+                h_s = self._dgrad2_c8(ss, dy, W2s, off, self.ab_bits_s, self.dab_s, self.ws_s)
+            elif self.fq_dab:
                 moe_ffn_dgrad2_q(ss, dy, W2s, self.ab_s, off, self.dab_s, self.dabq_s, self.dabs_s)
             else:
                 moe_ffn_dgrad2(ss, dy, W2s, self.ab_s, off, self.dab_s, self.ws_s)
-            moe_ffn_wgrad2(ss, self.h_s, dy, off, self.dW2s, self.ws_s)
+            moe_ffn_wgrad2(ss, h_s, dy, off, self.dW2s, self.ws_s)
+            del h_s
             if self.fq_dab:
                 moe_ffn_dgrad1_mx(ss, self.dabq_s, self.dabs_s, W1s, W3s, off, self.dx_s, self.ws_s)
             else:
@@ -312,6 +458,10 @@ class MoEExpertLayer:
         s = self.shape
         if self.mx_dispatch:
             moe_ffn_wgrad1_mx(s, self.xq_cols, self.xs_cols, self.dab, self.offsets, self.dW1, self.dW3, self.ws)
+        elif self.ckpt8:
+            x_perm = self._e(self.R, self.d)
+            moe_permute(s, self._params[0], self.slot_row, None, x_perm)
+            moe_ffn_wgrad1(s, x_perm, self.dab, self.offsets, self.dW1, self.dW3, self.ws)
         else:
             moe_ffn_wgrad1(s, self.x_perm, self.dab, self.offsets, self.dW1, self.dW3, self.ws)
         if self.recompute:
@@ -331,8 +481,15 @@ class MoEExpertLayer:
     def activation_bytes(self):
         """Bytes of expert-FFN activations held from the forward to the backward: the
         routed rows (x_perm, or with the MXFP8 dispatch their two E4M3 layouts with
-        scales), y_perm, and ab and h unless they are recomputed."""
-        eb = self.y_perm.element_size()
+        scales), y_perm, and ab and h unless they are recomputed.  With ckpt8 the 8-bit ab and
+        y_perm in their place (and no bf16 routed rows)."""
+        if self.weights4:
+            return 0
+        eb = self.y.element_size()
+        if self.ckpt8:
+            n = sum(t.numel() for t in (*self.ab_bits, *self.y_bits))
+            return n + (sum(t.numel() for t in (self.xq_rows, self.xs_rows, self.xq_cols, self.xs_cols))
+                        if self.mx_dispatch else 0)
         n = self.R * self.d * eb
         if self.mx_dispatch:
             n += sum(t.numel() for t in (self.xq_rows, self.xs_rows, self.xq_cols, self.xs_cols))
@@ -344,9 +501,9 @@ class MoEExpertLayer:
 
 
 def _shares(t, *others):
-    """Does t lie in the memory of one of `others`?"""
+    """Does t lie in the memory of one of `others` (None: a buffer that is not there)?"""
     at = t.untyped_storage().data_ptr()
-    return t.numel() > 0 and any(at == o.untyped_storage().data_ptr() for o in others)
+    return t.numel() > 0 and any(o is not None and at == o.untyped_storage().data_ptr() for o in others)
 
 
 class MoEBlock:
@@ -361,13 +518,16 @@ class MoEBlock:
               -> moe_block_norm_bwd (unless xn was given) -> wgrad1
 
     y is never stored: the combine's norm takes it from registers and the backward gathers it
-    again.  A layer with the MXFP8 dispatch writes its routed gradient rows in E4M3 from dy, so
-    there the combine and the norm are separate calls.  The block owns its buffers and holds one
+    again.  A layer with the MXFP8 dispatch writes its routed gradient rows in E4M3 from dy, and one
+    with 8-bit checkpoints keeps its routed outputs in the combine, so there the combine and the norm
+    are separate calls and y is stored.  Over a layer with 4-bit weights the block serves: it has no
+    backward.  The block owns its buffers and holds one
     forward at a time, like its layer, and its calls run on the current stream."""
 
     def __init__(self, layer: MoEExpertLayer, res_scale=1.0, eps=1e-6):
         self.layer, self.res_scale, self.eps = layer, float(res_scale), float(eps)
         self._saved = None
+        self._stores_y = layer.mx_dispatch or layer.ckpt8
         e, T, d, f32 = layer._e, layer.T, layer.d, torch.float32
         self.xn, self.v, self.xn_next = e(T, d), e(T, d), e(T, d)
         self.rstd_pre, self.rstd_post, self.rstd_next = e(T, dtype=f32), e(T, dtype=f32), e(T, dtype=f32)
@@ -384,11 +544,12 @@ class MoEBlock:
             raise ValueError("a block takes w_pre, or the xn of the block before")
         L, s = self.layer, self.layer.shape
         # written before h or xn is read for the last time: by the norm, the combine, or the backward
-        work = (self.v, self.xn_next, self.dv, self.dy, L.dx, *((L.y,) if L.mx_dispatch else ()))
+        work = (self.v, self.xn_next, self.dv, self.dy, L.dx, *((L.y,) if self._stores_y else ()))
         if _shares(h, *work, *((self.xn,) if xn is None else ())) or (xn is not None and _shares(xn, *work)):
             raise ValueError("a block cannot read its own output or working buffers: this forward or its backward "
                              "overwrites them")
         L._check_losses(topk_idx, mask)
+        L._check_inputs(self.xn if xn is None else xn, (W1, W3, W2, *(shared or ())))
         if xn is None:
             xn = self.xn
             moe_block_norm_fwd(s, h, None, None, None, w_pre, 1.0, self.eps, None, xn, None, self.rstd_pre)
@@ -398,9 +559,8 @@ class MoEBlock:
         g = L._params[-1]
         out = (gate, w_post, w_next, self.res_scale, self.eps, self.v, None if w_next is None else self.xn_next,
                None if w_post is None else self.rstd_post, None if w_next is None else self.rstd_next)
-        if L.mx_dispatch:
-            moe_combine(s, L.y_perm, g, L.slot_row, y_add, L.y)
-            moe_block_norm_fwd(s, h, L.y, *out)
+        if self._stores_y:
+            moe_block_norm_fwd(s, h, L._combine(y_add), *out)
         else:
             moe_combine_norm(s, L.y_perm, g, L.slot_row, y_add, h, *out)
         self._saved = (h, gate, w_pre, w_post, w_next, y_add)
@@ -410,6 +570,7 @@ class MoEBlock:
         """dv [T, d] (None: v was used through xn_next only), dxn_next [T, d] with w_next, dloss as
         MoEExpertLayer.backward.  Returns dh; with a given xn, (dh, dxn) for the block before.
         dw_pre, dw_post, dw_next, dgate and the layer's gradients are left in their buffers."""
+        self.layer._check_backward()
         if self._saved is None:
             raise RuntimeError("the block has no forward to go back through (none ran, or the last one was refused)")
         L, s = self.layer, self.layer.shape
@@ -419,10 +580,9 @@ class MoEBlock:
         tail = (None if gate is None else self.dgate, None if w_post is None else self.dw_post,
                 None if w_next is None else self.dw_next, L.ws)
         g = L._params[-1]
-        if L.mx_dispatch:
+        if self._stores_y:
             moe_block_norm_bwd(s, dv, dxn_next, self.v, L.y, *mid, self.dy, *tail)
-            moe_combine_bwd_mx(s, self.dy, L.y_perm, g, L.slot_row, L.row_src, L.offsets, L.dgates, L.dyq_rows,
-                               L.dys_rows, L.dyq_cols, L.dys_cols)
+            L._combine_bwd(self.dy)
         else:
             moe_combine_norm_bwd(s, dv, dxn_next, self.v, L.y_perm, g, L.slot_row, y_add, *mid,
                                  None if y_add is None else self.dy, L.dy_perm, L.dgates, *tail)
@@ -461,6 +621,7 @@ class MoEExpertFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, Wr, W1, W3, W2, layer: MoEExpertLayer, bias=None):
+        layer._check_backward()
         x, Wr, W1, W3, W2 = (t.contiguous() for t in (x, Wr, W1, W3, W2))
         y = layer.forward(x, W1, W3, W2, Wr=Wr, bias=None if bias is None else bias.contiguous())
         ctx.save_for_backward(x, Wr, W1, W3, W2)
