@@ -9,13 +9,6 @@
 // two elements an instruction) and the bf16 matrix cores multiply them with the unquantised rows,
 // summing in fp32: the only roundings are the sums' and the one of each output.  fp32 rows take the
 // fp32 matrix cores in the same way.
-//
-// A tile is 16 weight rows by up to 16 NT routed rows of one expert.  The weights are the matrix
-// product's left operand: lane l holds weight row l % 16 and 64 consecutive elements (two blocks, two
-// 16-byte loads) of every 256, the block 64 (l / 16) of them; the right operand's lane holds the same
-// elements of routed row l % 16.  Which element of the reduction a lane's register stands for is the
-// same on both sides, so the order inside a matrix instruction does not matter.  The waves of a
-// workgroup share the reduction, 256 elements in turn, and add their sums through LDS in wave order.
 #include "lanes.h"
 #include "tilemap.h"
 #include "w4.h"
@@ -71,24 +64,6 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(int64_t nblk, const T
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kChunk = 256;  // elements of the reduction a wave takes at a time
-constexpr int kRowsW = 16;   // weight rows of a tile
-
-// 2^s of a scale byte (NaN for 255)
-__device__ __forceinline__ float mx4_scale(int byte) {
-  return byte == 255 ? __uint_as_float(0x7fc00000u) : __builtin_ldexpf(1.f, byte - 127);
-}
-
-// Eight codes as bf16
-__device__ __forceinline__ bf16x8 widen_bf16(uint32_t c, float scale) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2);
-  const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3);
-  return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
-}
-
 struct W4Args {
   int R, K, N, E;           // rows, reduction, weight rows of an expert, experts
   const int* offsets;
@@ -98,127 +73,462 @@ struct W4Args {
   void* out;                // [R][N]
 };
 
-// A lane's 64 elements (two blocks) of one weight row, and of NT routed rows, times each other
-template <typename T, int NT>
-__device__ __forceinline__ void multiply(const uint4 (&q)[2], const float (&sc)[2], const T* const (&x)[NT],
-                                         const bool (&have)[NT], int k, f32x4 (&acc)[NT]) {
+// A scale byte as the widening instructions take it: they read the exponent field alone, 0 as 2^-127
+// and 255 as NaN.
+__device__ __forceinline__ float mx4_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Eight codes as bf16 or float
+__device__ __forceinline__ bf16x8 widen_bf16(uint32_t c, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2);
+  const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3);
+  return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+}
+__device__ __forceinline__ void widen_f32(uint32_t c, float scale, float (&v)[8]) {
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 0);
+  const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1);
+  const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 2);
+  const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 3);
+  v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = d[0], v[5] = d[1], v[6] = e[0], v[7] = e[1];
+}
+
+// Sums over the lanes up to and including each
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast31 into rows 2 and 3
+  return v;
+}
+
+// The tiles of a launch: an expert's rows in runs of at most ROWS (even shares of whole 16s where EVEN),
+// its weight rows in ntn tiles; the runs that share a weight tile follow one another.  Every wave finds
+// its tiles by itself, so no barrier stands before the first load: a lane holds one expert of a window
+// of 64, whose run counts are scanned in registers, and as tiles are asked for in ascending order the
+// window only moves forward.
+struct W4Tile {
+  int e, m0, m_end, nt;  // e < 0: past the last tile
+};
+template <int ROWS, bool EVEN>
+struct W4Finder {
+  const int* offsets;
+  int E, ntn, lane, e0, lo, hi, runs, incl;
+  __device__ __forceinline__ void window(int before) {
+    const int e = e0 + lane;
+    lo = e < E ? offsets[e] : 0;
+    hi = e < E ? offsets[e + 1] : 0;
+    runs = (hi - lo + ROWS - 1) / ROWS;
+    incl = before + wave_scan(runs);
+  }
+  __device__ __forceinline__ W4Finder(const int* off, int E_, int ntn_, int lane_)
+      : offsets(off), E(E_), ntn(ntn_), lane(lane_), e0(0) {
+    window(0);
+  }
+  __device__ __forceinline__ W4Tile find(int t) {
+    while (true) {
+      const uint64_t hit = __ballot(t >= (incl - runs) * ntn && t < incl * ntn);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        const int me = __builtin_amdgcn_readlane(runs, l), end = __builtin_amdgcn_readlane(hi, l);
+        const int start = __builtin_amdgcn_readlane(lo, l);
+        const int local = t - (__builtin_amdgcn_readlane(incl, l) - me) * ntn;
+        const int nt = me == 1 ? local : local / me;
+        const int per = EVEN && me > 1 ? ((end - start + 15) / 16 + me - 1) / me * 16 : ROWS;
+        const int m0 = start + (local - nt * me) * per;
+        return W4Tile{e0 + l, m0, m0 + per < end ? m0 + per : end, nt};
+      }
+      e0 += kWave;
+      if (e0 >= E) return W4Tile{-1, 0, 0, 0};
+      window(__builtin_amdgcn_readlane(incl, kWave - 1));
+    }
+  }
+};
+
+// ---- few rows: the weights stream through registers
+// A tile is 16 weight rows by up to 16 routed rows of one expert.  The weights are the matrix product's
+// left operand, the routed rows its right: lane l holds elements of weight row l % 16 and of routed row
+// l % 16, the same ones of the reduction, and which they are is free.  bf16: NB blocks of 32 at 128
+// apart, block l / 16 of each 128, so that the four lanes of a row read 64 bytes of codes side by side;
+// fp32: 16 of each 64.  The 8 waves of a workgroup are `tiles` neighbouring tiles by 8 / tiles shares of
+// the reduction, taken piece by piece; the shares' sums are added through LDS in order.  Each wave loads
+// the codes of its next piece, of this tile or the next, before it multiplies the one it has.
+constexpr int kStreamWaves = 8;
+constexpr int kStreamMaxRows = 12;  // rows an expert, on average
+constexpr int kRowsW = 16;          // rows and weight rows of a tile
+
+// NB: blocks of a lane's piece; 0: half a block (fp32 rows).  TAIL: the last piece may end inside.
+template <typename T, int P, int NB, bool TAIL>
+struct Stream {
+  static constexpr int B = NB ? NB : 1;            // blocks touched
+  static constexpr int Q = NB ? 4 * NB : 2;        // code words
+  static constexpr int SPAN = NB ? 128 * NB : 64;  // elements of the reduction a wave takes at a time
+  static constexpr int X = 8 * Q * sizeof(T) / 16;
+  struct Codes {
+    uint32_t q[P][Q];
+    uint32_t sc[P][B];
+    bool live;  // the wave has this piece (the same in all lanes)
+  };
+  const W4Args& a;
+  int wr, grp;
+
+  // element k + at(b) is the lane's first of block b of the piece that begins at k
+  __device__ __forceinline__ int at(int b) const { return NB ? 128 * b + 32 * grp : 16 * grp; }
+
+  __device__ __forceinline__ void load_codes(Codes& c, const W4Tile& t, int col, int k) const {
+    c.live = t.e >= 0 && k < a.K;
+    if (!c.live) return;
+    const int64_t wrow = (int64_t)t.e * a.N + col + wr;
+    const uint8_t* const qs[2] = {a.q0, a.q1};
+    const uint8_t* const ss[2] = {a.s0, a.s1};
 #pragma unroll
-  for (int b = 0; b < 2; b++) {
-    const uint32_t w[4] = {q[b].x, q[b].y, q[b].z, q[b].w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if constexpr (sizeof(T) == 2) {
-        const bf16x8 a = widen_bf16(w[i], sc[b]);
-#pragma unroll
-        for (int n = 0; n < NT; n++) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (have[n]) v = *reinterpret_cast<const uint4*>(x[n] + k + 32 * b + 8 * i);
-          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, v), acc[n], 0, 0, 0);
-        }
+    for (int h = 0; h < P; h++) {
+      const uint8_t* q = qs[h] + wrow * (a.K / 2) + k / 2 + at(0) / 2;
+      const uint8_t* s = ss[h] + wrow * (a.K / kMx4Block) + k / kMx4Block;
+      if constexpr (NB == 0) {
+        const uint2 v = *reinterpret_cast<const uint2*>(q);
+        c.q[h][0] = v.x, c.q[h][1] = v.y;
+        c.sc[h][0] = *reinterpret_cast<const uint16_t*>(s) >> (8 * (grp >> 1)) & 255;
       } else {
-        float v[NT][8];
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
-#pragma unroll
-          for (int j = 0; j < 8; j++) v[n][j] = 0.f;
-          if (have[n]) load8<float>(x[n] + k + 32 * b + 8 * i, v[n]);
+        for (int b = 0; b < NB; b++) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (!TAIL || k + at(b) < a.K) v = *reinterpret_cast<const uint4*>(q + 64 * b);
+          c.q[h][4 * b] = v.x, c.q[h][4 * b + 1] = v.y, c.q[h][4 * b + 2] = v.z, c.q[h][4 * b + 3] = v.w;
         }
-        const f32x2 a[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], sc[b], 0),
-                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], sc[b], 1),
-                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], sc[b], 2),
-                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], sc[b], 3)};
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-#pragma unroll
-          for (int n = 0; n < NT; n++)
-            acc[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j >> 1][j & 1], v[n][j], acc[n], 0, 0, 0);
+        if constexpr (TAIL) {  // the row's bytes may end here
+          c.sc[h][0] = k + at(0) < a.K ? s[grp] : 0;
+        } else if constexpr (NB == 1) {
+          c.sc[h][0] = *reinterpret_cast<const uint32_t*>(s) >> (8 * grp) & 255;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(s);
+          c.sc[h][0] = v.x >> (8 * grp) & 255;
+          c.sc[h][1] = v.y >> (8 * grp) & 255;
+        }
       }
     }
   }
-}
 
-template <typename T, bool GATED, int NT>
-__global__ void __launch_bounds__(kThreads) w4_kernel(W4Args p) {
-  constexpr int P = GATED ? 2 : 1;  // projections
-  constexpr int ROWS = 16 * NT;
-  __shared__ int s_map[kMaxExperts + 1];
-  __shared__ float s_acc[kWaves][P][ROWS][kRowsW + 1];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wr = lane & 15, grp = lane >> 4;
-  auto seg = [&](int e) { return p.offsets[e]; };
-  const int tiles = build_tile_map<Group::M, ROWS, kRowsW, kThreads>(s_map, seg, p.E, p.R, p.N, tid);
-  const T* X = static_cast<const T*>(p.X);
-  const uint8_t* const qs[2] = {p.q0, p.q1};
-  const uint8_t* const ss[2] = {p.s0, p.s1};
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const TileRange tr = tile_at<Group::M, ROWS, kRowsW, true>(t, s_map, seg, p.E, p.R, p.N, p.K);
-    const int64_t wrow = (int64_t)tr.e * p.N + tr.n0 + wr;
-    const T* x[NT];
-    bool have[NT];
+  // Lanes without a routed row keep what they hold: each lane's column of the product is its own, and
+  // theirs is not stored.  Behind the end of the reduction zeros meet the zero codes.
+  __device__ __forceinline__ void load_rows(uint4 (&x)[X], const W4Tile& t, int k) const {
+    const int r = t.m0 + wr;
+    const T* row = static_cast<const T*>(a.X) + (int64_t)r * a.K + k;
 #pragma unroll
-    for (int n = 0; n < NT; n++) {
-      const int r = tr.m0 + 16 * n + wr;
-      have[n] = r < tr.m_end;
-      x[n] = X + (int64_t)(have[n] ? r : tr.m0) * p.K;
-    }
-    f32x4 acc[P][NT] = {};
-    for (int k0 = wave * kChunk; k0 < p.K; k0 += kWaves * kChunk) {
-      const int k = k0 + 64 * grp;
-      const bool in = k < p.K;  // K is a multiple of 64
-      bool here[NT];
+    for (int b = 0; b < B; b++) {
+      if (TAIL) {
 #pragma unroll
-      for (int n = 0; n < NT; n++) here[n] = have[n] && in;
+        for (int i = 0; i < X / B; i++) x[b * (X / B) + i] = make_uint4(0, 0, 0, 0);
+      }
+      if (r < t.m_end && (!TAIL || k + at(b) < a.K)) {
 #pragma unroll
-      for (int h = 0; h < P; h++) {
-        uint4 q[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        float sc[2] = {1.f, 1.f};
-        if (in) {
-          const uint4* src = reinterpret_cast<const uint4*>(qs[h] + wrow * (p.K / 2) + k / 2);
-          q[0] = src[0];
-          q[1] = src[1];
-          const uint32_t two = *reinterpret_cast<const uint16_t*>(ss[h] + wrow * (p.K / kMx4Block) + k / kMx4Block);
-          sc[0] = mx4_scale(two & 255);
-          sc[1] = mx4_scale(two >> 8);
-        }
-        multiply<T, NT>(q, sc, x, here, k, acc[h]);
+        for (int i = 0; i < X / B; i++) x[b * (X / B) + i] = reinterpret_cast<const uint4*>(row + at(b))[i];
       }
     }
+  }
+
+  __device__ __forceinline__ void multiply(const Codes& c, const uint4 (&x)[X], f32x4 (&acc)[P]) const {
+#pragma unroll
+    for (int i = 0; i < Q; i++) {
+#pragma unroll
+      for (int h = 0; h < P; h++) {
+        const float sc = mx4_scale(c.sc[h][i / 4]);
+        if constexpr (sizeof(T) == 2) {
+          acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_bf16(c.q[h][i], sc), __builtin_bit_cast(bf16x8, x[i]),
+                                                           acc[h], 0, 0, 0);
+        } else {
+          float w[8];
+          widen_f32(c.q[h][i], sc, w);
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            const uint4& u = x[2 * i + j / 4];
+            const uint32_t b = j % 4 == 0 ? u.x : j % 4 == 1 ? u.y : j % 4 == 2 ? u.z : u.w;
+            acc[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[j], __uint_as_float(b), acc[h], 0, 0, 0);
+          }
+        }
+      }
+    }
+  }
+};
+
+template <typename T, int P, int NB, bool TAIL>
+__global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args a, int tiles) {
+  using S = Stream<T, P, NB, TAIL>;
+  constexpr int NW = kStreamWaves, ROWS = kRowsW;
+  __shared__ float s_acc[2][NW][P][ROWS][kRowsW + 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const S st{a, lane & 15, lane >> 4};
+  const int shares = NW / tiles, share = wave % shares, sub = wave / shares;
+  const int iters = (a.K + S::SPAN * shares - 1) / (S::SPAN * shares);
+  const int width = kRowsW * tiles;  // weight rows of the workgroup's tiles
+  int t = xcd_logical_wg();
+  W4Finder<ROWS, false> finder(a.offsets, a.E, a.N / width, lane);
+  W4Tile tile = finder.find(t), ahead = tile;  // the tile in hand, and that of the next piece
+  if (tile.e < 0) return;
+  int it = 0, buf = 0;
+  f32x4 acc[P] = {};
+  typename S::Codes even, odd;
+  uint4 x[S::X] = {};
+  st.load_codes(even, tile, tile.nt * width + kRowsW * sub, share * S::SPAN);
+  // multiplies `cur` while the codes behind it load into `nxt`; false behind the last tile
+  auto step = [&](const typename S::Codes& cur, typename S::Codes& nxt) __attribute__((always_inline)) {
+    if (cur.live) st.load_rows(x, tile, (it * shares + share) * S::SPAN);
+    const bool last = ++it == iters;
+    if (last) {
+      it = 0;
+      t += gridDim.x;
+      ahead = finder.find(t);
+    }
+    st.load_codes(nxt, ahead, ahead.nt * width + kRowsW * sub, (it * shares + share) * S::SPAN);
+    if (cur.live) st.multiply(cur, x, acc);
+    if (!last) return true;
     // lane l holds weight rows 4 (l / 16) .. + 3 of routed row l % 16
 #pragma unroll
-    for (int h = 0; h < P; h++)
+    for (int h = 0; h < P; h++) {
 #pragma unroll
-      for (int n = 0; n < NT; n++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) s_acc[wave][h][16 * n + wr][4 * grp + i] = acc[h][n][i];
+      for (int i = 0; i < 4; i++) s_acc[buf][wave][h][st.wr][4 * st.grp + i] = acc[h][i];
+      acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     __syncthreads();
-    for (int o = tid; o < ROWS * kRowsW; o += kThreads) {
-      const int r = o / kRowsW, c = o % kRowsW;
+    const int rows = tile.m_end - tile.m0;  // at most ROWS
+    for (int o = tid; o < rows * width; o += 64 * NW) {
+      const int r = o / width, c = o % width;
+      const int w0 = (c / kRowsW) * shares;
       float v[P];
 #pragma unroll
       for (int h = 0; h < P; h++) {
-        v[h] = s_acc[0][h][r][c];
-#pragma unroll
-        for (int w = 1; w < kWaves; w++) v[h] += s_acc[w][h][r][c];
+        v[h] = s_acc[buf][w0][h][r][c % kRowsW];
+        for (int w = 1; w < shares; w++) v[h] += s_acc[buf][w0 + w][h][r][c % kRowsW];
       }
       float out = v[0];
-      if constexpr (GATED) out = v[0] * sigmoidf_(v[0]) * v[1];
-      if (tr.m0 + r < tr.m_end) Elem<T>::store(static_cast<T*>(p.out) + (int64_t)(tr.m0 + r) * p.N + tr.n0 + c, out);
+      if constexpr (P == 2) out = v[0] * sigmoidf_(v[0]) * v[1];
+      Elem<T>::store(static_cast<T*>(a.out) + (int64_t)(tile.m0 + r) * a.N + tile.nt * width + c, out);
     }
-    __syncthreads();  // s_acc is the next tile's too
+    buf ^= 1;  // read until the barrier of the next tile, written again behind it
+    tile = ahead;
+    return tile.e >= 0;
+  };
+  while (step(even, odd) && step(odd, even)) {
   }
 }
 
-template <typename T, bool GATED>
+// ---- many rows: the rows in LDS, each weight widened once for up to 96 of them
+// A workgroup takes 64 weight rows of both projections (gated) or 128 of one, 2 x 16 a wave, by up to 96
+// routed rows.  256 bytes of every routed row are staged in LDS (16-byte chunks exchanged by the row's
+// number, so that 16 rows at one place fall on distinct banks) while the 256 before are multiplied; rows
+// and weights are loaded into registers two steps ahead.
+constexpr int kTileRows = 96, kTileThreads = 256;
+
+template <typename T>
+struct Tile4 {
+  static constexpr int KC = 256 / sizeof(T);  // elements of the reduction a step
+  static constexpr int EPL = KC / 4;          // a lane's (32 or 16)
+  static constexpr int Q = EPL / 8;           // code words of them
+};
+
+// A step's products for NTA runs of 16 routed rows
+template <typename T, int NTA>
+__device__ __forceinline__ void multiply_step(const uint4 (*x)[16], const uint32_t (&q)[2][Tile4<T>::Q],
+                                              const uint32_t (&sc)[2], int wr, int grp, f32x4 (&acc)[2][NTA]) {
+  const float s0 = mx4_scale(sc[0]), s1 = mx4_scale(sc[1]);
+#pragma unroll
+  for (int i = 0; i < Tile4<T>::Q; i++) {
+    if constexpr (sizeof(T) == 2) {
+      const bf16x8 w0 = widen_bf16(q[0][i], s0), w1 = widen_bf16(q[1][i], s1);
+#pragma unroll
+      for (int n = 0; n < NTA; n++) {
+        const bf16x8 b = __builtin_bit_cast(bf16x8, x[16 * n + wr][(grp * 4 + i) ^ wr]);
+        acc[0][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, b, acc[0][n], 0, 0, 0);
+        acc[1][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, b, acc[1][n], 0, 0, 0);
+      }
+    } else {
+      float w0[8], w1[8];
+      widen_f32(q[0][i], s0, w0);
+      widen_f32(q[1][i], s1, w1);
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+#pragma unroll
+        for (int n = 0; n < NTA; n++) {
+          const float4 b = __builtin_bit_cast(float4, x[16 * n + wr][(grp * 4 + 2 * i + u) ^ wr]);
+          const float bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            acc[0][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(w0[4 * u + j], bv[j], acc[0][n], 0, 0, 0);
+            acc[1][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(w1[4 * u + j], bv[j], acc[1][n], 0, 0, 0);
+          }
+        }
+      }
+    }
+  }
+}
+
+// One tile with NTA runs of 16 routed rows
+template <typename T, int P, int NTA>
+__device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, uint4 (*s_x)[kTileRows][16]) {
+  using C = Tile4<T>;
+  constexpr int KC = C::KC, EPL = C::EPL, Q = C::Q, XE = 16 / sizeof(T);
+  constexpr int BN = 128 / P;  // weight rows of a tile (per projection)
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wr = lane & 15, grp = lane >> 4;
+  const int steps = (a.K + KC - 1) / KC;
+  const int xr = tid >> 4, xc = tid & 15;  // this thread's row and 16-byte chunk of every 16 staged rows
+  const int rows = tile.m_end - tile.m0;
+  // the wave's two sets of 16 weight rows: both projections of the same, or 32 of the one
+  const uint8_t *qp[2], *sp[2];
+  int ncol[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    ncol[h] = tile.nt * BN + (P == 2 ? 16 * wave : 32 * wave + 16 * h);
+    const int n = ncol[h] + wr < a.N ? ncol[h] + wr : a.N - 1;  // past the last: read, not stored
+    const int64_t wrow = (int64_t)tile.e * a.N + n;
+    qp[h] = (P == 2 && h ? a.q1 : a.q0) + wrow * (a.K / 2) + grp * (EPL / 2);
+    sp[h] = (P == 2 && h ? a.s1 : a.s0) + wrow * (a.K / kMx4Block) + grp * EPL / kMx4Block;
+  }
+  const T* xp[NTA];
+#pragma unroll
+  for (int n = 0; n < NTA; n++) {
+    const int r = 16 * n + xr < rows ? 16 * n + xr : rows - 1;  // rows past the last repeat it, not stored
+    xp[n] = static_cast<const T*>(a.X) + (int64_t)(tile.m0 + r) * a.K + xc * XE;
+  }
+  uint4 xs[2][NTA];
+  uint32_t q[3][2][Q];  // of this step and the two behind it
+  uint32_t sc[3][2];
+  auto load_x = [&](int step, uint4(&x)[NTA]) __attribute__((always_inline)) {
+    const bool in = step * KC + xc * XE < a.K;
+#pragma unroll
+    for (int n = 0; n < NTA; n++) {
+      x[n] = make_uint4(0, 0, 0, 0);  // past the reduction's end zeros meet zero codes
+      if (in) x[n] = *reinterpret_cast<const uint4*>(xp[n] + step * KC);
+    }
+  };
+  auto load_w = [&](int step, uint32_t(&w)[2][Q], uint32_t(&s)[2]) __attribute__((always_inline)) {
+    const int k = step * KC;
+    const bool in = k + grp * EPL < a.K;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int i = 0; i < Q; i++) w[h][i] = 0;
+      s[h] = 0;
+      if (in) {
+        if constexpr (Q == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(qp[h] + k / 2);
+          w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(qp[h] + k / 2);
+          w[h][0] = v.x, w[h][1] = v.y;
+        }
+        s[h] = sp[h][k / kMx4Block];
+      }
+    }
+  };
+  auto stage = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < NTA; n++) s_x[buf][16 * n + xr][xc ^ xr] = xs[buf][n];
+  };
+  f32x4 acc[2][NTA] = {};
+  load_x(0, xs[0]);
+  load_w(0, q[0], sc[0]);
+  load_x(1, xs[1]);
+  load_w(1, q[1], sc[1]);
+  stage(0);
+  __syncthreads();
+  for (int step = 0; step < steps; step += 2) {
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      if (step + u < steps) {
+        load_x(step + u + 2, xs[u]);
+        load_w(step + u + 2, q[2], sc[2]);
+        multiply_step<T, NTA>(s_x[u], q[0], sc[0], wr, grp, acc);
+        stage(u ^ 1);
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+#pragma unroll
+          for (int i = 0; i < Q; i++) q[0][h][i] = q[1][h][i], q[1][h][i] = q[2][h][i];
+          sc[0][h] = sc[1][h], sc[1][h] = sc[2][h];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NTA; n++) {
+    const int r = 16 * n + wr;
+    if (r < rows) {
+      T* o = static_cast<T*>(a.out) + (int64_t)(tile.m0 + r) * a.N + 4 * grp;
+      auto put = [&](int col, const f32x4& v) {
+        if (col >= a.N) return;
+        if constexpr (sizeof(T) == 2)
+          *reinterpret_cast<uint2*>(o + col) = make_uint2((uint32_t)f2bf(v[0]) | ((uint32_t)f2bf(v[1]) << 16),
+                                                          (uint32_t)f2bf(v[2]) | ((uint32_t)f2bf(v[3]) << 16));
+        else
+          *reinterpret_cast<float4*>(o + col) = make_float4(v[0], v[1], v[2], v[3]);
+      };
+      if constexpr (P == 2) {
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = acc[0][n][i] * sigmoidf_(acc[0][n][i]) * acc[1][n][i];
+        put(ncol[0], v);
+      } else {
+        put(ncol[0], acc[0][n]);
+        put(ncol[1], acc[1][n]);
+      }
+    }
+  }
+}
+
+template <typename T, int P>
+__global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(W4Args a) {
+  __shared__ __attribute__((aligned(16))) uint4 s_x[2][kTileRows][16];
+  W4Finder<kTileRows, true> finder(a.offsets, a.E, (a.N * P + 127) / 128, threadIdx.x & 63);
+  for (int t = xcd_logical_wg();; t += gridDim.x) {
+    const W4Tile tile = finder.find(t);
+    if (tile.e < 0) break;
+    switch ((tile.m_end - tile.m0 + 15) / 16) {
+      case 1: do_tile<T, P, 1>(a, tile, s_x); break;
+      case 2: do_tile<T, P, 2>(a, tile, s_x); break;
+      case 3: do_tile<T, P, 3>(a, tile, s_x); break;
+      case 4: do_tile<T, P, 4>(a, tile, s_x); break;
+      case 5: do_tile<T, P, 5>(a, tile, s_x); break;
+      default: do_tile<T, P, 6>(a, tile, s_x);
+    }
+  }
+}
+
+template <int ROWS>
+unsigned w4_grid(const W4Args& p, int ntn, int per_cu) {
+  const int64_t bound = ((int64_t)p.R / ROWS + (p.R < p.E ? p.R : p.E)) * ntn;  // tiles of any routing
+  const int64_t most = (int64_t)device_cu_count() * per_cu;
+  const int64_t g = bound < most ? bound : most;
+  return (unsigned)((g + 7) / 8 * 8);
+}
+
+template <typename T, int P, int NB, bool TAIL>
+hipError_t launch_stream(const W4Args& p, int tiles, hipStream_t st) {
+  hipLaunchKernelGGL((w4_stream_kernel<T, P, NB, TAIL>), dim3(w4_grid<kRowsW>(p, p.N / (kRowsW * tiles), 2)),
+                     dim3(64 * kStreamWaves), 0, st, p, tiles);
+  return hipGetLastError();
+}
+
+template <typename T, int P>
 hipError_t launch_w4(const W4Args& p, hipStream_t st) {
   if (p.R == 0) return hipSuccess;
-  const int64_t bound = ((int64_t)p.R / 16 + (p.R < p.E ? p.R : p.E)) * (p.N / kRowsW);
-  const int64_t most = (int64_t)device_cu_count() * 64;
-  const unsigned grid = (unsigned)(bound < most ? bound : most);
-  if (p.R <= 16)
-    hipLaunchKernelGGL((w4_kernel<T, GATED, 1>), dim3(grid), dim3(kThreads), 0, st, p);
-  else
-    hipLaunchKernelGGL((w4_kernel<T, GATED, 2>), dim3(grid), dim3(kThreads), 0, st, p);
-  return hipGetLastError();
+  if (p.R > (int64_t)p.E * kStreamMaxRows) {
+    constexpr int BN = 128 / P;
+    hipLaunchKernelGGL((w4_tile_kernel<T, P>), dim3(w4_grid<kTileRows>(p, (p.N + BN - 1) / BN, 64)), dim3(kTileThreads),
+                       0, st, p);
+    return hipGetLastError();
+  }
+  // four tiles a workgroup, two shares of the reduction each, where that leaves every compute unit four
+  // workgroups; else fewer tiles and more shares
+  const int64_t all = (int64_t)(p.R < p.E ? p.R : p.E) * (p.N / kRowsW);
+  const int64_t cus = device_cu_count();
+  const int tiles = all >= 16 * cus ? 4 : all >= 4 * cus ? 2 : 1;
+  if constexpr (sizeof(T) == 4) return launch_stream<T, P, 0, false>(p, tiles, st);
+  else if (p.K % 128 != 0) return launch_stream<T, P, 1, true>(p, tiles, st);
+  else if (p.K % 256 != 0 || p.K < 256 * kStreamWaves / tiles) return launch_stream<T, P, 1, false>(p, tiles, st);
+  else return launch_stream<T, P, 2, false>(p, tiles, st);
 }
 
 }  // namespace
@@ -238,13 +548,13 @@ hipError_t mx4_quantize_rows(int eb, int rows, int cols, const void* src, uint8_
 hipError_t gemm1_fwd_w4(int eb, const GemmShape& g, const int* offsets, const void* X, const uint8_t* W1q,
                         const uint8_t* W1s, const uint8_t* W3q, const uint8_t* W3s, void* h, hipStream_t st) {
   const W4Args p{g.R, g.d, g.f, g.E, offsets, X, W1q, W1s, W3q, W3s, h};
-  return eb == 2 ? launch_w4<bf16_t, true>(p, st) : launch_w4<float, true>(p, st);
+  return eb == 2 ? launch_w4<bf16_t, 2>(p, st) : launch_w4<float, 2>(p, st);
 }
 
 hipError_t gemm2_fwd_w4(int eb, const GemmShape& g, const int* offsets, const void* H, const uint8_t* W2q,
                         const uint8_t* W2s, void* Y, hipStream_t st) {
   const W4Args p{g.R, g.f, g.d, g.E, offsets, H, W2q, W2s, nullptr, nullptr, Y};
-  return eb == 2 ? launch_w4<bf16_t, false>(p, st) : launch_w4<float, false>(p, st);
+  return eb == 2 ? launch_w4<bf16_t, 1>(p, st) : launch_w4<float, 1>(p, st);
 }
 
 }  // namespace moe
