@@ -147,17 +147,28 @@ struct W4Finder {
   }
 };
 
+// First tile of a workgroup: workgroups b and b + 8 run on one XCD, which takes 8 neighbouring tiles of
+// every 64 (they share weight tiles or routed rows, and so its L2), so that a last round that is not full
+// is spread over all XCDs.
+__device__ __forceinline__ int first_tile() {
+  const int b = blockIdx.x, in = b & 63;
+  return gridDim.x % 64 == 0 ? b - in + (in & 7) * 8 + in / 8 : b;
+}
+
 // ---- few rows: the weights stream through registers
-// A tile is 16 weight rows by up to 16 routed rows of one expert.  The weights are the matrix product's
+// A tile is 16 weight rows by up to 8 routed rows of one expert.  The weights are the matrix product's
 // left operand, the routed rows its right: lane l holds elements of weight row l % 16 and of routed row
-// l % 16, the same ones of the reduction, and which they are is free.  bf16: NB blocks of 32 at 128
-// apart, block l / 16 of each 128, so that the four lanes of a row read 64 bytes of codes side by side;
-// fp32: 16 of each 64.  The 8 waves of a workgroup are `tiles` neighbouring tiles by 8 / tiles shares of
-// the reduction, taken piece by piece; the shares' sums are added through LDS in order.  Each wave loads
-// the codes of its next piece, of this tile or the next, before it multiplies the one it has.
+// l % 8 (the upper half of the columns is computed twice), the same ones of the reduction, and which
+// they are is free.  bf16: NB blocks of 32 at 128 apart, block l / 16 of each 128, so that the four lanes
+// of a row read 64 bytes of codes side by side; fp32: 16 of each 64.  The 8 waves of a workgroup are
+// `tiles` neighbouring tiles by 8 / tiles shares of the reduction, taken piece by piece; the shares' sums
+// are added through LDS in order.  Each wave loads its next piece, of this tile or the next, before it
+// multiplies the one it has; the routed rows' part comes in whole rows (a load for two of them) and is
+// handed to the lanes through LDS of the wave's own.
 constexpr int kStreamWaves = 8;
 constexpr int kStreamMaxRows = 12;  // rows an expert, on average
-constexpr int kRowsW = 16;          // rows and weight rows of a tile
+constexpr int kRowsW = 16;          // weight rows of a tile
+constexpr int kRowsX = 8;           // routed rows of a tile
 
 // NB: blocks of a lane's piece; 0: half a block (fp32 rows).  TAIL: the last piece may end inside.
 template <typename T, int P, int NB, bool TAIL>
@@ -165,19 +176,21 @@ struct Stream {
   static constexpr int B = NB ? NB : 1;            // blocks touched
   static constexpr int Q = NB ? 4 * NB : 2;        // code words
   static constexpr int SPAN = NB ? 128 * NB : 64;  // elements of the reduction a wave takes at a time
-  static constexpr int X = 8 * Q * sizeof(T) / 16;
-  struct Codes {
+  static constexpr int LPR = SPAN * sizeof(T) / 16;  // lanes (16-byte chunks) of a routed row's piece
+  static constexpr int RPL = kWave / LPR;            // rows of a load
+  static constexpr int XL = kRowsX / RPL;            // loads
+  struct Piece {
     uint32_t q[P][Q];
     uint32_t sc[P][B];
     bool live;  // the wave has this piece (the same in all lanes)
   };
   const W4Args& a;
-  int wr, grp;
+  int lane, wr, grp;
 
   // element k + at(b) is the lane's first of block b of the piece that begins at k
   __device__ __forceinline__ int at(int b) const { return NB ? 128 * b + 32 * grp : 16 * grp; }
 
-  __device__ __forceinline__ void load_codes(Codes& c, const W4Tile& t, int col, int k) const {
+  __device__ __forceinline__ void load_codes(Piece& c, const W4Tile& t, int col, int k) const {
     c.live = t.e >= 0 && k < a.K;
     if (!c.live) return;
     const int64_t wrow = (int64_t)t.e * a.N + col + wr;
@@ -211,42 +224,52 @@ struct Stream {
     }
   }
 
-  // Lanes without a routed row keep what they hold: each lane's column of the product is its own, and
-  // theirs is not stored.  Behind the end of the reduction zeros meet the zero codes.
-  __device__ __forceinline__ void load_rows(uint4 (&x)[X], const W4Tile& t, int k) const {
-    const int r = t.m0 + wr;
-    const T* row = static_cast<const T*>(a.X) + (int64_t)r * a.K + k;
+  // Rows that are not there keep what the register or LDS holds: a row is one column of the product,
+  // and theirs is not stored.  Behind the end of the reduction zeros meet the zero codes.
+  __device__ __forceinline__ void load_rows(uint4 (&x)[XL], const W4Tile& t, int k) const {
+    const int rows = t.m_end - t.m0, chunk = lane % LPR;
+    const T* src = static_cast<const T*>(a.X) + (int64_t)t.m0 * a.K + k + chunk * (16 / (int)sizeof(T));
 #pragma unroll
-    for (int b = 0; b < B; b++) {
-      if (TAIL) {
+    for (int i = 0; i < XL; i++) {
+      const int r = i * RPL + lane / LPR;
+      uint4 v = TAIL ? make_uint4(0, 0, 0, 0) : x[i];
+      if (r < rows && (!TAIL || k + chunk * (16 / (int)sizeof(T)) < a.K))
+        v = *reinterpret_cast<const uint4*>(src + (int64_t)r * a.K);
+      x[i] = v;
+    }
+  }
+  // 16-byte chunks of a row are exchanged by its number: the 8 rows' at one place are on distinct banks
+  __device__ __forceinline__ void hand_over(const uint4 (&x)[XL], uint4 (*s)[LPR], const W4Tile& t) const {
 #pragma unroll
-        for (int i = 0; i < X / B; i++) x[b * (X / B) + i] = make_uint4(0, 0, 0, 0);
-      }
-      if (r < t.m_end && (!TAIL || k + at(b) < a.K)) {
-#pragma unroll
-        for (int i = 0; i < X / B; i++) x[b * (X / B) + i] = reinterpret_cast<const uint4*>(row + at(b))[i];
-      }
+    for (int i = 0; i < XL; i++) {
+      const int r = i * RPL + lane / LPR;
+      if (i * RPL < t.m_end - t.m0) s[r][(lane % LPR) ^ r] = x[i];
     }
   }
 
-  __device__ __forceinline__ void multiply(const Codes& c, const uint4 (&x)[X], f32x4 (&acc)[P]) const {
+  __device__ __forceinline__ void multiply(const Piece& c, const uint4 (*s)[LPR], f32x4 (&acc)[P]) const {
+    const int r = wr % kRowsX;
 #pragma unroll
     for (int i = 0; i < Q; i++) {
+      if constexpr (sizeof(T) == 2) {
+        const bf16x8 x = __builtin_bit_cast(bf16x8, s[r][(16 * (i / 4) + 4 * grp + i % 4) ^ r]);
 #pragma unroll
-      for (int h = 0; h < P; h++) {
-        const float sc = mx4_scale(c.sc[h][i / 4]);
-        if constexpr (sizeof(T) == 2) {
-          acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_bf16(c.q[h][i], sc), __builtin_bit_cast(bf16x8, x[i]),
-                                                           acc[h], 0, 0, 0);
-        } else {
-          float w[8];
-          widen_f32(c.q[h][i], sc, w);
+        for (int h = 0; h < P; h++)
+          acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_bf16(c.q[h][i], mx4_scale(c.sc[h][i / 4])), x, acc[h],
+                                                           0, 0, 0);
+      } else {
+        float w[P][8];
 #pragma unroll
-          for (int j = 0; j < 8; j++) {
-            const uint4& u = x[2 * i + j / 4];
-            const uint32_t b = j % 4 == 0 ? u.x : j % 4 == 1 ? u.y : j % 4 == 2 ? u.z : u.w;
-            acc[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[j], __uint_as_float(b), acc[h], 0, 0, 0);
-          }
+        for (int h = 0; h < P; h++) widen_f32(c.q[h][i], mx4_scale(c.sc[h][0]), w[h]);
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+          const float4 x = __builtin_bit_cast(float4, s[r][(4 * grp + 2 * i + u) ^ r]);
+          const float xv[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int h = 0; h < P; h++)
+              acc[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[h][4 * u + j], xv[j], acc[h], 0, 0, 0);
         }
       }
     }
@@ -256,25 +279,27 @@ struct Stream {
 template <typename T, int P, int NB, bool TAIL>
 __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args a, int tiles) {
   using S = Stream<T, P, NB, TAIL>;
-  constexpr int NW = kStreamWaves, ROWS = kRowsW;
+  constexpr int NW = kStreamWaves, ROWS = kRowsX;
+  __shared__ __attribute__((aligned(16))) uint4 s_x[NW][ROWS][S::LPR];
   __shared__ float s_acc[2][NW][P][ROWS][kRowsW + 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const S st{a, lane & 15, lane >> 4};
+  const S st{a, lane, lane & 15, lane >> 4};
   const int shares = NW / tiles, share = wave % shares, sub = wave / shares;
   const int iters = (a.K + S::SPAN * shares - 1) / (S::SPAN * shares);
   const int width = kRowsW * tiles;  // weight rows of the workgroup's tiles
-  int t = xcd_logical_wg();
+  int t = first_tile();
   W4Finder<ROWS, false> finder(a.offsets, a.E, a.N / width, lane);
   W4Tile tile = finder.find(t), ahead = tile;  // the tile in hand, and that of the next piece
   if (tile.e < 0) return;
   int it = 0, buf = 0;
   f32x4 acc[P] = {};
-  typename S::Codes even, odd;
-  uint4 x[S::X] = {};
+  typename S::Piece even, odd;
+  uint4 x[S::XL] = {};
   st.load_codes(even, tile, tile.nt * width + kRowsW * sub, share * S::SPAN);
-  // multiplies `cur` while the codes behind it load into `nxt`; false behind the last tile
-  auto step = [&](const typename S::Codes& cur, typename S::Codes& nxt) __attribute__((always_inline)) {
-    if (cur.live) st.load_rows(x, tile, (it * shares + share) * S::SPAN);
+  if (even.live) st.load_rows(x, tile, share * S::SPAN);
+  // multiplies `cur` while the piece behind it loads into `nxt`; false behind the last tile
+  auto step = [&](const typename S::Piece& cur, typename S::Piece& nxt) __attribute__((always_inline)) {
+    if (cur.live) st.hand_over(x, s_x[wave], tile);
     const bool last = ++it == iters;
     if (last) {
       it = 0;
@@ -282,13 +307,18 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
       ahead = finder.find(t);
     }
     st.load_codes(nxt, ahead, ahead.nt * width + kRowsW * sub, (it * shares + share) * S::SPAN);
-    if (cur.live) st.multiply(cur, x, acc);
+    if (nxt.live) st.load_rows(x, ahead, (it * shares + share) * S::SPAN);
+    wave_lds_fence();
+    if (cur.live) st.multiply(cur, s_x[wave], acc);
+    wave_lds_fence();
     if (!last) return true;
     // lane l holds weight rows 4 (l / 16) .. + 3 of routed row l % 16
 #pragma unroll
     for (int h = 0; h < P; h++) {
+      if (st.wr < ROWS) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) s_acc[buf][wave][h][st.wr][4 * st.grp + i] = acc[h][i];
+        for (int i = 0; i < 4; i++) s_acc[buf][wave][h][st.wr][4 * st.grp + i] = acc[h][i];
+      }
       acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     __syncthreads();
@@ -482,7 +512,7 @@ template <typename T, int P>
 __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(W4Args a) {
   __shared__ __attribute__((aligned(16))) uint4 s_x[2][kTileRows][16];
   W4Finder<kTileRows, true> finder(a.offsets, a.E, (a.N * P + 127) / 128, threadIdx.x & 63);
-  for (int t = xcd_logical_wg();; t += gridDim.x) {
+  for (int t = first_tile();; t += gridDim.x) {
     const W4Tile tile = finder.find(t);
     if (tile.e < 0) break;
     switch ((tile.m_end - tile.m0 + 15) / 16) {
@@ -501,12 +531,12 @@ unsigned w4_grid(const W4Args& p, int ntn, int per_cu) {
   const int64_t bound = ((int64_t)p.R / ROWS + (p.R < p.E ? p.R : p.E)) * ntn;  // tiles of any routing
   const int64_t most = (int64_t)device_cu_count() * per_cu;
   const int64_t g = bound < most ? bound : most;
-  return (unsigned)((g + 7) / 8 * 8);
+  return (unsigned)(g < 64 ? g : (g + 63) / 64 * 64);
 }
 
 template <typename T, int P, int NB, bool TAIL>
 hipError_t launch_stream(const W4Args& p, int tiles, hipStream_t st) {
-  hipLaunchKernelGGL((w4_stream_kernel<T, P, NB, TAIL>), dim3(w4_grid<kRowsW>(p, p.N / (kRowsW * tiles), 2)),
+  hipLaunchKernelGGL((w4_stream_kernel<T, P, NB, TAIL>), dim3(w4_grid<kRowsX>(p, p.N / (kRowsW * tiles), 2)),
                      dim3(64 * kStreamWaves), 0, st, p, tiles);
   return hipGetLastError();
 }
