@@ -85,40 +85,110 @@ __global__ void __launch_bounds__(kThreads) ck8_unpack_swiglu_kernel(int64_t n, 
   }
 }
 
+// Eight elements as loaded
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16_t> {
+  uint4 q;
+  __device__ __forceinline__ void load(const bf16_t* p) { q = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+
+// Both combines: a wave a token, whose rows and gates the lanes hold and pass on; U chunks of all k (up
+// to KG) rows are loaded before any arithmetic.  KG = 0: any k, a row at a time.
+
 // y[t] = y_add[t] + sum_j gates[t, j] y_perm[slot_row[t, j]] in the order and arithmetic of the plain
 // combine (bit for bit its y); every routed row is read by exactly one token, so its codes are
-// written on the way.
-template <typename T>
+// written on the way.  blockIdx.y: parts of the row, which do not depend on each other.
+template <typename T, int KG, int U>
 __global__ void __launch_bounds__(kThreads) combine_c8_kernel(int ntok, int d, int k, const T* __restrict__ y_perm,
                                                               const float* __restrict__ gates,
                                                               const int32_t* __restrict__ slot_row,
                                                               const T* __restrict__ y_add, T* __restrict__ y,
                                                               int8_t* __restrict__ yq, uint8_t* __restrict__ ys) {
   const int lane = threadIdx.x & 63;
-  const int nchunk = d / 8;
+  const int nchunk = d / 8;  // a multiple of 8: quads stay whole
+  auto encode = [&](const float (&v)[8], int64_t r, int c) __attribute__((always_inline)) {
+    const int byte = ck8_scale_byte(quad_amax(v));
+    reinterpret_cast<uint2*>(yq + r * d)[c] = encode8(v, byte);
+    if ((lane & 3) == 0) ys[r * (d / kCk8Block) + (c >> 2)] = (uint8_t)byte;
+  };
   for (int64_t t = (int64_t)blockIdx.x * kTokPerBlock + (threadIdx.x >> 6); t < ntok;
        t += (int64_t)gridDim.x * kTokPerBlock) {
-    for (int c = lane; c < nchunk; c += kWave) {  // nchunk is a multiple of 8: quads stay whole
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (y_add) load8<T>(y_add + t * d + c * 8, acc);
-      for (int j = 0; j < k; j++) {
-        const int64_t r = slot_row[t * k + j];
-        const float g = gates[t * k + j];
-        float v[8];
-        load8<T>(y_perm + r * d + c * 8, v);
-        const int byte = ck8_scale_byte(quad_amax(v));
-        reinterpret_cast<uint2*>(yq + r * d)[c] = encode8(v, byte);
-        if ((lane & 3) == 0) ys[r * (d / kCk8Block) + (c >> 2)] = (uint8_t)byte;
+    const int my_r = lane < k ? slot_row[t * k + lane] : 0;
+    const float my_g = lane < k ? gates[t * k + lane] : 0.f;
+    for (int c0 = blockIdx.y * U * kWave + lane; c0 < nchunk; c0 += gridDim.y * U * kWave) {
+      if constexpr (KG > 0) {
+        Raw8<T> q[U][KG + 1];
 #pragma unroll
-        for (int i = 0; i < 8; i++) acc[i] = fmaf(g, v[i], acc[i]);
+        for (int u = 0; u < U; u++) {
+          const int c = c0 + u * kWave;
+          q[u][KG].zero();
+          if (y_add && c < nchunk) q[u][KG].load(y_add + t * d + c * 8);
+#pragma unroll
+          for (int j = 0; j < KG; j++) {
+            const int64_t r = __builtin_amdgcn_readlane(my_r, j);
+            if (j < k && c < nchunk) q[u][j].load(y_perm + r * d + c * 8);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+          const int c = c0 + u * kWave;
+          if (c < nchunk) {
+            float acc[8];
+            q[u][KG].widen(acc);
+#pragma unroll
+            for (int j = 0; j < KG; j++) {
+              if (j < k) {
+                const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_g), j));
+                float v[8];
+                q[u][j].widen(v);
+                encode(v, __builtin_amdgcn_readlane(my_r, j), c);
+#pragma unroll
+                for (int i = 0; i < 8; i++) acc[i] = fmaf(g, v[i], acc[i]);
+              }
+            }
+            store8<T>(y + t * d + c * 8, acc);
+          }
+        }
+      } else {
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (y_add) load8<T>(y_add + t * d + c0 * 8, acc);
+        for (int j = 0; j < k; j++) {
+          const int64_t r = __builtin_amdgcn_readlane(my_r, j);
+          const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_g), j));
+          float v[8];
+          load8<T>(y_perm + r * d + c0 * 8, v);
+          encode(v, r, c0);
+#pragma unroll
+          for (int i = 0; i < 8; i++) acc[i] = fmaf(g, v[i], acc[i]);
+        }
+        store8<T>(y + t * d + c0 * 8, acc);
       }
-      store8<T>(y + t * d + c * 8, acc);
     }
   }
 }
 
 // In the order and arithmetic of the plain backward (its results, bit for bit, on the kept values).
-template <typename T>
+template <typename T, int KG, int U>
 __global__ void __launch_bounds__(kThreads) combine_bwd_c8_kernel(int ntok, int d, int k, const T* __restrict__ dy,
                                                                   const int8_t* __restrict__ yq,
                                                                   const uint8_t* __restrict__ ys,
@@ -129,23 +199,79 @@ __global__ void __launch_bounds__(kThreads) combine_bwd_c8_kernel(int ntok, int 
   const int nchunk = d / 8;
   for (int64_t t = (int64_t)blockIdx.x * kTokPerBlock + (threadIdx.x >> 6); t < ntok;
        t += (int64_t)gridDim.x * kTokPerBlock) {
-    for (int j = 0; j < k; j++) {
-      const int64_t r = slot_row[t * k + j];
-      const float g = gates[t * k + j];
-      float dot = 0.f;
-      for (int c = lane; c < nchunk; c += kWave) {
-        float u[8], v[8], o[8];
-        load8<T>(dy + t * d + c * 8, u);
-        decode8(reinterpret_cast<const uint2*>(yq + r * d)[c], ys[r * (d / kCk8Block) + (c >> 2)], v);
+    const int my_r = lane < k ? slot_row[t * k + lane] : 0;
+    const float my_g = lane < k ? gates[t * k + lane] : 0.f;
+    if constexpr (KG > 0) {
+      float dot[KG];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          dot = fmaf(u[i], v[i], dot);
-          o[i] = g * u[i];
+      for (int j = 0; j < KG; j++) dot[j] = 0.f;
+      for (int c0 = lane; c0 < nchunk; c0 += U * kWave) {
+        Raw8<T> e[U];
+        uint2 q[U][KG];
+        int s[U][KG];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+          const int c = c0 + u * kWave;
+          if (c < nchunk) e[u].load(dy + t * d + c * 8);
+#pragma unroll
+          for (int j = 0; j < KG; j++) {
+            const int64_t r = __builtin_amdgcn_readlane(my_r, j);
+            if (j < k && c < nchunk) {
+              q[u][j] = reinterpret_cast<const uint2*>(yq + r * d)[c];
+              s[u][j] = ys[r * (d / kCk8Block) + (c >> 2)];
+            }
+          }
         }
-        store8<T>(dy_perm + r * d + c * 8, o);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+          const int c = c0 + u * kWave;
+          if (c < nchunk) {
+            float x[8];
+            e[u].widen(x);
+#pragma unroll
+            for (int j = 0; j < KG; j++) {
+              if (j < k) {
+                const int64_t r = __builtin_amdgcn_readlane(my_r, j);
+                const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_g), j));
+                float v[8], o[8];
+                decode8(q[u][j], s[u][j], v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                  dot[j] = fmaf(x[i], v[i], dot[j]);
+                  o[i] = g * x[i];
+                }
+                store8<T>(dy_perm + r * d + c * 8, o);
+              }
+            }
+          }
+        }
       }
-      dot = wave_sum(dot);
-      if (lane == 0) dgates[t * k + j] = dot;
+#pragma unroll
+      for (int j = 0; j < KG; j++) {
+        if (j < k) {
+          const float sum = wave_sum(dot[j]);
+          if (lane == 0) dgates[t * k + j] = sum;
+        }
+      }
+    } else {
+      for (int j = 0; j < k; j++) {
+        const int64_t r = __builtin_amdgcn_readlane(my_r, j);
+        const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_g), j));
+        float dot = 0.f;
+        for (int c = lane; c < nchunk; c += kWave) {
+          float u[8], v[8], o[8];
+          load8<T>(dy + t * d + c * 8, u);
+          decode8(reinterpret_cast<const uint2*>(yq + r * d)[c], ys[r * (d / kCk8Block) + (c >> 2)], v);
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            dot = fmaf(u[i], v[i], dot);
+            o[i] = g * u[i];
+          }
+          store8<T>(dy_perm + r * d + c * 8, o);
+        }
+        dot = wave_sum(dot);
+        if (lane == 0) dgates[t * k + j] = dot;
+      }
     }
   }
 }
@@ -188,15 +314,46 @@ hipError_t ck8_unpack_rows(int eb, int rows, int cols, const int8_t* q, const ui
   return hipGetLastError();
 }
 
+template <typename T>
+static hipError_t combine_c8(int T_, int d, int k, const T* y_perm, const float* gates, const int32_t* slot_row,
+                             const T* y_add, T* y, int8_t* yq, uint8_t* ys, hipStream_t st) {
+  constexpr int U = 2;
+  const int parts = (d / 8 + U * kWave - 1) / (U * kWave);
+  const dim3 grid(grid_for(T_, kTokPerBlock).x, T_ * (int64_t)parts <= 4096 ? parts : 1);
+  if (k <= 4)
+    hipLaunchKernelGGL((combine_c8_kernel<T, 4, U>), grid, dim3(kThreads), 0, st, T_, d, k, y_perm, gates, slot_row,
+                       y_add, y, yq, ys);
+  else if (k <= 8)
+    hipLaunchKernelGGL((combine_c8_kernel<T, 8, 1>), grid, dim3(kThreads), 0, st, T_, d, k, y_perm, gates, slot_row,
+                       y_add, y, yq, ys);
+  else
+    hipLaunchKernelGGL((combine_c8_kernel<T, 0, 1>), grid, dim3(kThreads), 0, st, T_, d, k, y_perm, gates, slot_row,
+                       y_add, y, yq, ys);
+  return hipGetLastError();
+}
+
 hipError_t combine_rows_c8(int eb, int T, int d, int k, const void* y_perm, const float* gates, const int32_t* slot_row,
                            const void* y_add, void* y, int8_t* yq, uint8_t* ys, hipStream_t st) {
   if (T == 0) return hipSuccess;
   if (eb == 2)
-    hipLaunchKernelGGL(combine_c8_kernel<bf16_t>, grid_for(T, kTokPerBlock), dim3(kThreads), 0, st, T, d, k,
-                       (const bf16_t*)y_perm, gates, slot_row, (const bf16_t*)y_add, (bf16_t*)y, yq, ys);
+    return combine_c8(T, d, k, (const bf16_t*)y_perm, gates, slot_row, (const bf16_t*)y_add, (bf16_t*)y, yq, ys, st);
+  return combine_c8(T, d, k, (const float*)y_perm, gates, slot_row, (const float*)y_add, (float*)y, yq, ys, st);
+}
+
+template <typename T>
+static hipError_t combine_bwd_c8(int T_, int d, int k, const T* dy, const int8_t* yq, const uint8_t* ys,
+                                 const float* gates, const int32_t* slot_row, T* dy_perm, float* dgates,
+                                 hipStream_t st) {
+  const dim3 grid = grid_for(T_, kTokPerBlock);
+  if (k <= 4)
+    hipLaunchKernelGGL((combine_bwd_c8_kernel<T, 4, 2>), grid, dim3(kThreads), 0, st, T_, d, k, dy, yq, ys, gates,
+                       slot_row, dy_perm, dgates);
+  else if (k <= 8)
+    hipLaunchKernelGGL((combine_bwd_c8_kernel<T, 8, 1>), grid, dim3(kThreads), 0, st, T_, d, k, dy, yq, ys, gates,
+                       slot_row, dy_perm, dgates);
   else
-    hipLaunchKernelGGL(combine_c8_kernel<float>, grid_for(T, kTokPerBlock), dim3(kThreads), 0, st, T, d, k,
-                       (const float*)y_perm, gates, slot_row, (const float*)y_add, (float*)y, yq, ys);
+    hipLaunchKernelGGL((combine_bwd_c8_kernel<T, 0, 1>), grid, dim3(kThreads), 0, st, T_, d, k, dy, yq, ys, gates,
+                       slot_row, dy_perm, dgates);
   return hipGetLastError();
 }
 
@@ -204,13 +361,8 @@ hipError_t combine_rows_bwd_c8(int eb, int T, int d, int k, const void* dy, cons
                                const float* gates, const int32_t* slot_row, void* dy_perm, float* dgates,
                                hipStream_t st) {
   if (T == 0) return hipSuccess;
-  if (eb == 2)
-    hipLaunchKernelGGL(combine_bwd_c8_kernel<bf16_t>, grid_for(T, kTokPerBlock), dim3(kThreads), 0, st, T, d, k,
-                       (const bf16_t*)dy, yq, ys, gates, slot_row, (bf16_t*)dy_perm, dgates);
-  else
-    hipLaunchKernelGGL(combine_bwd_c8_kernel<float>, grid_for(T, kTokPerBlock), dim3(kThreads), 0, st, T, d, k,
-                       (const float*)dy, yq, ys, gates, slot_row, (float*)dy_perm, dgates);
-  return hipGetLastError();
+  if (eb == 2) return combine_bwd_c8(T, d, k, (const bf16_t*)dy, yq, ys, gates, slot_row, (bf16_t*)dy_perm, dgates, st);
+  return combine_bwd_c8(T, d, k, (const float*)dy, yq, ys, gates, slot_row, (float*)dy_perm, dgates, st);
 }
 
 }  // namespace moe
