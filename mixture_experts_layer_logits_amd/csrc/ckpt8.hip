@@ -85,12 +85,18 @@ __global__ void __launch_bounds__(kThreads) ck8_unpack_swiglu_kernel(int64_t n, 
   }
 }
 
-// Eight elements as loaded
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Eight elements as loaded; load_last: by their last reader (they leave the caches to what comes next:
+// 62 -> 57 us for the combine of T = 8192, k = 4, d = 2048)
 template <typename T> struct Raw8;
 template <> struct Raw8<bf16_t> {
-  uint4 q;
-  __device__ __forceinline__ void load(const bf16_t* p) { q = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
+  u32x4 q;
+  __device__ __forceinline__ void load(const bf16_t* p) { q = *reinterpret_cast<const u32x4*>(p); }
+  __device__ __forceinline__ void load_last(const bf16_t* p) {
+    q = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  }
+  __device__ __forceinline__ void zero() { q = u32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -101,20 +107,25 @@ template <> struct Raw8<bf16_t> {
   }
 };
 template <> struct Raw8<float> {
-  float4 a, b;
+  f32x4 a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+    a = reinterpret_cast<const f32x4*>(p)[0];
+    b = reinterpret_cast<const f32x4*>(p)[1];
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load_last(const float* p) {
+    a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+    b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = f32x4{0.f, 0.f, 0.f, 0.f}; }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
 };
 
-// Both combines: a wave a token, whose rows and gates the lanes hold and pass on; U chunks of all k (up
-// to KG) rows are loaded before any arithmetic.  KG = 0: any k, a row at a time.
-
+// A wave a token, whose rows and gates the lanes hold and pass on; U chunks of all k (up to KG) rows are
+// loaded before any arithmetic (U = 4: 106 us against 112 with 2, at T = 8192, k = 4, d = 2048 with the
+// unpack behind it).  KG = 0: any k, a row at a time.
+//
 // y[t] = y_add[t] + sum_j gates[t, j] y_perm[slot_row[t, j]] in the order and arithmetic of the plain
 // combine (bit for bit its y); every routed row is read by exactly one token, so its codes are
 // written on the way.  blockIdx.y: parts of the row, which do not depend on each other.
@@ -128,7 +139,9 @@ __global__ void __launch_bounds__(kThreads) combine_c8_kernel(int ntok, int d, i
   const int nchunk = d / 8;  // a multiple of 8: quads stay whole
   auto encode = [&](const float (&v)[8], int64_t r, int c) __attribute__((always_inline)) {
     const int byte = ck8_scale_byte(quad_amax(v));
-    reinterpret_cast<uint2*>(yq + r * d)[c] = encode8(v, byte);
+    const uint2 w = encode8(v, byte);
+    // read again only in the backward (111 -> 105 us with the unpack behind it)
+    __builtin_nontemporal_store((uint64_t)w.y << 32 | w.x, reinterpret_cast<uint64_t*>(yq + r * d) + c);
     if ((lane & 3) == 0) ys[r * (d / kCk8Block) + (c >> 2)] = (uint8_t)byte;
   };
   for (int64_t t = (int64_t)blockIdx.x * kTokPerBlock + (threadIdx.x >> 6); t < ntok;
@@ -146,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) combine_c8_kernel(int ntok, int d, i
 #pragma unroll
           for (int j = 0; j < KG; j++) {
             const int64_t r = __builtin_amdgcn_readlane(my_r, j);
-            if (j < k && c < nchunk) q[u][j].load(y_perm + r * d + c * 8);
+            if (j < k && c < nchunk) q[u][j].load_last(y_perm + r * d + c * 8);
           }
         }
 #pragma unroll
@@ -187,9 +200,11 @@ __global__ void __launch_bounds__(kThreads) combine_c8_kernel(int ntok, int d, i
   }
 }
 
-// In the order and arithmetic of the plain backward (its results, bit for bit, on the kept values).
-template <typename T, int KG, int U>
-__global__ void __launch_bounds__(kThreads) combine_bwd_c8_kernel(int ntok, int d, int k, const T* __restrict__ dy,
+// In the order and arithmetic of the plain backward (its results, bit for bit, on the kept values).  A
+// wave a routed slot: the k waves that share a token's dy read it from the caches (184 us at T = 16384, k =
+// 4, d = 4096, against 195 for a wave a token; 12.9 against 16.5 at T = 1531, k = 6, d = 1088 in fp32).
+template <typename T, int U>
+__global__ void __launch_bounds__(kThreads) combine_bwd_c8_kernel(int64_t nslot, int d, int k, const T* __restrict__ dy,
                                                                   const int8_t* __restrict__ yq,
                                                                   const uint8_t* __restrict__ ys,
                                                                   const float* __restrict__ gates,
@@ -197,82 +212,42 @@ __global__ void __launch_bounds__(kThreads) combine_bwd_c8_kernel(int ntok, int 
                                                                   T* __restrict__ dy_perm, float* __restrict__ dgates) {
   const int lane = threadIdx.x & 63;
   const int nchunk = d / 8;
-  for (int64_t t = (int64_t)blockIdx.x * kTokPerBlock + (threadIdx.x >> 6); t < ntok;
-       t += (int64_t)gridDim.x * kTokPerBlock) {
-    const int my_r = lane < k ? slot_row[t * k + lane] : 0;
-    const float my_g = lane < k ? gates[t * k + lane] : 0.f;
-    if constexpr (KG > 0) {
-      float dot[KG];
+  for (int64_t i = (int64_t)blockIdx.x * kTokPerBlock + (threadIdx.x >> 6); i < nslot;
+       i += (int64_t)gridDim.x * kTokPerBlock) {
+    const int64_t t = i / k, r = slot_row[i];
+    const float g = gates[i];
+    float dot = 0.f;
+    for (int c0 = lane; c0 < nchunk; c0 += U * kWave) {
+      Raw8<T> e[U];
+      uint2 q[U];
+      int s[U];
 #pragma unroll
-      for (int j = 0; j < KG; j++) dot[j] = 0.f;
-      for (int c0 = lane; c0 < nchunk; c0 += U * kWave) {
-        Raw8<T> e[U];
-        uint2 q[U][KG];
-        int s[U][KG];
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-          const int c = c0 + u * kWave;
-          if (c < nchunk) e[u].load(dy + t * d + c * 8);
-#pragma unroll
-          for (int j = 0; j < KG; j++) {
-            const int64_t r = __builtin_amdgcn_readlane(my_r, j);
-            if (j < k && c < nchunk) {
-              q[u][j] = reinterpret_cast<const uint2*>(yq + r * d)[c];
-              s[u][j] = ys[r * (d / kCk8Block) + (c >> 2)];
-            }
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-          const int c = c0 + u * kWave;
-          if (c < nchunk) {
-            float x[8];
-            e[u].widen(x);
-#pragma unroll
-            for (int j = 0; j < KG; j++) {
-              if (j < k) {
-                const int64_t r = __builtin_amdgcn_readlane(my_r, j);
-                const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_g), j));
-                float v[8], o[8];
-                decode8(q[u][j], s[u][j], v);
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                  dot[j] = fmaf(x[i], v[i], dot[j]);
-                  o[i] = g * x[i];
-                }
-                store8<T>(dy_perm + r * d + c * 8, o);
-              }
-            }
-          }
+      for (int u = 0; u < U; u++) {
+        const int c = c0 + u * kWave;
+        if (c < nchunk) {
+          e[u].load(dy + t * d + c * 8);
+          q[u] = reinterpret_cast<const uint2*>(yq + r * d)[c];
+          s[u] = ys[r * (d / kCk8Block) + (c >> 2)];
         }
       }
 #pragma unroll
-      for (int j = 0; j < KG; j++) {
-        if (j < k) {
-          const float sum = wave_sum(dot[j]);
-          if (lane == 0) dgates[t * k + j] = sum;
-        }
-      }
-    } else {
-      for (int j = 0; j < k; j++) {
-        const int64_t r = __builtin_amdgcn_readlane(my_r, j);
-        const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_g), j));
-        float dot = 0.f;
-        for (int c = lane; c < nchunk; c += kWave) {
-          float u[8], v[8], o[8];
-          load8<T>(dy + t * d + c * 8, u);
-          decode8(reinterpret_cast<const uint2*>(yq + r * d)[c], ys[r * (d / kCk8Block) + (c >> 2)], v);
+      for (int u = 0; u < U; u++) {
+        const int c = c0 + u * kWave;
+        if (c < nchunk) {
+          float x[8], v[8], o[8];
+          e[u].widen(x);
+          decode8(q[u], s[u], v);
 #pragma unroll
-          for (int i = 0; i < 8; i++) {
-            dot = fmaf(u[i], v[i], dot);
-            o[i] = g * u[i];
+          for (int n = 0; n < 8; n++) {
+            dot = fmaf(x[n], v[n], dot);
+            o[n] = g * x[n];
           }
           store8<T>(dy_perm + r * d + c * 8, o);
         }
-        dot = wave_sum(dot);
-        if (lane == 0) dgates[t * k + j] = dot;
       }
     }
+    dot = wave_sum(dot);
+    if (lane == 0) dgates[i] = dot;
   }
 }
 
@@ -317,14 +292,15 @@ hipError_t ck8_unpack_rows(int eb, int rows, int cols, const int8_t* q, const ui
 template <typename T>
 static hipError_t combine_c8(int T_, int d, int k, const T* y_perm, const float* gates, const int32_t* slot_row,
                              const T* y_add, T* y, int8_t* yq, uint8_t* ys, hipStream_t st) {
-  constexpr int U = 2;
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;  // fp32 rows take twice the registers
+  // few tokens: the parts of a row to a wave each, up to what the waves of the device hold
   const int parts = (d / 8 + U * kWave - 1) / (U * kWave);
   const dim3 grid(grid_for(T_, kTokPerBlock).x, T_ * (int64_t)parts <= 4096 ? parts : 1);
   if (k <= 4)
     hipLaunchKernelGGL((combine_c8_kernel<T, 4, U>), grid, dim3(kThreads), 0, st, T_, d, k, y_perm, gates, slot_row,
                        y_add, y, yq, ys);
   else if (k <= 8)
-    hipLaunchKernelGGL((combine_c8_kernel<T, 8, 1>), grid, dim3(kThreads), 0, st, T_, d, k, y_perm, gates, slot_row,
+    hipLaunchKernelGGL((combine_c8_kernel<T, 8, U / 2>), grid, dim3(kThreads), 0, st, T_, d, k, y_perm, gates, slot_row,
                        y_add, y, yq, ys);
   else
     hipLaunchKernelGGL((combine_c8_kernel<T, 0, 1>), grid, dim3(kThreads), 0, st, T_, d, k, y_perm, gates, slot_row,
@@ -344,16 +320,9 @@ template <typename T>
 static hipError_t combine_bwd_c8(int T_, int d, int k, const T* dy, const int8_t* yq, const uint8_t* ys,
                                  const float* gates, const int32_t* slot_row, T* dy_perm, float* dgates,
                                  hipStream_t st) {
-  const dim3 grid = grid_for(T_, kTokPerBlock);
-  if (k <= 4)
-    hipLaunchKernelGGL((combine_bwd_c8_kernel<T, 4, 2>), grid, dim3(kThreads), 0, st, T_, d, k, dy, yq, ys, gates,
-                       slot_row, dy_perm, dgates);
-  else if (k <= 8)
-    hipLaunchKernelGGL((combine_bwd_c8_kernel<T, 8, 1>), grid, dim3(kThreads), 0, st, T_, d, k, dy, yq, ys, gates,
-                       slot_row, dy_perm, dgates);
-  else
-    hipLaunchKernelGGL((combine_bwd_c8_kernel<T, 0, 1>), grid, dim3(kThreads), 0, st, T_, d, k, dy, yq, ys, gates,
-                       slot_row, dy_perm, dgates);
+  const int64_t n = (int64_t)T_ * k;
+  hipLaunchKernelGGL((combine_bwd_c8_kernel<T, 4>), grid_for(n, kTokPerBlock), dim3(kThreads), 0, st, n, d, k, dy, yq,
+                     ys, gates, slot_row, dy_perm, dgates);
   return hipGetLastError();
 }
 
