@@ -93,6 +93,16 @@ __device__ __forceinline__ void widen_f32(uint32_t c, float scale, float (&v)[8]
   v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = d[0], v[5] = d[1], v[6] = e[0], v[7] = e[1];
 }
 
+// Loads go through buffer resources: a lane whose offset lies past the end (kNowhere: anywhere's) reads
+// zeros and fetches nothing, so no load stands under a branch, and the number of loads in flight, which the
+// waits count, is known.
+constexpr uint32_t kNowhere = 0xffffffffu;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 // Sums over the lanes up to and including each
 __device__ __forceinline__ int wave_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1, 2, 4, 8
@@ -166,7 +176,11 @@ __device__ __forceinline__ int first_tile() {
 // multiplies the one it has; the routed rows' part comes in whole rows (a load for two of them) and is
 // handed to the lanes through LDS of the wave's own.
 constexpr int kStreamWaves = 8;
-constexpr int kStreamMaxRows = 12;  // rows an expert, on average
+// Rows an expert, on average, up to which the weights stream; above, the tiles of many rows are faster
+// (us, stream / tiles).  bf16: 4 rows 29.5 / 34.5, 6 rows 34.5 / 34.4, 12 rows 50 / 38 (E = 64, d = 2048, f
+// = 1024, gated); 4 rows 45 / 50, 8 rows 61 / 51 (E = 32, d = 4096, f = 1536).  fp32, whose products take
+// most of the time: 8 rows 13.1 / 14.6, 16 rows 21.4 / 22.8, 24 rows 27.4 / 23.0 (E = 8, K = 1024, N = 2048)
+constexpr int kStreamMaxRows16 = 5, kStreamMaxRows32 = 16;
 constexpr int kRowsW = 16;          // weight rows of a tile
 constexpr int kRowsX = 8;           // routed rows of a tile
 
@@ -179,10 +193,15 @@ struct Stream {
   static constexpr int LPR = SPAN * sizeof(T) / 16;  // lanes (16-byte chunks) of a routed row's piece
   static constexpr int RPL = kWave / LPR;            // rows of a load
   static constexpr int XL = kRowsX / RPL;            // loads
+  static constexpr int SB = SPAN / kMx4Block;        // scale bytes of a row's piece
   struct Piece {
     uint32_t q[P][Q];
-    uint32_t sc[P][B];
     bool live;  // the wave has this piece (the same in all lanes)
+  };
+  // Scale bytes of four pieces that follow one another: lane l holds those of piece l / 16, row l % 16, so
+  // that a row's come in one load; TAIL: of one piece, byte l / 16
+  struct Scales {
+    uint32_t w[P][NB == 2 ? 2 : 1];
   };
   const W4Args& a;
   int lane, wr, grp;
@@ -192,75 +211,89 @@ struct Stream {
 
   __device__ __forceinline__ void load_codes(Piece& c, const W4Tile& t, int col, int k) const {
     c.live = t.e >= 0 && k < a.K;
-    if (!c.live) return;
-    const int64_t wrow = (int64_t)t.e * a.N + col + wr;
+    const int64_t wrow = (int64_t)(t.e >= 0 ? t.e : 0) * a.N + col;
     const uint8_t* const qs[2] = {a.q0, a.q1};
-    const uint8_t* const ss[2] = {a.s0, a.s1};
+    const uint32_t qb = a.K / 2;  // bytes of a row
 #pragma unroll
     for (int h = 0; h < P; h++) {
-      const uint8_t* q = qs[h] + wrow * (a.K / 2) + k / 2 + at(0) / 2;
-      const uint8_t* s = ss[h] + wrow * (a.K / kMx4Block) + k / kMx4Block;
+      const auto q = buffer(qs[h] + wrow * qb, c.live ? kRowsW * qb : 0);
+      const uint32_t qo = wr * qb + (k + at(0)) / 2;
       if constexpr (NB == 0) {
-        const uint2 v = *reinterpret_cast<const uint2*>(q);
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(q, qo, 0, 0);
         c.q[h][0] = v.x, c.q[h][1] = v.y;
-        c.sc[h][0] = *reinterpret_cast<const uint16_t*>(s) >> (8 * (grp >> 1)) & 255;
       } else {
 #pragma unroll
         for (int b = 0; b < NB; b++) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (!TAIL || k + at(b) < a.K) v = *reinterpret_cast<const uint4*>(q + 64 * b);
+          const u32x4 v =
+              __builtin_amdgcn_raw_buffer_load_b128(q, !TAIL || k + at(0) < a.K ? qo + 64 * b : kNowhere, 0, 0);
           c.q[h][4 * b] = v.x, c.q[h][4 * b + 1] = v.y, c.q[h][4 * b + 2] = v.z, c.q[h][4 * b + 3] = v.w;
-        }
-        if constexpr (TAIL) {  // the row's bytes may end here
-          c.sc[h][0] = k + at(0) < a.K ? s[grp] : 0;
-        } else if constexpr (NB == 1) {
-          c.sc[h][0] = *reinterpret_cast<const uint32_t*>(s) >> (8 * grp) & 255;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(s);
-          c.sc[h][0] = v.x >> (8 * grp) & 255;
-          c.sc[h][1] = v.y >> (8 * grp) & 255;
         }
       }
     }
   }
-
-  // Rows that are not there keep what the register or LDS holds: a row is one column of the product,
-  // and theirs is not stored.  Behind the end of the reduction zeros meet the zero codes.
-  __device__ __forceinline__ void load_rows(uint4 (&x)[XL], const W4Tile& t, int k) const {
-    const int rows = t.m_end - t.m0, chunk = lane % LPR;
-    const T* src = static_cast<const T*>(a.X) + (int64_t)t.m0 * a.K + k + chunk * (16 / (int)sizeof(T));
+  __device__ __forceinline__ void load_scales(Scales& c, const W4Tile& t, int col, int k) const {
+    const int64_t wrow = (int64_t)(t.e >= 0 ? t.e : 0) * a.N + col;
+    const uint8_t* const ss[2] = {a.s0, a.s1};
+    const uint32_t sb = a.K / kMx4Block;
 #pragma unroll
-    for (int i = 0; i < XL; i++) {
-      const int r = i * RPL + lane / LPR;
-      uint4 v = TAIL ? make_uint4(0, 0, 0, 0) : x[i];
-      if (r < rows && (!TAIL || k + chunk * (16 / (int)sizeof(T)) < a.K))
-        v = *reinterpret_cast<const uint4*>(src + (int64_t)r * a.K);
-      x[i] = v;
+    for (int h = 0; h < P; h++) {
+      const auto s = buffer(ss[h] + wrow * sb, t.e >= 0 && k < a.K ? kRowsW * sb : 0);
+      const uint32_t so = wr * sb + k / kMx4Block;
+      if constexpr (TAIL) {
+        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b8(s, k + at(0) < a.K ? so + grp : kNowhere, 0, 0);
+      } else if constexpr (NB == 2) {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(s, so + SB * grp, 0, 0);
+        c.w[h][0] = v.x, c.w[h][1] = v.y;
+      } else if constexpr (NB == 1) {
+        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b32(s, so + SB * grp, 0, 0);
+      } else {
+        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b16(s, so + SB * grp, 0, 0);
+      }
     }
+  }
+  // The scale of projection h's block b of the p-th of the four pieces, as the widening instructions take it
+  __device__ __forceinline__ float scale(const Scales& c, int p, int h, int b) const {
+    if constexpr (TAIL) return mx4_scale(c.w[h][0]);
+    const uint32_t w = __builtin_amdgcn_ds_bpermute(4 * (16 * p + wr), c.w[h][NB == 2 ? b : 0]);
+    return mx4_scale(w >> (8 * (NB ? grp : grp >> 1)) & 255);
+  }
+
+  __device__ __forceinline__ void load_rows(u32x4 (&x)[XL], const W4Tile& t, int k) const {
+    const uint32_t row = a.K * sizeof(T);
+    const uint32_t o = k * sizeof(T) + (lane % LPR) * 16;
+    const auto r = buffer(static_cast<const T*>(a.X) + (int64_t)t.m0 * a.K, t.e >= 0 && k < a.K ? (t.m_end - t.m0) * row : 0);
+#pragma unroll
+    for (int i = 0; i < XL; i++)
+      x[i] = __builtin_amdgcn_raw_buffer_load_b128(r, !TAIL || o < row ? (i * RPL + lane / LPR) * row + o : kNowhere, 0, 0);
   }
   // 16-byte chunks of a row are exchanged by its number: the 8 rows' at one place are on distinct banks
-  __device__ __forceinline__ void hand_over(const uint4 (&x)[XL], uint4 (*s)[LPR], const W4Tile& t) const {
+  __device__ __forceinline__ void hand_over(const u32x4 (&x)[XL], u32x4 (*s)[LPR]) const {
 #pragma unroll
     for (int i = 0; i < XL; i++) {
       const int r = i * RPL + lane / LPR;
-      if (i * RPL < t.m_end - t.m0) s[r][(lane % LPR) ^ r] = x[i];
+      s[r][(lane % LPR) ^ r] = x[i];
     }
   }
 
-  __device__ __forceinline__ void multiply(const Piece& c, const uint4 (*s)[LPR], f32x4 (&acc)[P]) const {
+  __device__ __forceinline__ void multiply(const Piece& c, const Scales& sc, int p, const u32x4 (*s)[LPR],
+                                           f32x4 (&acc)[P]) const {
     const int r = wr % kRowsX;
+    float f[P][B];
+#pragma unroll
+    for (int h = 0; h < P; h++)
+#pragma unroll
+      for (int b = 0; b < B; b++) f[h][b] = scale(sc, p, h, b);
 #pragma unroll
     for (int i = 0; i < Q; i++) {
       if constexpr (sizeof(T) == 2) {
         const bf16x8 x = __builtin_bit_cast(bf16x8, s[r][(16 * (i / 4) + 4 * grp + i % 4) ^ r]);
 #pragma unroll
         for (int h = 0; h < P; h++)
-          acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_bf16(c.q[h][i], mx4_scale(c.sc[h][i / 4])), x, acc[h],
-                                                           0, 0, 0);
+          acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_bf16(c.q[h][i], f[h][i / 4]), x, acc[h], 0, 0, 0);
       } else {
         float w[P][8];
 #pragma unroll
-        for (int h = 0; h < P; h++) widen_f32(c.q[h][i], mx4_scale(c.sc[h][0]), w[h]);
+        for (int h = 0; h < P; h++) widen_f32(c.q[h][i], f[h][0], w[h]);
 #pragma unroll
         for (int u = 0; u < 2; u++) {
           const float4 x = __builtin_bit_cast(float4, s[r][(4 * grp + 2 * i + u) ^ r]);
@@ -280,9 +313,9 @@ template <typename T, int P, int NB, bool TAIL>
 __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args a, int tiles) {
   using S = Stream<T, P, NB, TAIL>;
   constexpr int NW = kStreamWaves, ROWS = kRowsX;
-  __shared__ __attribute__((aligned(16))) uint4 s_x[NW][ROWS][S::LPR];
+  __shared__ __attribute__((aligned(16))) u32x4 s_x[NW][ROWS][S::LPR];
   __shared__ float s_acc[2][NW][P][ROWS][kRowsW + 1];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const S st{a, lane, lane & 15, lane >> 4};
   const int shares = NW / tiles, share = wave % shares, sub = wave / shares;
   const int iters = (a.K + S::SPAN * shares - 1) / (S::SPAN * shares);
@@ -291,26 +324,36 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
   W4Finder<ROWS, false> finder(a.offsets, a.E, a.N / width, lane);
   W4Tile tile = finder.find(t), ahead = tile;  // the tile in hand, and that of the next piece
   if (tile.e < 0) return;
+  constexpr int GROUP = TAIL ? 1 : 4;  // pieces whose scales are loaded at once
+  auto first = [&](int i) { return (share * iters + i) * S::SPAN; };  // element of piece i of a tile
+  auto column = [&](const W4Tile& t) { return t.nt * width + kRowsW * sub; };
   int it = 0, buf = 0;
   f32x4 acc[P] = {};
   typename S::Piece even, odd;
-  uint4 x[S::XL] = {};
-  st.load_codes(even, tile, tile.nt * width + kRowsW * sub, share * S::SPAN);
-  if (even.live) st.load_rows(x, tile, share * S::SPAN);
+  typename S::Scales now, then;  // of the pieces in hand, and of those behind them
+  u32x4 x[S::XL];
+  st.load_scales(now, tile, column(tile), first(0));
+  st.load_rows(x, tile, first(0));
+  st.load_codes(even, tile, column(tile), first(0));
+  then = now;
   // multiplies `cur` while the piece behind it loads into `nxt`; false behind the last tile
   auto step = [&](const typename S::Piece& cur, typename S::Piece& nxt) __attribute__((always_inline)) {
-    if (cur.live) st.hand_over(x, s_x[wave], tile);
+    st.hand_over(x, s_x[wave]);
+    const int at = it % GROUP;
     const bool last = ++it == iters;
     if (last) {
       it = 0;
       t += gridDim.x;
       ahead = finder.find(t);
     }
-    st.load_codes(nxt, ahead, ahead.nt * width + kRowsW * sub, (it * shares + share) * S::SPAN);
-    if (nxt.live) st.load_rows(x, ahead, (it * shares + share) * S::SPAN);
+    const bool group = it % GROUP == 0;
+    if (group) st.load_scales(then, ahead, column(ahead), first(it));
+    st.load_rows(x, ahead, first(it));
+    st.load_codes(nxt, ahead, column(ahead), first(it));
     wave_lds_fence();
-    if (cur.live) st.multiply(cur, s_x[wave], acc);
+    if (cur.live) st.multiply(cur, now, at, s_x[wave], acc);
     wave_lds_fence();
+    if (group) now = then;
     if (!last) return true;
     // lane l holds weight rows 4 (l / 16) .. + 3 of routed row l % 16
 #pragma unroll
@@ -345,11 +388,13 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
 }
 
 // ---- many rows: the rows in LDS, each weight widened once for up to 96 of them
-// A workgroup takes 64 weight rows of both projections (gated) or 128 of one, 2 x 16 a wave, by up to 96
-// routed rows.  256 bytes of every routed row are staged in LDS (16-byte chunks exchanged by the row's
-// number, so that 16 rows at one place fall on distinct banks) while the 256 before are multiplied; rows
-// and weights are loaded into registers two steps ahead.
-constexpr int kTileRows = 96, kTileThreads = 256;
+// A workgroup of NW waves takes 16 NW weight rows of both projections (gated) or 32 NW of one, 2 x 16 a
+// wave, by up to 96 routed rows.  256 bytes of every routed row are staged in LDS (16-byte chunks
+// exchanged by the row's number, so that 16 rows at one place fall on distinct banks) while the 256
+// before are multiplied; rows and weights are loaded into registers two steps ahead.  What bounds it are
+// the bytes that a compute unit loads, weights or rows, from the L2 or from memory (about 24 a
+// nanosecond, at most): launch_w4 picks the NW that loads fewest.
+constexpr int kTileRows = 96;
 
 template <typename T>
 struct Tile4 {
@@ -360,9 +405,8 @@ struct Tile4 {
 
 // A step's products for NTA runs of 16 routed rows
 template <typename T, int NTA>
-__device__ __forceinline__ void multiply_step(const uint4 (*x)[16], const uint32_t (&q)[2][Tile4<T>::Q],
-                                              const uint32_t (&sc)[2], int wr, int grp, f32x4 (&acc)[2][NTA]) {
-  const float s0 = mx4_scale(sc[0]), s1 = mx4_scale(sc[1]);
+__device__ __forceinline__ void multiply_step(const u32x4 (*x)[16], const uint32_t (&q)[2][Tile4<T>::Q], float s0,
+                                              float s1, int wr, int grp, f32x4 (&acc)[2][NTA]) {
 #pragma unroll
   for (int i = 0; i < Tile4<T>::Q; i++) {
     if constexpr (sizeof(T) == 2) {
@@ -395,91 +439,110 @@ __device__ __forceinline__ void multiply_step(const uint4 (*x)[16], const uint32
 }
 
 // One tile with NTA runs of 16 routed rows
-template <typename T, int P, int NTA>
-__device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, uint4 (*s_x)[kTileRows][16]) {
+template <typename T, int P, int NW, bool TAIL, int NTA>
+__device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32x4 (*s_x)[kTileRows][16]) {
   using C = Tile4<T>;
-  constexpr int KC = C::KC, EPL = C::EPL, Q = C::Q, XE = 16 / sizeof(T);
-  constexpr int BN = 128 / P;  // weight rows of a tile (per projection)
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int KC = C::KC, EPL = C::EPL, Q = C::Q;
+  constexpr int BN = 32 * NW / P;                        // weight rows of a tile (per projection)
+  constexpr int XN = (NTA * 256 + 64 * NW - 1) / (64 * NW);  // 16-byte chunks of routed rows a thread loads
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = lane & 15, grp = lane >> 4;
   const int steps = (a.K + KC - 1) / KC;
-  const int xr = tid >> 4, xc = tid & 15;  // this thread's row and 16-byte chunk of every 16 staged rows
+  const int xr = tid >> 4, xc = tid & 15;  // row xr + 4 NW n, chunk xc
   const int rows = tile.m_end - tile.m0;
   // the wave's two sets of 16 weight rows: both projections of the same, or 32 of the one
-  const uint8_t *qp[2], *sp[2];
+  const uint32_t qb = a.K / 2, sb = a.K / kMx4Block, xb = a.K * sizeof(T);  // bytes of a row
+  __amdgpu_buffer_rsrc_t qr[2], sr[2];
   int ncol[2];
 #pragma unroll
   for (int h = 0; h < 2; h++) {
     ncol[h] = tile.nt * BN + (P == 2 ? 16 * wave : 32 * wave + 16 * h);
-    const int n = ncol[h] + wr < a.N ? ncol[h] + wr : a.N - 1;  // past the last: read, not stored
-    const int64_t wrow = (int64_t)tile.e * a.N + n;
-    qp[h] = (P == 2 && h ? a.q1 : a.q0) + wrow * (a.K / 2) + grp * (EPL / 2);
-    sp[h] = (P == 2 && h ? a.s1 : a.s0) + wrow * (a.K / kMx4Block) + grp * EPL / kMx4Block;
+    const int64_t wrow = (int64_t)tile.e * a.N + ncol[h];
+    const bool in = ncol[h] < a.N;  // N is a multiple of 16
+    qr[h] = buffer((P == 2 && h ? a.q1 : a.q0) + wrow * qb, in ? 16 * qb : 0);
+    sr[h] = buffer((P == 2 && h ? a.s1 : a.s0) + wrow * sb, in ? 16 * sb : 0);
   }
-  const T* xp[NTA];
+  const auto rr = buffer(static_cast<const T*>(a.X) + (int64_t)tile.m0 * a.K, rows * xb);
+  constexpr int AHEAD = 3;  // steps that weights are loaded ahead (even + 1: the rows' sets take turns too)
+  u32x4 xs[2][XN];
+  uint32_t q[AHEAD + 1][2][Q];
+  uint32_t sc[TAIL ? AHEAD + 1 : 2][2];  // TAIL: of each step; else of 4 steps, as the lane's of step l / 16
+  // past the reduction's end both sides are zero
+  auto load_x = [&](int step, u32x4(&x)[XN]) __attribute__((always_inline)) {
+    const uint32_t o = step * 256 + xc * 16;
 #pragma unroll
-  for (int n = 0; n < NTA; n++) {
-    const int r = 16 * n + xr < rows ? 16 * n + xr : rows - 1;  // rows past the last repeat it, not stored
-    xp[n] = static_cast<const T*>(a.X) + (int64_t)(tile.m0 + r) * a.K + xc * XE;
-  }
-  uint4 xs[2][NTA];
-  uint32_t q[3][2][Q];  // of this step and the two behind it
-  uint32_t sc[3][2];
-  auto load_x = [&](int step, uint4(&x)[NTA]) __attribute__((always_inline)) {
-    const bool in = step * KC + xc * XE < a.K;
-#pragma unroll
-    for (int n = 0; n < NTA; n++) {
-      x[n] = make_uint4(0, 0, 0, 0);  // past the reduction's end zeros meet zero codes
-      if (in) x[n] = *reinterpret_cast<const uint4*>(xp[n] + step * KC);
-    }
+    for (int n = 0; n < XN; n++)
+      x[n] = __builtin_amdgcn_raw_buffer_load_b128(rr, o < xb ? (xr + 4 * NW * n) * xb + o : kNowhere, 0, 0);
   };
-  auto load_w = [&](int step, uint32_t(&w)[2][Q], uint32_t(&s)[2]) __attribute__((always_inline)) {
-    const int k = step * KC;
-    const bool in = k + grp * EPL < a.K;
+  auto load_w = [&](int step, uint32_t(&w)[2][Q]) __attribute__((always_inline)) {
+    const int k = step * KC + grp * EPL;
+    const uint32_t qo = k < a.K ? wr * qb + k / 2 : kNowhere;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-#pragma unroll
-      for (int i = 0; i < Q; i++) w[h][i] = 0;
-      s[h] = 0;
-      if (in) {
-        if constexpr (Q == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(qp[h] + k / 2);
-          w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(qp[h] + k / 2);
-          w[h][0] = v.x, w[h][1] = v.y;
-        }
-        s[h] = sp[h][k / kMx4Block];
+      if constexpr (Q == 4) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(qr[h], qo, 0, 0);
+        w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
+      } else {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(qr[h], qo, 0, 0);
+        w[h][0] = v.x, w[h][1] = v.y;
       }
     }
+  };
+  // a row's scale bytes of four steps come in one load, a step's to each of its four lanes
+  auto load_s = [&](int step, uint32_t(&s)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      if constexpr (TAIL) {
+        const int k = step * KC + grp * EPL;
+        s[h] = __builtin_amdgcn_raw_buffer_load_b8(sr[h], k < a.K ? wr * sb + k / kMx4Block : kNowhere, 0, 0);
+      } else {
+        constexpr int SB = KC / kMx4Block;
+        const uint32_t o = wr * sb + (step + grp) * SB;
+        if constexpr (SB == 4) s[h] = __builtin_amdgcn_raw_buffer_load_b32(sr[h], o, 0, 0);
+        else s[h] = __builtin_amdgcn_raw_buffer_load_b16(sr[h], o, 0, 0);
+      }
+    }
+  };
+  auto scale = [&](uint32_t s, int v) __attribute__((always_inline)) {
+    if constexpr (TAIL) return mx4_scale(s);
+    const uint32_t w = __builtin_amdgcn_ds_bpermute(4 * (16 * v + wr), s);
+    return mx4_scale(w >> (8 * (grp * EPL / kMx4Block)) & 255);
   };
   auto stage = [&](int buf) __attribute__((always_inline)) {
 #pragma unroll
-    for (int n = 0; n < NTA; n++) s_x[buf][16 * n + xr][xc ^ xr] = xs[buf][n];
+    for (int n = 0; n < XN; n++) {
+      const int r = xr + 4 * NW * n;
+      if (16 * NTA % (4 * NW) == 0 || r < 16 * NTA) s_x[buf][r][xc ^ (r & 15)] = xs[buf][n];
+    }
   };
   f32x4 acc[2][NTA] = {};
   load_x(0, xs[0]);
-  load_w(0, q[0], sc[0]);
+#pragma unroll
+  for (int v = 0; v < AHEAD; v++) load_w(v, q[v]);
+  load_s(0, sc[0]);
+  if constexpr (TAIL) {
+    load_s(1, sc[1]);
+    load_s(2, sc[2]);
+  }
   load_x(1, xs[1]);
-  load_w(1, q[1], sc[1]);
   stage(0);
   __syncthreads();
-  for (int step = 0; step < steps; step += 2) {
+  constexpr int N = AHEAD + 1;
+  static_assert(N == 4, "steps whose scales come together");
+  for (int step = 0; step < steps;) {
+    // a register set is loaded again the step after its use: no set is copied, which would wait for it
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
-      if (step + u < steps) {
-        load_x(step + u + 2, xs[u]);
-        load_w(step + u + 2, q[2], sc[2]);
-        multiply_step<T, NTA>(s_x[u], q[0], sc[0], wr, grp, acc);
-        stage(u ^ 1);
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-#pragma unroll
-          for (int i = 0; i < Q; i++) q[0][h][i] = q[1][h][i], q[1][h][i] = q[2][h][i];
-          sc[0][h] = sc[1][h], sc[1][h] = sc[2][h];
-        }
-      }
+    for (int v = 0; v < 2 * N; v++) {
+      load_x(step + 2, xs[v & 1]);
+      load_w(step + AHEAD, q[(v + AHEAD) % N]);
+      if constexpr (TAIL) load_s(step + AHEAD, sc[(v + AHEAD) % N]);
+      else if (v % N == 0) load_s(step + N, sc[v / N ^ 1]);
+      __builtin_amdgcn_sched_barrier(0);  // the loads go first
+      const uint32_t(&s)[2] = sc[TAIL ? v % N : v / N];
+      multiply_step<T, NTA>(s_x[v & 1], q[v % N], scale(s[0], v % N), scale(s[1], v % N), wr, grp, acc);
+      stage((v & 1) ^ 1);
+      __syncthreads();
+      if (++step == steps) break;
     }
   }
 #pragma unroll
@@ -508,20 +571,21 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, uin
   }
 }
 
-template <typename T, int P>
-__global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(W4Args a) {
-  __shared__ __attribute__((aligned(16))) uint4 s_x[2][kTileRows][16];
-  W4Finder<kTileRows, true> finder(a.offsets, a.E, (a.N * P + 127) / 128, threadIdx.x & 63);
+template <typename T, int P, int NW, bool TAIL>
+__global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : NW / 4) w4_tile_kernel(W4Args a) {
+  constexpr int BN = 32 * NW / P;
+  __shared__ __attribute__((aligned(16))) u32x4 s_x[2][kTileRows][16];
+  W4Finder<kTileRows, true> finder(a.offsets, a.E, (a.N + BN - 1) / BN, threadIdx.x & 63);
   for (int t = first_tile();; t += gridDim.x) {
     const W4Tile tile = finder.find(t);
     if (tile.e < 0) break;
     switch ((tile.m_end - tile.m0 + 15) / 16) {
-      case 1: do_tile<T, P, 1>(a, tile, s_x); break;
-      case 2: do_tile<T, P, 2>(a, tile, s_x); break;
-      case 3: do_tile<T, P, 3>(a, tile, s_x); break;
-      case 4: do_tile<T, P, 4>(a, tile, s_x); break;
-      case 5: do_tile<T, P, 5>(a, tile, s_x); break;
-      default: do_tile<T, P, 6>(a, tile, s_x);
+      case 1: do_tile<T, P, NW, TAIL, 1>(a, tile, s_x); break;
+      case 2: do_tile<T, P, NW, TAIL, 2>(a, tile, s_x); break;
+      case 3: do_tile<T, P, NW, TAIL, 3>(a, tile, s_x); break;
+      case 4: do_tile<T, P, NW, TAIL, 4>(a, tile, s_x); break;
+      case 5: do_tile<T, P, NW, TAIL, 5>(a, tile, s_x); break;
+      default: do_tile<T, P, NW, TAIL, 6>(a, tile, s_x);
     }
   }
 }
@@ -541,14 +605,36 @@ hipError_t launch_stream(const W4Args& p, int tiles, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <typename T, int P, int NW, bool TAIL>
+hipError_t launch_tile(const W4Args& p, hipStream_t st) {
+  constexpr int BN = 32 * NW / P;
+  hipLaunchKernelGGL((w4_tile_kernel<T, P, NW, TAIL>), dim3(w4_grid<kTileRows>(p, (p.N + BN - 1) / BN, 64)),
+                     dim3(64 * NW), 0, st, p);
+  return hipGetLastError();
+}
+
+// Bytes that the busiest compute unit loads with tiles of NW waves, for rows spread evenly
+template <int P>
+int64_t tile_bytes(const W4Args& p, int nw) {
+  const int64_t bn = 32 * nw / P, experts = p.R < p.E ? p.R : p.E, rows = (p.R + experts - 1) / experts;
+  const int64_t runs = (rows + kTileRows - 1) / kTileRows;
+  const int64_t tiles = experts * runs * ((p.N + bn - 1) / bn);
+  const int64_t cus = device_cu_count();
+  return (tiles + cus - 1) / cus * (rows / runs * p.K * 2 + bn * P * p.K * 17 / 32);
+}
+
 template <typename T, int P>
 hipError_t launch_w4(const W4Args& p, hipStream_t st) {
   if (p.R == 0) return hipSuccess;
-  if (p.R > (int64_t)p.E * kStreamMaxRows) {
-    constexpr int BN = 128 / P;
-    hipLaunchKernelGGL((w4_tile_kernel<T, P>), dim3(w4_grid<kTileRows>(p, (p.N + BN - 1) / BN, 64)), dim3(kTileThreads),
-                       0, st, p);
-    return hipGetLastError();
+  if (p.R > (int64_t)p.E * (sizeof(T) == 2 ? kStreamMaxRows16 : kStreamMaxRows32)) {
+    if constexpr (sizeof(T) == 2) {
+      if (p.K % 128 != 0) return launch_tile<T, P, 4, true>(p, st);
+      // 12 waves read the rows a third as often: 88 -> 67 us at 64 rows an expert (E = 32, K = 4096, N = 1536,
+      // gated; the estimate falls to 0.55), 55.5 -> 52 at 16 (0.79); 45 -> 52 where it does not fall (32
+      // rows, E = 64, K = 2048, N = 1024: 1.02)
+      if (4 * tile_bytes<P>(p, 12) < 3 * tile_bytes<P>(p, 4)) return launch_tile<T, P, 12, false>(p, st);
+    }
+    return launch_tile<T, P, 4, false>(p, st);
   }
   // four tiles a workgroup, two shares of the reduction each, where that leaves every compute unit four
   // workgroups; else fewer tiles and more shares
