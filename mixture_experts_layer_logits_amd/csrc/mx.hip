@@ -963,7 +963,8 @@ static hipError_t launch_mx(const Prob& p, hipStream_t st) {
 // ordered on the stream.
 // ---------------------------------------------------------------------------------------
 static size_t al(size_t b) { return (b + 255) / 256 * 256; }
-static size_t qbytes(int64_t rows, int64_t K) { return al((size_t)(rows * K)) + al((size_t)(rows * (K / kMxBlock))); }
+// the two regions of one operand, as Carve takes them (K need not be a multiple of the block)
+static size_t qbytes(int64_t rows, int64_t K) { return al((size_t)(rows * K)) + al((size_t)(rows * K / kMxBlock)); }
 
 size_t mx_workspace_bytes(int R, int d, int f, int E) {
   const int64_t Rp = (int64_t)R + (int64_t)kMxSegPad * E;
