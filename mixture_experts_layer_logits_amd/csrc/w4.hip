@@ -9,6 +9,8 @@
 // two elements an instruction) and the bf16 matrix cores multiply them with the unquantised rows,
 // summing in fp32: the only roundings are the sums' and the one of each output.  fp32 rows take the
 // fp32 matrix cores in the same way.
+#include <type_traits>
+
 #include "lanes.h"
 #include "tilemap.h"
 #include "w4.h"
@@ -116,8 +118,8 @@ __device__ __forceinline__ int wave_scan(int v) {
 
 // The tiles of a launch: an expert's rows in runs of at most ROWS (even shares of whole 16s where EVEN),
 // its weight rows in ntn tiles; the runs that share a weight tile follow one another.  Every wave finds
-// its tiles by itself, so no barrier stands before the first load: a lane holds one expert of a window
-// of 64, whose run counts are scanned in registers, and as tiles are asked for in ascending order the
+// its tiles by itself, so no barrier stands before the first load: a lane holds two experts of a window
+// of 128, whose run counts are scanned in registers, and as tiles are asked for in ascending order the
 // window only moves forward.
 struct W4Tile {
   int e, m0, m_end, nt;  // e < 0: past the last tile
@@ -125,13 +127,15 @@ struct W4Tile {
 template <int ROWS, bool EVEN>
 struct W4Finder {
   const int* offsets;
-  int E, ntn, lane, e0, lo, hi, runs, incl;
+  int E, ntn, lane, e0, at[3], incl;  // at: where the lane's experts e0 + 2 lane, + 1 begin, and the next
+  static __device__ __forceinline__ int runs(int rows) { return (rows + ROWS - 1) / ROWS; }
   __device__ __forceinline__ void window(int before) {
-    const int e = e0 + lane;
-    lo = e < E ? offsets[e] : 0;
-    hi = e < E ? offsets[e + 1] : 0;
-    runs = (hi - lo + ROWS - 1) / ROWS;
-    incl = before + wave_scan(runs);
+#pragma unroll
+    for (int i = 0; i < 3; i++) {
+      const int e = e0 + 2 * lane + i;
+      at[i] = offsets[e < E ? e : E];
+    }
+    incl = before + wave_scan(runs(at[1] - at[0]) + runs(at[2] - at[1]));
   }
   __device__ __forceinline__ W4Finder(const int* off, int E_, int ntn_, int lane_)
       : offsets(off), E(E_), ntn(ntn_), lane(lane_), e0(0) {
@@ -139,18 +143,23 @@ struct W4Finder {
   }
   __device__ __forceinline__ W4Tile find(int t) {
     while (true) {
-      const uint64_t hit = __ballot(t >= (incl - runs) * ntn && t < incl * ntn);
+      const int mine = runs(at[1] - at[0]) + runs(at[2] - at[1]);
+      const uint64_t hit = __ballot(t >= (incl - mine) * ntn && t < incl * ntn);
       if (hit) {
         const int l = __builtin_ctzll(hit);
-        const int me = __builtin_amdgcn_readlane(runs, l), end = __builtin_amdgcn_readlane(hi, l);
-        const int start = __builtin_amdgcn_readlane(lo, l);
-        const int local = t - (__builtin_amdgcn_readlane(incl, l) - me) * ntn;
+        const int a0 = __builtin_amdgcn_readlane(at[0], l), a1 = __builtin_amdgcn_readlane(at[1], l),
+                  a2 = __builtin_amdgcn_readlane(at[2], l);
+        const int r0 = runs(a1 - a0), r1 = runs(a2 - a1);
+        int local = t - (__builtin_amdgcn_readlane(incl, l) - r0 - r1) * ntn;
+        const bool second = local >= r0 * ntn;
+        if (second) local -= r0 * ntn;
+        const int me = second ? r1 : r0, start = second ? a1 : a0, end = second ? a2 : a1;
         const int nt = me == 1 ? local : local / me;
         const int per = EVEN && me > 1 ? ((end - start + 15) / 16 + me - 1) / me * 16 : ROWS;
         const int m0 = start + (local - nt * me) * per;
-        return W4Tile{e0 + l, m0, m0 + per < end ? m0 + per : end, nt};
+        return W4Tile{e0 + 2 * l + (second ? 1 : 0), m0, m0 + per < end ? m0 + per : end, nt};
       }
-      e0 += kWave;
+      e0 += 2 * kWave;
       if (e0 >= E) return W4Tile{-1, 0, 0, 0};
       window(__builtin_amdgcn_readlane(incl, kWave - 1));
     }
@@ -177,10 +186,11 @@ __device__ __forceinline__ int first_tile() {
 // handed to the lanes through LDS of the wave's own.
 constexpr int kStreamWaves = 8;
 // Rows an expert, on average, up to which the weights stream; above, the tiles of many rows are faster
-// (us, stream / tiles).  bf16: 4 rows 29.5 / 34.5, 6 rows 34.5 / 34.4, 12 rows 50 / 38 (E = 64, d = 2048, f
-// = 1024, gated); 4 rows 45 / 50, 8 rows 61 / 51 (E = 32, d = 4096, f = 1536).  fp32, whose products take
-// most of the time: 8 rows 13.1 / 14.6, 16 rows 21.4 / 22.8, 24 rows 27.4 / 23.0 (E = 8, K = 1024, N = 2048)
-constexpr int kStreamMaxRows16 = 5, kStreamMaxRows32 = 16;
+// (us, stream / tiles).  4 rows 29.5 / 34.5, 6 rows 34.5 / 34.4, 12 rows 50 / 38 (bf16, E = 64, d = 2048, f
+// = 1024, gated); 4 rows 65 / 81, 8 rows 95 / 82 (the same in fp32).  fp32 tiles, whose products take most of
+// the time, need one for every compute unit: else 8 rows 11.9 / 15.1, 32 rows 30.5 / 31.4, 48 rows 43.5 /
+// 39.7 (E = 8, K = 1024, N = 2048)
+constexpr int kStreamMaxRows = 5, kStreamMaxRowsFew = 32;
 constexpr int kRowsW = 16;          // weight rows of a tile
 constexpr int kRowsX = 8;           // routed rows of a tile
 
@@ -275,8 +285,13 @@ struct Stream {
     }
   }
 
-  __device__ __forceinline__ void multiply(const Piece& c, const Scales& sc, int p, const u32x4 (*s)[LPR],
-                                           f32x4 (&acc)[P]) const {
+  // fp32: 4 x 4 products of one element, 16 at a time, a lane's with four weight rows' and the four routed
+  // rows of set g, so that no column of the product stands empty; the four sixteenths of the wave with one
+  // set of weight rows hold parts of the reduction, added at the end.  8 rows an expert: 13.1 us with 16 x
+  // 16 products, 11.9 with these (E = 8, K = 1024, N = 2048).
+  static constexpr int SETS = sizeof(T) == 4 ? kRowsX / 4 : 1;
+  __device__ __forceinline__ void multiply(const Piece& c, const Scales& sc, int p, const u32x4 (*s)[LPR], int rows,
+                                           f32x4 (&acc)[P][SETS]) const {
     const int r = wr % kRowsX;
     float f[P][B];
 #pragma unroll
@@ -289,20 +304,26 @@ struct Stream {
         const bf16x8 x = __builtin_bit_cast(bf16x8, s[r][(16 * (i / 4) + 4 * grp + i % 4) ^ r]);
 #pragma unroll
         for (int h = 0; h < P; h++)
-          acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_bf16(c.q[h][i], f[h][i / 4]), x, acc[h], 0, 0, 0);
+          acc[h][0] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_bf16(c.q[h][i], f[h][i / 4]), x, acc[h][0], 0, 0, 0);
       } else {
         float w[P][8];
 #pragma unroll
         for (int h = 0; h < P; h++) widen_f32(c.q[h][i], f[h][0], w[h]);
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-          const float4 x = __builtin_bit_cast(float4, s[r][(4 * grp + 2 * i + u) ^ r]);
-          const float xv[4] = {x.x, x.y, x.z, x.w};
+        for (int g = 0; g < SETS; g++) {
+          if (g > 0 && rows <= 4 * g) break;
+          const int rg = 4 * g + lane % 4;
 #pragma unroll
-          for (int j = 0; j < 4; j++)
+          for (int u = 0; u < 2; u++) {
+            const float4 x = __builtin_bit_cast(float4, s[rg][(4 * grp + 2 * i + u) ^ rg]);
+            const float xv[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int h = 0; h < P; h++)
-              acc[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[h][4 * u + j], xv[j], acc[h], 0, 0, 0);
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+              for (int h = 0; h < P; h++)
+                acc[h][g] = __builtin_amdgcn_mfma_f32_4x4x1f32(w[h][4 * u + j], xv[j], acc[h][g], 0, 0, 0);
+          }
         }
       }
     }
@@ -328,7 +349,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
   auto first = [&](int i) { return (share * iters + i) * S::SPAN; };  // element of piece i of a tile
   auto column = [&](const W4Tile& t) { return t.nt * width + kRowsW * sub; };
   int it = 0, buf = 0;
-  f32x4 acc[P] = {};
+  f32x4 acc[P][S::SETS] = {};
   typename S::Piece even, odd;
   typename S::Scales now, then;  // of the pieces in hand, and of those behind them
   u32x4 x[S::XL];
@@ -351,18 +372,32 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
     st.load_rows(x, ahead, first(it));
     st.load_codes(nxt, ahead, column(ahead), first(it));
     wave_lds_fence();
-    if (cur.live) st.multiply(cur, now, at, s_x[wave], acc);
+    if (cur.live) st.multiply(cur, now, at, s_x[wave], tile.m_end - tile.m0, acc);
     wave_lds_fence();
     if (group) now = then;
     if (!last) return true;
-    // lane l holds weight rows 4 (l / 16) .. + 3 of routed row l % 16
 #pragma unroll
     for (int h = 0; h < P; h++) {
-      if (st.wr < ROWS) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) s_acc[buf][wave][h][st.wr][4 * st.grp + i] = acc[h][i];
+      for (int g = 0; g < S::SETS; g++) {
+        f32x4& v = acc[h][g];
+        if constexpr (sizeof(T) == 2) {
+          // lane l holds weight rows 4 (l / 16) .. + 3 of routed row l % 16
+          if (st.wr < ROWS) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) s_acc[buf][wave][h][st.wr][4 * st.grp + i] = v[i];
+          }
+        } else {
+          // lane l holds weight rows 4 (l / 4 % 4) .. + 3 of routed row 4 g + l % 4, a quarter of the sum
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const float half = v[i] + other_half<16>(v[i]);
+            const float sum = half + other_half<32>(half);
+            if (lane < 16) s_acc[buf][wave][h][4 * g + lane % 4][4 * (lane / 4) + i] = sum;
+          }
+        }
+        v = f32x4{0.f, 0.f, 0.f, 0.f};
       }
-      acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     __syncthreads();
     const int rows = tile.m_end - tile.m0;  // at most ROWS
@@ -372,8 +407,18 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
       float v[P];
 #pragma unroll
       for (int h = 0; h < P; h++) {
-        v[h] = s_acc[buf][w0][h][r][c % kRowsW];
-        for (int w = 1; w < shares; w++) v[h] += s_acc[buf][w0 + w][h][r][c % kRowsW];
+        auto add = [&](auto n) {  // n shares, read at once and added in order
+          float part[decltype(n)::value];
+#pragma unroll
+          for (int w = 0; w < n; w++) part[w] = s_acc[buf][w0 + w][h][r][c % kRowsW];
+          float sum = part[0];
+#pragma unroll
+          for (int w = 1; w < n; w++) sum += part[w];
+          return sum;
+        };
+        v[h] = shares == 8   ? add(std::integral_constant<int, 8>())
+               : shares == 4 ? add(std::integral_constant<int, 4>())
+                             : add(std::integral_constant<int, 2>());
       }
       float out = v[0];
       if constexpr (P == 2) out = v[0] * sigmoidf_(v[0]) * v[1];
@@ -439,15 +484,17 @@ __device__ __forceinline__ void multiply_step(const u32x4 (*x)[16], const uint32
 }
 
 // One tile with NTA runs of 16 routed rows
-template <typename T, int P, int NW, bool TAIL, int NTA>
-__device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32x4 (*s_x)[kTileRows][16]) {
+template <typename T, int P, int NW, int KS, bool TAIL, int NTA>
+__device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32x4 (*s_all)[2][kTileRows][16]) {
   using C = Tile4<T>;
   constexpr int KC = C::KC, EPL = C::EPL, Q = C::Q;
   constexpr int BN = 32 * NW / P;                        // weight rows of a tile (per projection)
   constexpr int XN = (NTA * 256 + 64 * NW - 1) / (64 * NW);  // 16-byte chunks of routed rows a thread loads
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x % (64 * NW), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int share = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * NW));
+  u32x4(*s_x)[kTileRows][16] = s_all[share];
   const int wr = lane & 15, grp = lane >> 4;
-  const int steps = (a.K + KC - 1) / KC;
+  const int steps = (a.K + KC * KS - 1) / (KC * KS);  // of this share: KS i + share
   const int xr = tid >> 4, xc = tid & 15;  // row xr + 4 NW n, chunk xc
   const int rows = tile.m_end - tile.m0;
   // the wave's two sets of 16 weight rows: both projections of the same, or 32 of the one
@@ -469,13 +516,13 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
   uint32_t sc[TAIL ? AHEAD + 1 : 2][2];  // TAIL: of each step; else of 4 steps, as the lane's of step l / 16
   // past the reduction's end both sides are zero
   auto load_x = [&](int step, u32x4(&x)[XN]) __attribute__((always_inline)) {
-    const uint32_t o = step * 256 + xc * 16;
+    const uint32_t o = (step * KS + share) * 256 + xc * 16;
 #pragma unroll
     for (int n = 0; n < XN; n++)
       x[n] = __builtin_amdgcn_raw_buffer_load_b128(rr, o < xb ? (xr + 4 * NW * n) * xb + o : kNowhere, 0, 0);
   };
   auto load_w = [&](int step, uint32_t(&w)[2][Q]) __attribute__((always_inline)) {
-    const int k = step * KC + grp * EPL;
+    const int k = (step * KS + share) * KC + grp * EPL;
     const uint32_t qo = k < a.K ? wr * qb + k / 2 : kNowhere;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
@@ -493,11 +540,11 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
 #pragma unroll
     for (int h = 0; h < 2; h++) {
       if constexpr (TAIL) {
-        const int k = step * KC + grp * EPL;
+        const int k = (step * KS + share) * KC + grp * EPL;
         s[h] = __builtin_amdgcn_raw_buffer_load_b8(sr[h], k < a.K ? wr * sb + k / kMx4Block : kNowhere, 0, 0);
       } else {
         constexpr int SB = KC / kMx4Block;
-        const uint32_t o = wr * sb + (step + grp) * SB;
+        const uint32_t o = wr * sb + ((step + grp) * KS + share) * SB;
         if constexpr (SB == 4) s[h] = __builtin_amdgcn_raw_buffer_load_b32(sr[h], o, 0, 0);
         else s[h] = __builtin_amdgcn_raw_buffer_load_b16(sr[h], o, 0, 0);
       }
@@ -545,6 +592,24 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
       if (++step == steps) break;
     }
   }
+  if constexpr (KS == 2) {  // the second share's sums go through the LDS of both
+    f32x4* s_sum = reinterpret_cast<f32x4*>(s_all);
+    if (share == 1) {
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int n = 0; n < NTA; n++) s_sum[(h * NTA + n) * 64 * NW + tid] = acc[h][n];
+    }
+    __syncthreads();
+    if (share == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int n = 0; n < NTA; n++) acc[h][n] += s_sum[(h * NTA + n) * 64 * NW + tid];
+    }
+    __syncthreads();  // the next tile's rows go there
+    if (share == 1) return;
+  }
 #pragma unroll
   for (int n = 0; n < NTA; n++) {
     const int r = 16 * n + wr;
@@ -571,21 +636,21 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
   }
 }
 
-template <typename T, int P, int NW, bool TAIL>
-__global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 : NW / 4) w4_tile_kernel(W4Args a) {
+template <typename T, int P, int NW, int KS, bool TAIL>
+__global__ void __launch_bounds__(64 * NW * KS, NW == 12 ? 3 : 2) w4_tile_kernel(W4Args a) {
   constexpr int BN = 32 * NW / P;
-  __shared__ __attribute__((aligned(16))) u32x4 s_x[2][kTileRows][16];
+  __shared__ __attribute__((aligned(16))) u32x4 s_x[KS][2][kTileRows][16];
   W4Finder<kTileRows, true> finder(a.offsets, a.E, (a.N + BN - 1) / BN, threadIdx.x & 63);
   for (int t = first_tile();; t += gridDim.x) {
     const W4Tile tile = finder.find(t);
     if (tile.e < 0) break;
     switch ((tile.m_end - tile.m0 + 15) / 16) {
-      case 1: do_tile<T, P, NW, TAIL, 1>(a, tile, s_x); break;
-      case 2: do_tile<T, P, NW, TAIL, 2>(a, tile, s_x); break;
-      case 3: do_tile<T, P, NW, TAIL, 3>(a, tile, s_x); break;
-      case 4: do_tile<T, P, NW, TAIL, 4>(a, tile, s_x); break;
-      case 5: do_tile<T, P, NW, TAIL, 5>(a, tile, s_x); break;
-      default: do_tile<T, P, NW, TAIL, 6>(a, tile, s_x);
+      case 1: do_tile<T, P, NW, KS, TAIL, 1>(a, tile, s_x); break;
+      case 2: do_tile<T, P, NW, KS, TAIL, 2>(a, tile, s_x); break;
+      case 3: do_tile<T, P, NW, KS, TAIL, 3>(a, tile, s_x); break;
+      case 4: do_tile<T, P, NW, KS, TAIL, 4>(a, tile, s_x); break;
+      case 5: do_tile<T, P, NW, KS, TAIL, 5>(a, tile, s_x); break;
+      default: do_tile<T, P, NW, KS, TAIL, 6>(a, tile, s_x);
     }
   }
 }
@@ -605,41 +670,47 @@ hipError_t launch_stream(const W4Args& p, int tiles, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, int P, int NW, bool TAIL>
+template <typename T, int P, int NW, int KS, bool TAIL>
 hipError_t launch_tile(const W4Args& p, hipStream_t st) {
   constexpr int BN = 32 * NW / P;
-  hipLaunchKernelGGL((w4_tile_kernel<T, P, NW, TAIL>), dim3(w4_grid<kTileRows>(p, (p.N + BN - 1) / BN, 64)),
-                     dim3(64 * NW), 0, st, p);
+  hipLaunchKernelGGL((w4_tile_kernel<T, P, NW, KS, TAIL>), dim3(w4_grid<kTileRows>(p, (p.N + BN - 1) / BN, 64)),
+                     dim3(64 * NW * KS), 0, st, p);
   return hipGetLastError();
 }
 
-// Bytes that the busiest compute unit loads with tiles of NW waves, for rows spread evenly
+// Tiles of NW waves, for rows spread evenly, and the bytes that the busiest compute unit loads for them
+struct TileWork {
+  int64_t tiles, bytes;
+};
 template <int P>
-int64_t tile_bytes(const W4Args& p, int nw) {
+TileWork tile_work(const W4Args& p, int nw) {
   const int64_t bn = 32 * nw / P, experts = p.R < p.E ? p.R : p.E, rows = (p.R + experts - 1) / experts;
   const int64_t runs = (rows + kTileRows - 1) / kTileRows;
   const int64_t tiles = experts * runs * ((p.N + bn - 1) / bn);
   const int64_t cus = device_cu_count();
-  return (tiles + cus - 1) / cus * (rows / runs * p.K * 2 + bn * P * p.K * 17 / 32);
+  return {tiles, (tiles + cus - 1) / cus * (rows / runs * p.K * 2 + bn * P * p.K * 17 / 32)};
 }
 
 template <typename T, int P>
 hipError_t launch_w4(const W4Args& p, hipStream_t st) {
   if (p.R == 0) return hipSuccess;
-  if (p.R > (int64_t)p.E * (sizeof(T) == 2 ? kStreamMaxRows16 : kStreamMaxRows32)) {
+  const int64_t cus = device_cu_count();
+  const TileWork four = tile_work<P>(p, 4);
+  const bool few = sizeof(T) == 4 && four.tiles < cus;
+  if (p.R > (int64_t)p.E * (few ? kStreamMaxRowsFew : kStreamMaxRows)) {
     if constexpr (sizeof(T) == 2) {
-      if (p.K % 128 != 0) return launch_tile<T, P, 4, true>(p, st);
+      if (p.K % 128 != 0) return launch_tile<T, P, 4, 1, true>(p, st);
       // 12 waves read the rows a third as often: 88 -> 67 us at 64 rows an expert (E = 32, K = 4096, N = 1536,
       // gated; the estimate falls to 0.55), 55.5 -> 52 at 16 (0.79); 45 -> 52 where it does not fall (32
       // rows, E = 64, K = 2048, N = 1024: 1.02)
-      if (4 * tile_bytes<P>(p, 12) < 3 * tile_bytes<P>(p, 4)) return launch_tile<T, P, 12, false>(p, st);
+      if (4 * tile_work<P>(p, 12).bytes < 3 * four.bytes) return launch_tile<T, P, 12, 1, false>(p, st);
     }
-    return launch_tile<T, P, 4, false>(p, st);
+    if (four.tiles <= cus) return launch_tile<T, P, 4, 2, false>(p, st);
+    return launch_tile<T, P, 4, 1, false>(p, st);
   }
   // four tiles a workgroup, two shares of the reduction each, where that leaves every compute unit four
   // workgroups; else fewer tiles and more shares
   const int64_t all = (int64_t)(p.R < p.E ? p.R : p.E) * (p.N / kRowsW);
-  const int64_t cus = device_cu_count();
   const int tiles = all >= 16 * cus ? 4 : all >= 4 * cus ? 2 : 1;
   if constexpr (sizeof(T) == 4) return launch_stream<T, P, 0, false>(p, tiles, st);
   else if (p.K % 128 != 0) return launch_stream<T, P, 1, true>(p, tiles, st);
