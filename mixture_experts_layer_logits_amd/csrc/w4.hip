@@ -178,8 +178,8 @@ __device__ __forceinline__ int first_tile() {
 // A tile is 16 weight rows by up to 8 routed rows of one expert.  The weights are the matrix product's
 // left operand, the routed rows its right: lane l holds elements of weight row l % 16 and of routed row
 // l % 8 (the upper half of the columns is computed twice), the same ones of the reduction, and which
-// they are is free.  bf16: NB blocks of 32 at 128 apart, block l / 16 of each 128, so that the four lanes
-// of a row read 64 bytes of codes side by side; fp32: 16 of each 64.  The 8 waves of a workgroup are
+// they are is free: NB blocks of 32 at 128 apart, block l / 16 of each 128, so that the four lanes of a
+// row read 64 bytes of codes side by side.  The 8 waves of a workgroup are
 // `tiles` neighbouring tiles by 8 / tiles shares of the reduction, taken piece by piece; the shares' sums
 // are added through LDS in order.  Each wave loads its next piece, of this tile or the next, before it
 // multiplies the one it has; the routed rows' part comes in whole rows (a load for two of them) and is
@@ -194,12 +194,11 @@ constexpr int kStreamMaxRows = 5, kStreamMaxRowsFew = 32;
 constexpr int kRowsW = 16;          // weight rows of a tile
 constexpr int kRowsX = 8;           // routed rows of a tile
 
-// NB: blocks of a lane's piece; 0: half a block (fp32 rows).  TAIL: the last piece may end inside.
+// NB: blocks of a lane's piece (1 or 2).  TAIL: the last piece may end inside (NB = 1).
 template <typename T, int P, int NB, bool TAIL>
 struct Stream {
-  static constexpr int B = NB ? NB : 1;            // blocks touched
-  static constexpr int Q = NB ? 4 * NB : 2;        // code words
-  static constexpr int SPAN = NB ? 128 * NB : 64;  // elements of the reduction a wave takes at a time
+  static constexpr int Q = 4 * NB;       // code words
+  static constexpr int SPAN = 128 * NB;  // elements of the reduction a wave takes at a time
   static constexpr int LPR = SPAN * sizeof(T) / 16;  // lanes (16-byte chunks) of a routed row's piece
   static constexpr int RPL = kWave / LPR;            // rows of a load
   static constexpr int XL = kRowsX / RPL;            // loads
@@ -211,13 +210,10 @@ struct Stream {
   // Scale bytes of four pieces that follow one another: lane l holds those of piece l / 16, row l % 16, so
   // that a row's come in one load; TAIL: of one piece, byte l / 16
   struct Scales {
-    uint32_t w[P][NB == 2 ? 2 : 1];
+    uint32_t w[P][NB];
   };
   const W4Args& a;
   int lane, wr, grp;
-
-  // element k + at(b) is the lane's first of block b of the piece that begins at k
-  __device__ __forceinline__ int at(int b) const { return NB ? 128 * b + 32 * grp : 16 * grp; }
 
   __device__ __forceinline__ void load_codes(Piece& c, const W4Tile& t, int col, int k) const {
     c.live = t.e >= 0 && k < a.K;
@@ -227,17 +223,11 @@ struct Stream {
 #pragma unroll
     for (int h = 0; h < P; h++) {
       const auto q = buffer(qs[h] + wrow * qb, c.live ? kRowsW * qb : 0);
-      const uint32_t qo = wr * qb + (k + at(0)) / 2;
-      if constexpr (NB == 0) {
-        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(q, qo, 0, 0);
-        c.q[h][0] = v.x, c.q[h][1] = v.y;
-      } else {
+      const uint32_t qo = !TAIL || k + 32 * grp < a.K ? wr * qb + (k + 32 * grp) / 2 : kNowhere;
 #pragma unroll
-        for (int b = 0; b < NB; b++) {
-          const u32x4 v =
-              __builtin_amdgcn_raw_buffer_load_b128(q, !TAIL || k + at(0) < a.K ? qo + 64 * b : kNowhere, 0, 0);
-          c.q[h][4 * b] = v.x, c.q[h][4 * b + 1] = v.y, c.q[h][4 * b + 2] = v.z, c.q[h][4 * b + 3] = v.w;
-        }
+      for (int b = 0; b < NB; b++) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(q, qo + 64 * b, 0, 0);
+        c.q[h][4 * b] = v.x, c.q[h][4 * b + 1] = v.y, c.q[h][4 * b + 2] = v.z, c.q[h][4 * b + 3] = v.w;
       }
     }
   }
@@ -250,22 +240,20 @@ struct Stream {
       const auto s = buffer(ss[h] + wrow * sb, t.e >= 0 && k < a.K ? kRowsW * sb : 0);
       const uint32_t so = wr * sb + k / kMx4Block;
       if constexpr (TAIL) {
-        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b8(s, k + at(0) < a.K ? so + grp : kNowhere, 0, 0);
+        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b8(s, k + 32 * grp < a.K ? so + grp : kNowhere, 0, 0);
       } else if constexpr (NB == 2) {
         const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(s, so + SB * grp, 0, 0);
         c.w[h][0] = v.x, c.w[h][1] = v.y;
-      } else if constexpr (NB == 1) {
-        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b32(s, so + SB * grp, 0, 0);
       } else {
-        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b16(s, so + SB * grp, 0, 0);
+        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b32(s, so + SB * grp, 0, 0);
       }
     }
   }
   // The scale of projection h's block b of the p-th of the four pieces, as the widening instructions take it
   __device__ __forceinline__ float scale(const Scales& c, int p, int h, int b) const {
     if constexpr (TAIL) return mx4_scale(c.w[h][0]);
-    const uint32_t w = __builtin_amdgcn_ds_bpermute(4 * (16 * p + wr), c.w[h][NB == 2 ? b : 0]);
-    return mx4_scale(w >> (8 * (NB ? grp : grp >> 1)) & 255);
+    const uint32_t w = __builtin_amdgcn_ds_bpermute(4 * (16 * p + wr), c.w[h][b]);
+    return mx4_scale(w >> (8 * grp) & 255);
   }
 
   __device__ __forceinline__ void load_rows(u32x4 (&x)[XL], const W4Tile& t, int k) const {
@@ -293,11 +281,11 @@ struct Stream {
   __device__ __forceinline__ void multiply(const Piece& c, const Scales& sc, int p, const u32x4 (*s)[LPR], int rows,
                                            f32x4 (&acc)[P][SETS]) const {
     const int r = wr % kRowsX;
-    float f[P][B];
+    float f[P][NB];
 #pragma unroll
     for (int h = 0; h < P; h++)
 #pragma unroll
-      for (int b = 0; b < B; b++) f[h][b] = scale(sc, p, h, b);
+      for (int b = 0; b < NB; b++) f[h][b] = scale(sc, p, h, b);
 #pragma unroll
     for (int i = 0; i < Q; i++) {
       if constexpr (sizeof(T) == 2) {
@@ -309,14 +297,14 @@ struct Stream {
       } else {
         float w[P][8];
 #pragma unroll
-        for (int h = 0; h < P; h++) widen_f32(c.q[h][i], f[h][0], w[h]);
+        for (int h = 0; h < P; h++) widen_f32(c.q[h][i], f[h][i / 4], w[h]);
 #pragma unroll
         for (int g = 0; g < SETS; g++) {
           if (g > 0 && rows <= 4 * g) break;
           const int rg = 4 * g + lane % 4;
 #pragma unroll
           for (int u = 0; u < 2; u++) {
-            const float4 x = __builtin_bit_cast(float4, s[rg][(4 * grp + 2 * i + u) ^ rg]);
+            const float4 x = __builtin_bit_cast(float4, s[rg][(8 * grp + 2 * i + u) ^ rg]);
             const float xv[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int j = 0; j < 4; j++)
@@ -712,10 +700,12 @@ hipError_t launch_w4(const W4Args& p, hipStream_t st) {
   // workgroups; else fewer tiles and more shares
   const int64_t all = (int64_t)(p.R < p.E ? p.R : p.E) * (p.N / kRowsW);
   const int tiles = all >= 16 * cus ? 4 : all >= 4 * cus ? 2 : 1;
-  if constexpr (sizeof(T) == 4) return launch_stream<T, P, 0, false>(p, tiles, st);
-  else if (p.K % 128 != 0) return launch_stream<T, P, 1, true>(p, tiles, st);
-  else if (p.K % 256 != 0 || p.K < 256 * kStreamWaves / tiles) return launch_stream<T, P, 1, false>(p, tiles, st);
-  else return launch_stream<T, P, 2, false>(p, tiles, st);
+  if (p.K % 128 != 0) return launch_stream<T, P, 1, true>(p, tiles, st);
+  // two blocks a piece where every share has one of them (fp32 rows would not fit the registers)
+  if constexpr (sizeof(T) == 2) {
+    if (p.K % 256 == 0 && p.K >= 256 * kStreamWaves / tiles) return launch_stream<T, P, 2, false>(p, tiles, st);
+  }
+  return launch_stream<T, P, 1, false>(p, tiles, st);
 }
 
 }  // namespace
