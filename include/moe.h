@@ -44,7 +44,9 @@
  *    and loader waves than the measured defaults.  Each is read from the environment once,
  *    at the first launch that consults it, and kept until moe_tuning_reload.  They
  *    change only how the work is tiled and scheduled: every output element is still one fp32
- *    reduction over the same values in ascending order of the reduction index.
+ *    reduction over the same values in ascending order of the reduction index.  The products
+ *    with 4-bit weights and the GEMMs of the 8-bit checkpoints choose their tiles by the sizes
+ *    alone.
  *  - Limits: 1 <= k <= E <= 1024, T*k < 2^31, d and f multiples of 64; with MOE_MXFP8
  *    GEMMs d and f must be multiples of 128.  bf16 buffers need 16-byte alignment.
  */
@@ -492,7 +494,9 @@ moe_status moe_combine_norm_bwd(const moe_shape* s, const void* dv, const void* 
  *
  * MXFP4 rows: E2M1 codes (bit 3 the sign, bits 0-2 an index into 0, .5, 1, 1.5, 2, 3, 4, 6),
  * element 2i in the low half of byte i and 2i + 1 in the high half, and one scale byte b per
- * 32 elements along the row: value = code 2^(b - 127).  255 stands for a block of NaN.
+ * 32 elements along the row: value = code 2^(b - 127).  255 stands for a block of NaN.  Values are
+ * taken as bf16 or float, as `act`: one beyond the type's range is infinite, one below its smallest
+ * normal number may count as zero.
  *   W1q, W3q [E, f, d/2], W1s, W3s [E, f, d/32];  W2q [E, d, f/2], W2s [E, d, f/32]
  * Every buffer is 16-byte aligned.
  * --------------------------------------------------------------------------------------- */
@@ -507,7 +511,8 @@ moe_status moe_mx4_quantize(int32_t rows, int32_t cols, int32_t act, const void*
 /* h = silu(a) b with a = X_e W1_e^T, b = X_e W3_e^T in one kernel (a and b are not stored).
  * x_perm [R, d] act, h [R, f] act written.  The rows are not quantised: the weights widen
  * without a rounding and the sums are float (act MOE_BF16: bf16 products; MOE_F32: float).
- * moe_shape.gemm plays no part.  Any R; laid out for few rows per expert. */
+ * moe_shape.gemm plays no part.  d and f at most 2^22.  Up to five rows per expert (on average)
+ * the weights stream past the rows; for more, tiles of up to 96 rows share each weight. */
 moe_status moe_ffn_gemm1_fwd_w4(const moe_shape* s, const void* x_perm, const uint8_t* W1q, const uint8_t* W1s,
                                 const uint8_t* W3q, const uint8_t* W3s, const int32_t* offsets, void* h,
                                 void* stream);

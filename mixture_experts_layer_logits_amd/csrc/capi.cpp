@@ -667,6 +667,7 @@ moe_status moe_mx4_quantize(int32_t rows, int32_t cols, int32_t act, const void*
 moe_status moe_ffn_gemm1_fwd_w4(const moe_shape* s, const void* x_perm, const uint8_t* W1q, const uint8_t* W1s,
                                 const uint8_t* W3q, const uint8_t* W3s, const int32_t* offsets, void* h, void* st) {
   MOE_TRY(check_shape(s));
+  if (s->d > kW4MaxWidth || s->f > kW4MaxWidth) return MOE_EINVAL;
   MOE_TRY(check_ptrs({W1q, W1s, W3q, W3s}));
   MOE_TRY(check_rows(s, {x_perm, h}));
   if (!offsets) return MOE_ENULL;
@@ -676,6 +677,7 @@ moe_status moe_ffn_gemm1_fwd_w4(const moe_shape* s, const void* x_perm, const ui
 moe_status moe_ffn_gemm2_fwd_w4(const moe_shape* s, const void* h, const uint8_t* W2q, const uint8_t* W2s,
                                 const int32_t* offsets, void* y_perm, void* st) {
   MOE_TRY(check_shape(s));
+  if (s->d > kW4MaxWidth || s->f > kW4MaxWidth) return MOE_EINVAL;
   MOE_TRY(check_ptrs({W2q, W2s}));
   MOE_TRY(check_rows(s, {h, y_perm}));
   if (!offsets) return MOE_ENULL;

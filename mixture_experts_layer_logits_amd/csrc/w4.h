@@ -8,6 +8,7 @@
 namespace moe {
 
 constexpr int kMx4Block = 32;
+constexpr int kW4MaxWidth = 1 << 22;  // d and f: offsets inside a tile's rows are 32-bit
 
 // elem_bytes: 2 (bf16) or 4 (float)
 hipError_t mx4_quantize_rows(int elem_bytes, int rows, int cols, const void* src, uint8_t* q, uint8_t* s,

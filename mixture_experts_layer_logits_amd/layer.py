@@ -148,6 +148,8 @@ class MoEExpertLayer:
         dt = torch.float32 if act == MOE_F32 else torch.bfloat16
         self.dtype = dt
         dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:  # what later passes allocate lies there too
+            dev = torch.device("cuda", torch.cuda.current_device())
         e = lambda *s, dtype=dt: torch.empty(*s, dtype=dtype, device=dev)  # noqa: E731
         R = self.R
         i32, f32 = torch.int32, torch.float32

@@ -1,6 +1,7 @@
 """Refusals of the calls on 4-bit weights and 8-bit checkpoints: the documented status codes, before
 anything is enqueued, so they run without a GPU; and what the layer refuses on the host."""
 import ctypes
+import os
 
 import pytest
 import torch
@@ -49,6 +50,22 @@ def test_refused_before_launch(name, change, code):
 @pytest.mark.parametrize("shape", [dict(T=-1), dict(E=4, k=5), dict(E=1025), dict(d=100), dict(k=0)], ids=str)
 def test_bad_shapes_refused(name, shape):
     assert _call(name, _shape(**shape), CALLS[name].values()) == MOE_EINVAL
+
+
+@pytest.mark.parametrize("name", ["moe_ffn_gemm1_fwd_w4", "moe_ffn_gemm2_fwd_w4"])
+def test_rows_past_32_bit_offsets_are_refused(name):
+    assert _call(name, _shape(d=(1 << 22) + 64), CALLS[name].values()) == MOE_EINVAL
+    ok = {**CALLS[name], "offsets": 0}
+    assert _call(name, _shape(d=1 << 22), ok.values()) == MOE_ENULL  # not for its width
+
+
+def test_the_products_hand_rows_over_behind_a_fence():
+    """Lanes of a wave that pass routed rows on through LDS order the accesses with lanes.h's fence."""
+    src = open(os.path.join(os.path.dirname(LIB), "csrc", "w4.hip")).read()
+    body = src[src.index("st.hand_over"):]
+    assert body.index("wave_lds_fence()") < body.index("st.multiply(cur")
+    assert "wave_lds_fence()" in body[body.index("st.multiply(cur"):body.index("__syncthreads()")]
+    assert "__builtin_amdgcn_wave_barrier" not in src
 
 
 @pytest.mark.parametrize("name", [n for n in CALLS if n != "moe_ffn_gemm1_fwd_c8" and n != "moe_ffn_dgrad2_c8"])
