@@ -532,7 +532,8 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
         s[h] = __builtin_amdgcn_raw_buffer_load_b8(sr[h], k < a.K ? wr * sb + k / kMx4Block : kNowhere, 0, 0);
       } else {
         constexpr int SB = KC / kMx4Block;
-        const uint32_t o = wr * sb + ((step + grp) * KS + share) * SB;
+        const uint32_t at = ((step + grp) * KS + share) * SB;  // past the row's end the next row's, which may be NaN
+        const uint32_t o = at < sb ? wr * sb + at : kNowhere;
         if constexpr (SB == 4) s[h] = __builtin_amdgcn_raw_buffer_load_b32(sr[h], o, 0, 0);
         else s[h] = __builtin_amdgcn_raw_buffer_load_b16(sr[h], o, 0, 0);
       }

@@ -245,6 +245,32 @@ def test_numbers_that_are_none_stay_in_their_rows(T, E, act):
     assert np.array_equal(bad, want)
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [64, 128, 192, 384, 448])
+@pytest.mark.parametrize("T", [6, 70, 200])
+def test_a_nan_block_at_a_rows_end_or_begin_stays_in_its_row(T, K, act):
+    """Neither the row before (whose last step may reach past its end) nor the one behind sees it."""
+    m = _m()
+    E, other = 3, 64
+    dt = torch.float32 if act == "f32" else torch.bfloat16
+    a = m.MOE_F32 if act == "f32" else m.MOE_BF16
+    off = torch.tensor([0, T // 2, T // 2, T], dtype=torch.int32).cuda()
+    x = torch.ones(T, K, dtype=dt, device="cuda")
+    q, sc = ref.mx4_quantize(np.full((E, other, K), 0.5))
+    sc[2, 5, 0] = sc[2, 40, -1] = 255
+    w = [torch.from_numpy(t).cuda() for t in (q, sc)]
+    want = np.zeros((T, other), dtype=bool)
+    want[T // 2:, [5, 40]] = True
+    h = torch.zeros(T, other, dtype=dt, device="cuda")
+    m.moe_ffn_gemm1_fwd_w4(m.make_shape(T, K, other, E, 1, a), x, *w, *w, off, h)
+    assert np.array_equal(np.isnan(host(h)), want)
+    y = torch.zeros(T, other, dtype=dt, device="cuda")
+    m.moe_ffn_gemm2_fwd_w4(m.make_shape(T, other, K, E, 1, a), x, *w, off, y)
+    assert np.array_equal(np.isnan(host(y)), want)
+    fine = host(y)[~want]
+    assert (fine == 0.5 * K).all()
+
+
 def test_rows_do_not_depend_on_the_expert_that_holds_them():
     """Rows moved to another expert with the same weights come out the same, bit for bit."""
     m = _m()
