@@ -359,8 +359,8 @@ def moe_ffn_dgrad1_mx(shape, dabq_rows, dabs_rows, W1, W3, offsets, dx_perm, ws,
 
 # ------------------------------------------------------------------ around the layer
 def _call_checked(name, shape, args, stream=None):
-    """Call `name` with shape (None: the call takes none) and args in the C call's order: a tensor as (argument name, tensor or None, dtype,
-    number of elements), anything else as it is.  Tensors have to lie on one GPU, contiguous, of
+    """Call `name` with shape (None: the call takes none) and args in the C call's order: a tensor as
+    (argument name, tensor or None, dtype, number of elements), anything else as it is.  Tensors have to lie on one GPU, contiguous, of
     that type and size (dtype None: a workspace of any type, whose size in bytes is passed on
     behind it).  The call runs on that GPU's current stream if none is given, whichever device is
     the current one."""
@@ -474,8 +474,10 @@ def moe_combine_norm_bwd(shape, dv, dxn, v, y_perm, gates, slot_row, y_add, gate
 _I8 = torch.int8
 
 
-def _act_of(name, t):
+def _act_of(name, t, rows, cols):
     """The `act` argument of a call on rows of blocks: the rows' own type."""
+    if not (0 <= rows < 1 << 31 and 0 < cols < 1 << 31):  # the call takes 32 bits of each
+        raise ValueError(f"{name}: rows {rows} and cols {cols} must fit 32 bits, cols at least 32")
     if t.dtype is not _F32 and t.dtype is not torch.bfloat16:
         raise ValueError(f"{name}: rows must be float32 or bfloat16, got {t.dtype}")
     return MOE_F32 if t.dtype is _F32 else MOE_BF16
@@ -485,7 +487,7 @@ def moe_mx4_quantize(rows, cols, src, q, scales, stream=None):
     """MXFP4 of src [rows, cols] (float32 or bfloat16): q uint8 [rows, cols/2], scales uint8 [rows, cols/32]."""
     n = rows * cols
     _call_checked("moe_mx4_quantize", None, (
-        rows, cols, _act_of("moe_mx4_quantize", src), ("src", src, src.dtype, n), ("q", q, _U8, n // 2),
+        rows, cols, _act_of("moe_mx4_quantize", src, rows, cols), ("src", src, src.dtype, n), ("q", q, _U8, n // 2),
         ("scales", scales, _U8, n // 32)), stream)
 
 
@@ -513,7 +515,7 @@ def moe_ckpt8_pack(rows, cols, src, q, scales, stream=None):
     """MXINT8 of src [rows, cols] (float32 or bfloat16): q int8 [rows, cols], scales uint8 [rows, cols/32]."""
     n = rows * cols
     _call_checked("moe_ckpt8_pack", None, (
-        rows, cols, _act_of("moe_ckpt8_pack", src), ("src", src, src.dtype, n), ("q", q, _I8, n),
+        rows, cols, _act_of("moe_ckpt8_pack", src, rows, cols), ("src", src, src.dtype, n), ("q", q, _I8, n),
         ("scales", scales, _U8, n // 32)), stream)
 
 
@@ -522,7 +524,7 @@ def moe_ckpt8_unpack(rows, cols, q, scales, dst, h=None, stream=None):
     times its second."""
     n = rows * cols
     _call_checked("moe_ckpt8_unpack", None, (
-        rows, cols, _act_of("moe_ckpt8_unpack", dst), ("q", q, _I8, n), ("scales", scales, _U8, n // 32),
+        rows, cols, _act_of("moe_ckpt8_unpack", dst, rows, cols), ("q", q, _I8, n), ("scales", scales, _U8, n // 32),
         ("dst", dst, dst.dtype, n), ("h", h, dst.dtype, n // 2)), stream)
 
 

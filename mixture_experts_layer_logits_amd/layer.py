@@ -83,6 +83,8 @@ y = MoE(norm(h) w_pre), and the norm of the next block in the same pass.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import (MOE_BF16, MOE_F32, MOE_MX_DGRAD1, MOE_MX_DGRAD2, MOE_MX_GEMM1, MOE_MX_GEMM2, MOE_MX_WGRAD1,
@@ -105,7 +107,7 @@ def quantize_weights(*weights):
     pair (codes uint8 [.., n, K/2], scales uint8 [.., n, K/32]), as a layer with ``weights4`` takes them."""
     out = []
     for w in weights:
-        rows, K = w.numel() // w.shape[-1], w.shape[-1]
+        rows, K = math.prod(w.shape[:-1]), w.shape[-1]
         q = torch.empty(*w.shape[:-1], K // 2, dtype=torch.uint8, device=w.device)
         s = torch.empty(*w.shape[:-1], K // 32, dtype=torch.uint8, device=w.device)
         moe_mx4_quantize(rows, K, w, q, s)

@@ -111,6 +111,11 @@ def test_binding_refuses_types_and_tensors_off_the_gpu():
         m.moe_mx4_quantize(4, 64, x.half(), u8, u8)
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         m.moe_ckpt8_unpack(4, 64, u8, u8, x.double())
+    for call in (m.moe_mx4_quantize, m.moe_ckpt8_pack):
+        with pytest.raises(ValueError, match="fit 32 bits"):  # not wrapped to 4 rows
+            call((1 << 32) + 4, 64, x, u8, u8)
+    with pytest.raises(ValueError, match="fit 32 bits"):
+        m.moe_ckpt8_unpack(4, (1 << 32) + 64, u8, u8, x)
     s = m.make_shape(4, 64, 64, 2, 1, m.MOE_F32)
     with pytest.raises(ValueError, match="must live on the GPU"):
         m.moe_ffn_gemm2_fwd_w4(s, x, u8, u8, torch.zeros(3, dtype=torch.int32), x)
