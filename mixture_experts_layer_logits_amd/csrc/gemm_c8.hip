@@ -39,18 +39,19 @@ struct ProbDgrad2C8 : ProbDgrad2 {
   }
 };
 
-// Tiles.  128 x 256 with four loader waves, 64 deep in three stages, where its tiles fill the device
-// (the plain GEMMs' choice; 417 us for GEMM1 and 271 us for dgrad2 at E = 128, T = 8192, d = 2048, f =
-// 1024).  `tiles` counts them for the worst routing.  Below two a compute unit, or with a row or two per
-// expert, smaller tiles give more workgroups:
-//   GEMM1   64 x 128 in three stages (four waves of 32 x 64, so that a wave holds a and b of its
-//           columns): 12.5 against 22 us at R = 993, E = 6, d = 1088, f = 448; 57 against 65 at R =
-//           4000, E = 8 and 117 against 141 at R = 256, E = 128 (d = 2048, f = 1024)
-//   dgrad2  32 x 128 up to half a tile a compute unit: 11 against 26 us at R = 993, E = 6; 65 against 81
-//           at R = 256, E = 128; from there to two 128 x 128 in two stages: 71 against 79 us at R =
-//           32768, E = 8, d = 1024, f = 512
-static int64_t c8_tiles(const GemmShape& s, int N) {
-  return ((int64_t)s.R / 128 + (s.R < s.E ? s.R : s.E)) * ((N + 255) / 256);
+// Tiles (us below are of the named alternatives, in a graph).  128 x 256 with four loader waves, 64 deep in
+// three stages, where they fill the rounds of one tile a compute unit: 455 against 483 with 128 x 128 for
+// GEMM1 and 275 against 293 for dgrad2 at E = 128, R = 32768, d = 2048, f = 1024.  Where the last round or
+// the last columns stand empty 128 x 128 (8 waves, two workgroups a compute unit) is faster: GEMM1 118 against 127
+// (0.82 filled) but 194 against 197 (0.85), dgrad2 63 against 78 (0.69) but 192 against 176 (0.75).
+//
+// Tiles of a launch for the worst routing, and whether 128 x 256 ones use num / den of their rounds
+static int64_t c8_tiles(const GemmShape& s, int N, int bm, int bn) {
+  return ((int64_t)s.R / bm + (s.R < s.E ? s.R : s.E)) * ((N + bn - 1) / bn);
+}
+static bool c8_large(const GemmShape& s, int N, int num, int den) {
+  const int64_t tiles = c8_tiles(s, N, 128, 256), cus = device_cu_count(), rounds = (tiles + cus - 1) / cus;
+  return rounds > 1 && tiles * N * den >= rounds * cus * ((N + 255) / 256 * 256) * num;
 }
 
 hipError_t gemm1_fwd_c8_bf16(const GemmShape& s, const int* offsets, const bf16_t* X, const bf16_t* W1,
@@ -58,9 +59,11 @@ hipError_t gemm1_fwd_c8_bf16(const GemmShape& s, const int* offsets, const bf16_
   ProbGemm1C8 p;
   p.M = s.R; p.N = 2 * s.f; p.K = s.d; p.E = s.E; p.offsets = offsets; p.f = s.f;
   p.X = X; p.W1 = W1; p.W3 = W3; p.h = h; p.abq = abq; p.ab_s = ab_s;
-  if (c8_tiles(s, p.N) <= 2 * device_cu_count() || s.R <= (int64_t)16 * s.E)
-    return launch_pipe<TileCfg<64, 128, 2, 2>, ProbGemm1C8, 64, 3>(p, st);
-  return launch_pipe<TileCfg<128, 256, 2, 4>, ProbGemm1C8, 64, 3, 4>(p, st);
+  // up to 32 rows an expert 64 x 128 (four waves of 32 x 64, so that a wave holds a and b of its columns):
+  // 18 against 22 with 128 x 128 at R = 784, E = 43, d = 1344, f = 256, 206 against 221 at R = 4096, E = 128
+  if (s.R <= (int64_t)32 * s.E) return launch_pipe<TileCfg<64, 128, 2, 2>, ProbGemm1C8, 64, 3>(p, st);
+  if (c8_large(s, p.N, 27, 32)) return launch_pipe<TileCfg<128, 256, 2, 4>, ProbGemm1C8, 64, 3, 4>(p, st);
+  return launch_pipe<TileCfg<128, 128, 4, 2>, ProbGemm1C8, 64, 2>(p, st);
 }
 
 hipError_t dgrad2_c8_bf16(const GemmShape& s, const int* offsets, const bf16_t* dY, const bf16_t* W2,
@@ -68,12 +71,18 @@ hipError_t dgrad2_c8_bf16(const GemmShape& s, const int* offsets, const bf16_t* 
   ProbDgrad2C8 p;
   p.M = s.R; p.N = s.f; p.K = s.d; p.E = s.E; p.offsets = offsets;
   p.dY = dY; p.W2 = W2; p.dab = dab; p.abq = abq; p.ab_s = ab_s; p.h = h;
-  const int64_t tiles = c8_tiles(s, p.N), cus = device_cu_count();
-  if (2 * tiles <= cus || s.R <= (int64_t)4 * s.E)
-    return launch_pipe<TileCfg<32, 128, 1, 4>, ProbDgrad2C8, 64, 2>(p, st);
-  if (tiles <= 2 * cus && s.R > (int64_t)64 * s.E)
-    return launch_pipe<TileCfg<128, 128, 2, 2>, ProbDgrad2C8, 64, 2>(p, st);
-  return launch_pipe<TileCfg<128, 256, 2, 4>, ProbDgrad2C8, 64, 3, 4>(p, st);
+  // a row or two an expert: 32 rows a tile (66 against 69 with 64 x 64, R = 256, E = 128, f = 1024)
+  if (s.R <= (int64_t)4 * s.E) return launch_pipe<TileCfg<32, 128, 1, 4>, ProbDgrad2C8, 64, 2>(p, st);
+  // few tiles, or one column of them: 18 against 20 with 128 x 128 at R = 800, E = 8, f = 2048 (640 tiles; 16 against
+  // 15.6 at 893), 24 against 32 at R = 120000, f = 64
+  if (p.N <= 64 || c8_tiles(s, p.N, 64, 64) <= 3 * (int64_t)device_cu_count())
+    return launch_pipe<TileCfg<64, 64, 2, 2>, ProbDgrad2C8, 64, 2>(p, st);
+  // few columns, or a sixth of the last 128 empty: 27 against 29 with 128 x 128 at f = 128, 15 against 21 at 192, 48
+  // against 51 at 320
+  const int cols = (p.N + 127) / 128 * 128;
+  if (cols == 128 || 6 * (cols - p.N) >= cols) return launch_pipe<TileCfg<128, 64, 4, 2>, ProbDgrad2C8, 64, 2>(p, st);
+  if (c8_large(s, p.N, 3, 4)) return launch_pipe<TileCfg<128, 256, 2, 4>, ProbDgrad2C8, 64, 3, 4>(p, st);
+  return launch_pipe<TileCfg<128, 128, 4, 2>, ProbDgrad2C8, 64, 2>(p, st);
 }
 
 }  // namespace moe

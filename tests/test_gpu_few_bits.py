@@ -292,7 +292,8 @@ def test_rows_do_not_depend_on_the_expert_that_holds_them():
 
 # ------------------------------------------------------------------ 8-bit checkpoints
 FFN = [(1, 64, 64, 1, 1), (5, 128, 64, 4, 2), (40, 192, 320, 6, 3), (130, 256, 128, 3, 1), (257, 64, 192, 5, 2),
-       (300, 448, 64, 64, 4), (1100, 64, 64, 1, 1)]
+       (300, 448, 64, 64, 4), (1100, 64, 64, 1, 1),
+       (24700, 64, 128, 2, 1), (3300, 64, 1024, 2, 1), (16320, 64, 1024, 1, 1)]  # each of the larger tiles
 
 
 def _ffn_inputs(T, d, f, E, k, whole):
