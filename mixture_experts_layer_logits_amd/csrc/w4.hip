@@ -208,9 +208,9 @@ struct Stream {
     bool live;  // the wave has this piece (the same in all lanes)
   };
   // Scale bytes of four pieces that follow one another: lane l holds those of piece l / 16, row l % 16, so
-  // that a row's come in one load; TAIL: of one piece, byte l / 16
+  // that a row's come in one load; TAIL: in two, as K / 32 may be an odd number of pairs
   struct Scales {
-    uint32_t w[P][NB];
+    uint32_t w[P][NB], hi[TAIL ? P : 1];
   };
   const W4Args& a;
   int lane, wr, grp;
@@ -234,25 +234,26 @@ struct Stream {
   __device__ __forceinline__ void load_scales(Scales& c, const W4Tile& t, int col, int k) const {
     const int64_t wrow = (int64_t)(t.e >= 0 ? t.e : 0) * a.N + col;
     const uint8_t* const ss[2] = {a.s0, a.s1};
-    const uint32_t sb = a.K / kMx4Block;
+    const uint32_t sb = a.K / kMx4Block, at = k / kMx4Block + SB * grp, so = wr * sb + at;
 #pragma unroll
     for (int h = 0; h < P; h++) {
       const auto s = buffer(ss[h] + wrow * sb, t.e >= 0 && k < a.K ? kRowsW * sb : 0);
-      const uint32_t so = wr * sb + k / kMx4Block;
       if constexpr (TAIL) {
-        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b8(s, k + 32 * grp < a.K ? so + grp : kNowhere, 0, 0);
+        // past the row's end the next row's, which may be NaN
+        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b16(s, at < sb ? so : kNowhere, 0, 0);
+        c.hi[h] = __builtin_amdgcn_raw_buffer_load_b16(s, at + 2 < sb ? so + 2 : kNowhere, 0, 0);
       } else if constexpr (NB == 2) {
-        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(s, so + SB * grp, 0, 0);
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(s, so, 0, 0);
         c.w[h][0] = v.x, c.w[h][1] = v.y;
       } else {
-        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b32(s, so + SB * grp, 0, 0);
+        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b32(s, so, 0, 0);
       }
     }
   }
   // The scale of projection h's block b of the p-th of the four pieces, as the widening instructions take it
   __device__ __forceinline__ float scale(const Scales& c, int p, int h, int b) const {
-    if constexpr (TAIL) return mx4_scale(c.w[h][0]);
-    const uint32_t w = __builtin_amdgcn_ds_bpermute(4 * (16 * p + wr), c.w[h][b]);
+    const uint32_t w =
+        __builtin_amdgcn_ds_bpermute(4 * (16 * p + wr), TAIL ? c.w[h][0] | c.hi[h] << 16 : c.w[h][b]);
     return mx4_scale(w >> (8 * grp) & 255);
   }
 
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
   W4Finder<ROWS, false> finder(a.offsets, a.E, a.N / width, lane);
   W4Tile tile = finder.find(t), ahead = tile;  // the tile in hand, and that of the next piece
   if (tile.e < 0) return;
-  constexpr int GROUP = TAIL ? 1 : 4;  // pieces whose scales are loaded at once
+  constexpr int GROUP = 4;  // pieces whose scales are loaded at once
   auto first = [&](int i) { return (share * iters + i) * S::SPAN; };  // element of piece i of a tile
   auto column = [&](const W4Tile& t) { return t.nt * width + kRowsW * sub; };
   int it = 0, buf = 0;
