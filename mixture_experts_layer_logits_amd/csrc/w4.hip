@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
         };
         v[h] = shares == 8   ? add(std::integral_constant<int, 8>())
                : shares == 4 ? add(std::integral_constant<int, 4>())
-                             : add(std::integral_constant<int, 2>());
+               : shares == 2 ? add(std::integral_constant<int, 2>())
+                             : add(std::integral_constant<int, 1>());
       }
       float out = v[0];
       if constexpr (P == 2) out = v[0] * sigmoidf_(v[0]) * v[1];
@@ -681,6 +682,26 @@ TileWork tile_work(const W4Args& p, int nw) {
   return {tiles, (tiles + cus - 1) / cus * (rows / runs * p.K * 2 + bn * P * p.K * 17 / 32)};
 }
 
+// Tiles of a streaming workgroup, and so shares of the reduction (8 / tiles): the number that takes the
+// fewest rounds of pieces, a tile's end counting as some two of them (barrier and sums of the shares).
+// More shares than pieces leave waves idle, fewer tiles than the device holds leave it idle.
+// us with 1, 2, 4 tiles: 5.2, 4.3, 5.0 (T = 1, K = 1024, N = 2048, not gated), 9.3, 8.9, 7.5 (T = 10, E = 31, K =
+// 1280, N = 448), 16.9, 15.7, 14.4 (T = 8, E = 128, K = 2048, N = 1024); with 2, 4, 8: 20, 12, 9.5 (T = 32, E = 128,
+// K = 256, N = 2048).
+int stream_tiles(const W4Args& p, int span) {
+  const int64_t experts = p.R < p.E ? p.R : p.E, rows = (p.R + experts - 1) / experts;
+  const int64_t all = experts * ((rows + kRowsX - 1) / kRowsX) * (p.N / kRowsW), fit = device_cu_count();
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int tiles = 1; tiles <= kStreamWaves; tiles *= 2) {
+    const int shares = kStreamWaves / tiles;
+    if (p.N % (kRowsW * tiles) != 0 || (shares == 1 && p.K > 256)) break;
+    const int64_t cost = ((all / tiles + fit - 1) / fit) * (((int64_t)p.K + span * shares - 1) / (span * shares) + 2);
+    if (cost < least) least = cost, best = tiles;
+  }
+  return best;
+}
+
 template <typename T, int P>
 hipError_t launch_w4(const W4Args& p, hipStream_t st) {
   if (p.R == 0) return hipSuccess;
@@ -698,10 +719,7 @@ hipError_t launch_w4(const W4Args& p, hipStream_t st) {
     if (four.tiles <= cus) return launch_tile<T, P, 4, 2, false>(p, st);
     return launch_tile<T, P, 4, 1, false>(p, st);
   }
-  // four tiles a workgroup, two shares of the reduction each, where that leaves every compute unit four
-  // workgroups; else fewer tiles and more shares
-  const int64_t all = (int64_t)(p.R < p.E ? p.R : p.E) * (p.N / kRowsW);
-  const int tiles = all >= 16 * cus ? 4 : all >= 4 * cus ? 2 : 1;
+  const int tiles = stream_tiles(p, sizeof(T) == 2 && p.K % 256 == 0 ? 256 : 128);
   if (p.K % 128 != 0) return launch_stream<T, P, 1, true>(p, tiles, st);
   // two blocks a piece where every share has one of them (fp32 rows would not fit the registers)
   if constexpr (sizeof(T) == 2) {
