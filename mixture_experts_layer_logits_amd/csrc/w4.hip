@@ -116,19 +116,25 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// The tiles of a launch: an expert's rows in runs of at most ROWS (even shares of whole 16s where EVEN),
-// its weight rows in ntn tiles; the runs that share a weight tile follow one another.  Every wave finds
+// The tiles of a launch: an expert's rows in runs of at most kRowsX where UNIT is 8, of even shares of at most
+// `cap` whole 16s where UNIT is 16 (cap_inv: 2^32 / cap, rounded up), its weight rows in ntn tiles; the runs that share a weight tile follow one another.  Every wave finds
 // its tiles by itself, so no barrier stands before the first load: a lane holds two experts of a window
 // of 128, whose run counts are scanned in registers, and as tiles are asked for in ascending order the
 // window only moves forward.
 struct W4Tile {
   int e, m0, m_end, nt;  // e < 0: past the last tile
 };
-template <int ROWS, bool EVEN>
+template <int UNIT>
 struct W4Finder {
   const int* offsets;
-  int E, ntn, lane, e0, at[3], incl;  // at: where the lane's experts e0 + 2 lane, + 1 begin, and the next
-  static __device__ __forceinline__ int runs(int rows) { return (rows + ROWS - 1) / ROWS; }
+  int E, ntn, lane, cap;
+  uint32_t cap_inv;
+  int e0, at[3], incl;  // at: where the lane's experts e0 + 2 lane, + 1 begin, and the next
+  __device__ __forceinline__ int runs(int rows) const {
+    const int units = (rows + UNIT - 1) / UNIT;
+    if constexpr (UNIT == 8) return units;
+    return cap == 1 ? units : (int)__umulhi(units + cap - 1, cap_inv);
+  }
   __device__ __forceinline__ void window(int before) {
 #pragma unroll
     for (int i = 0; i < 3; i++) {
@@ -137,8 +143,8 @@ struct W4Finder {
     }
     incl = before + wave_scan(runs(at[1] - at[0]) + runs(at[2] - at[1]));
   }
-  __device__ __forceinline__ W4Finder(const int* off, int E_, int ntn_, int lane_)
-      : offsets(off), E(E_), ntn(ntn_), lane(lane_), e0(0) {
+  __device__ __forceinline__ W4Finder(const int* off, int E_, int ntn_, int lane_, int cap_ = 1, uint32_t inv = 0)
+      : offsets(off), E(E_), ntn(ntn_), lane(lane_), cap(cap_), cap_inv(inv), e0(0) {
     window(0);
   }
   __device__ __forceinline__ W4Tile find(int t) {
@@ -155,7 +161,9 @@ struct W4Finder {
         if (second) local -= r0 * ntn;
         const int me = second ? r1 : r0, start = second ? a1 : a0, end = second ? a2 : a1;
         const int nt = me == 1 ? local : local / me;
-        const int per = EVEN && me > 1 ? ((end - start + 15) / 16 + me - 1) / me * 16 : ROWS;
+        const int per = UNIT == 8   ? UNIT
+                        : me == 1 ? cap * UNIT
+                                  : ((end - start + UNIT - 1) / UNIT + me - 1) / me * UNIT;
         const int m0 = start + (local - nt * me) * per;
         return W4Tile{e0 + 2 * l + (second ? 1 : 0), m0, m0 + per < end ? m0 + per : end, nt};
       }
@@ -185,12 +193,6 @@ __device__ __forceinline__ int first_tile() {
 // multiplies the one it has; the routed rows' part comes in whole rows (a load for two of them) and is
 // handed to the lanes through LDS of the wave's own.
 constexpr int kStreamWaves = 8;
-// Rows an expert, on average, up to which the weights stream; above, the tiles of many rows are faster
-// (us, stream / tiles).  4 rows 29.5 / 34.5, 6 rows 34.5 / 34.4, 12 rows 50 / 38 (bf16, E = 64, d = 2048, f
-// = 1024, gated); 4 rows 65 / 81, 8 rows 95 / 82 (the same in fp32).  fp32 tiles, whose products take most of
-// the time, need one for every compute unit: else 8 rows 11.9 / 15.1, 32 rows 30.5 / 31.4, 48 rows 43.5 /
-// 39.7 (E = 8, K = 1024, N = 2048)
-constexpr int kStreamMaxRows = 5, kStreamMaxRowsFew = 32;
 constexpr int kRowsW = 16;          // weight rows of a tile
 constexpr int kRowsX = 8;           // routed rows of a tile
 
@@ -331,7 +333,8 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
   const int iters = (a.K + S::SPAN * shares - 1) / (S::SPAN * shares);
   const int width = kRowsW * tiles;  // weight rows of the workgroup's tiles
   int t = first_tile();
-  W4Finder<ROWS, false> finder(a.offsets, a.E, a.N / width, lane);
+  static_assert(ROWS == 8, "runs of the finder");
+  W4Finder<ROWS> finder(a.offsets, a.E, a.N / width, lane);
   W4Tile tile = finder.find(t), ahead = tile;  // the tile in hand, and that of the next piece
   if (tile.e < 0) return;
   constexpr int GROUP = 4;  // pieces whose scales are loaded at once
@@ -503,7 +506,7 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
   constexpr int AHEAD = 3;  // steps that weights are loaded ahead (even + 1: the rows' sets take turns too)
   u32x4 xs[2][XN];
   uint32_t q[AHEAD + 1][2][Q];
-  uint32_t sc[TAIL ? AHEAD + 1 : 2][2];  // TAIL: of each step; else of 4 steps, as the lane's of step l / 16
+  uint32_t sc[2][2], hi[2][2];  // of 4 steps, the lane's of step l / 16; hi: TAIL's second half
   // past the reduction's end both sides are zero
   auto load_x = [&](int step, u32x4(&x)[XN]) __attribute__((always_inline)) {
     const uint32_t o = (step * KS + share) * 256 + xc * 16;
@@ -525,24 +528,21 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
       }
     }
   };
-  // a row's scale bytes of four steps come in one load, a step's to each of its four lanes
-  auto load_s = [&](int step, uint32_t(&s)[2]) __attribute__((always_inline)) {
+  // a row's scale bytes of four steps come in one load (TAIL: two, see Stream), a step's to each of its four lanes
+  auto load_s = [&](int step, int set) __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      if constexpr (TAIL) {
-        const int k = (step * KS + share) * KC + grp * EPL;
-        s[h] = __builtin_amdgcn_raw_buffer_load_b8(sr[h], k < a.K ? wr * sb + k / kMx4Block : kNowhere, 0, 0);
-      } else {
-        constexpr int SB = KC / kMx4Block;
-        const uint32_t at = ((step + grp) * KS + share) * SB;  // past the row's end the next row's, which may be NaN
-        const uint32_t o = at < sb ? wr * sb + at : kNowhere;
-        if constexpr (SB == 4) s[h] = __builtin_amdgcn_raw_buffer_load_b32(sr[h], o, 0, 0);
-        else s[h] = __builtin_amdgcn_raw_buffer_load_b16(sr[h], o, 0, 0);
-      }
+      constexpr int SB = KC / kMx4Block;
+      const uint32_t at = ((step + grp) * KS + share) * SB;  // past the row's end the next row's, which may be NaN
+      const uint32_t o = at < sb ? wr * sb + at : kNowhere;
+      if constexpr (SB == 4 && !TAIL) sc[set][h] = __builtin_amdgcn_raw_buffer_load_b32(sr[h], o, 0, 0);
+      else sc[set][h] = __builtin_amdgcn_raw_buffer_load_b16(sr[h], o, 0, 0);
+      if constexpr (TAIL)
+        hi[set][h] = __builtin_amdgcn_raw_buffer_load_b16(sr[h], at + 2 < sb ? o + 2 : kNowhere, 0, 0);
     }
   };
-  auto scale = [&](uint32_t s, int v) __attribute__((always_inline)) {
-    if constexpr (TAIL) return mx4_scale(s);
+  auto scale = [&](int set, int h, int v) __attribute__((always_inline)) {
+    const uint32_t s = TAIL ? sc[set][h] | hi[set][h] << 16 : sc[set][h];
     const uint32_t w = __builtin_amdgcn_ds_bpermute(4 * (16 * v + wr), s);
     return mx4_scale(w >> (8 * (grp * EPL / kMx4Block)) & 255);
   };
@@ -557,11 +557,7 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
   load_x(0, xs[0]);
 #pragma unroll
   for (int v = 0; v < AHEAD; v++) load_w(v, q[v]);
-  load_s(0, sc[0]);
-  if constexpr (TAIL) {
-    load_s(1, sc[1]);
-    load_s(2, sc[2]);
-  }
+  load_s(0, 0);
   load_x(1, xs[1]);
   stage(0);
   __syncthreads();
@@ -573,11 +569,9 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
     for (int v = 0; v < 2 * N; v++) {
       load_x(step + 2, xs[v & 1]);
       load_w(step + AHEAD, q[(v + AHEAD) % N]);
-      if constexpr (TAIL) load_s(step + AHEAD, sc[(v + AHEAD) % N]);
-      else if (v % N == 0) load_s(step + N, sc[v / N ^ 1]);
+      if (v % N == 0) load_s(step + N, v / N ^ 1);
       __builtin_amdgcn_sched_barrier(0);  // the loads go first
-      const uint32_t(&s)[2] = sc[TAIL ? v % N : v / N];
-      multiply_step<T, NTA>(s_x[v & 1], q[v % N], scale(s[0], v % N), scale(s[1], v % N), wr, grp, acc);
+      multiply_step<T, NTA>(s_x[v & 1], q[v % N], scale(v / N, 0, v % N), scale(v / N, 1, v % N), wr, grp, acc);
       stage((v & 1) ^ 1);
       __syncthreads();
       if (++step == steps) break;
@@ -628,10 +622,10 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
 }
 
 template <typename T, int P, int NW, int KS, bool TAIL>
-__global__ void __launch_bounds__(64 * NW * KS, NW == 12 ? 3 : 2) w4_tile_kernel(W4Args a) {
+__global__ void __launch_bounds__(64 * NW * KS, NW == 12 ? 3 : 2) w4_tile_kernel(W4Args a, int cap, uint32_t cap_inv) {
   constexpr int BN = 32 * NW / P;
   __shared__ __attribute__((aligned(16))) u32x4 s_x[KS][2][kTileRows][16];
-  W4Finder<kTileRows, true> finder(a.offsets, a.E, (a.N + BN - 1) / BN, threadIdx.x & 63);
+  W4Finder<16> finder(a.offsets, a.E, (a.N + BN - 1) / BN, threadIdx.x & 63, cap, cap_inv);
   for (int t = first_tile();; t += gridDim.x) {
     const W4Tile tile = finder.find(t);
     if (tile.e < 0) break;
@@ -646,9 +640,9 @@ __global__ void __launch_bounds__(64 * NW * KS, NW == 12 ? 3 : 2) w4_tile_kernel
   }
 }
 
-template <int ROWS>
-unsigned w4_grid(const W4Args& p, int ntn, int per_cu) {
-  const int64_t bound = ((int64_t)p.R / ROWS + (p.R < p.E ? p.R : p.E)) * ntn;  // tiles of any routing
+// rows: of a tile, at most
+unsigned w4_grid(const W4Args& p, int rows, int ntn, int per_cu) {
+  const int64_t bound = ((int64_t)p.R / rows + (p.R < p.E ? p.R : p.E)) * ntn;  // tiles of any routing
   const int64_t most = (int64_t)device_cu_count() * per_cu;
   const int64_t g = bound < most ? bound : most;
   return (unsigned)(g < 64 ? g : (g + 63) / 64 * 64);
@@ -656,30 +650,83 @@ unsigned w4_grid(const W4Args& p, int ntn, int per_cu) {
 
 template <typename T, int P, int NB, bool TAIL>
 hipError_t launch_stream(const W4Args& p, int tiles, hipStream_t st) {
-  hipLaunchKernelGGL((w4_stream_kernel<T, P, NB, TAIL>), dim3(w4_grid<kRowsX>(p, p.N / (kRowsW * tiles), 2)),
+  hipLaunchKernelGGL((w4_stream_kernel<T, P, NB, TAIL>), dim3(w4_grid(p, kRowsX, p.N / (kRowsW * tiles), 2)),
                      dim3(64 * kStreamWaves), 0, st, p, tiles);
   return hipGetLastError();
 }
 
 template <typename T, int P, int NW, int KS, bool TAIL>
-hipError_t launch_tile(const W4Args& p, hipStream_t st) {
+hipError_t launch_tile(const W4Args& p, int cap, hipStream_t st) {
   constexpr int BN = 32 * NW / P;
-  hipLaunchKernelGGL((w4_tile_kernel<T, P, NW, KS, TAIL>), dim3(w4_grid<kTileRows>(p, (p.N + BN - 1) / BN, 64)),
-                     dim3(64 * NW * KS), 0, st, p);
+  hipLaunchKernelGGL((w4_tile_kernel<T, P, NW, KS, TAIL>), dim3(w4_grid(p, 16 * cap, (p.N + BN - 1) / BN, 64)),
+                     dim3(64 * NW * KS), 0, st, p, cap, (uint32_t)(((1ull << 32) + cap - 1) / cap));
   return hipGetLastError();
 }
 
-// Tiles of NW waves, for rows spread evenly, and the bytes that the busiest compute unit loads for them
-struct TileWork {
-  int64_t tiles, bytes;
+// What the tiles of a launch cost the busiest compute unit, as bytes that it could load in that time (24 a
+// nanosecond), for `waves` waves by up to `cap` 16s of rows, `shares` of the reduction: the bytes of its tiles,
+// in fp32 their products where these take longer (25 operations a byte, of 12 rows more than there are), and
+// 48 KB (2 us) a tile for its first loads and its end, more with two shares or 12 waves; a quarter of the
+// largest tile for the last round, and a quarter for 12 waves, of which no two tiles share a compute unit;
+// one tile of 4 waves alone loads a fifth slower.  Half of the experts leave a run unfilled, and the fullest
+// have 1.6 times the average.  Fitted to 56 shapes (1 to 256 rows an expert): what it chooses takes 2.3%
+// more than the fastest choice on average, 22% at worst.
+struct TileChoice {
+  int waves, shares, cap;
+  double cost;
 };
-template <int P>
-TileWork tile_work(const W4Args& p, int nw) {
-  const int64_t bn = 32 * nw / P, experts = p.R < p.E ? p.R : p.E, rows = (p.R + experts - 1) / experts;
-  const int64_t runs = (rows + kTileRows - 1) / kTileRows;
-  const int64_t tiles = experts * runs * ((p.N + bn - 1) / bn);
-  const int64_t cus = device_cu_count();
-  return {tiles, (tiles + cus - 1) / cus * (rows / runs * p.K * 2 + bn * P * p.K * 17 / 32)};
+template <typename T, int P>
+double tile_cost(const W4Args& p, int waves, int shares, int cap) {
+  const double k = p.K, bn = 32 * waves / P, experts = p.R < p.E ? p.R : p.E, rows = p.R / experts;
+  const double filled = p.R / (16.0 * cap) + experts / 2, runs = filled > experts ? filled : experts;
+  const double tiles = runs * ((p.N + (int)bn - 1) / (int)bn);
+  auto work = [&](double r) {
+    const double units = (double)((int64_t)(r + 15) / 16 * 16);
+    const double bytes = r * k * sizeof(T) + bn * P * k * 17 / 32, products = (units + 12) * bn * P * k * 2 / 25;
+    return (sizeof(T) == 4 && products > bytes ? products : bytes) + 49152 * (shares == 2 ? 1.5 : waves == 12 ? 2 : 1);
+  };
+  const double most = (double)((int64_t)(1.6 * rows + 15) / 16 * 16);
+  double one = work(most < 16 * cap ? most : 16 * cap);
+  if (shares == 1 && waves == 4) one *= 1.2;
+  const double all = tiles * work(p.R / runs) / device_cu_count() + one / 4;
+  return (all > one ? all : one) * (waves == 12 ? 1.25 : 1);
+}
+// The same of streaming: the bytes of its tiles, whose 16 weight rows load the routed rows again, and 72 KB; in
+// fp32 its products, 22 bytes an element of 16 weight rows by four routed ones.  A tile's end counts as 128
+// elements of the reduction
+template <typename T, int P>
+double stream_cost(const W4Args& p) {
+  const double experts = p.R < p.E ? p.R : p.E, cus = device_cu_count();
+  if (sizeof(T) == 4) return (p.R / 4.0 + experts / 2) * P * (p.N / kRowsW) * (p.K + 128.0) * 22 / cus;
+  const double filled = (double)p.R / kRowsX + experts / 2, runs = filled > experts ? filled : experts;
+  return runs * (p.N / kRowsW) * (p.K + 128.0) * (8.5 * P + 2 * p.R / runs) / cus + 73728;
+}
+
+// us of the alternatives (waves x shares, 16s a tile): 4 x 1, 6: 89, 4 x 1, 3: 97, 12 x 1, 6: 70 (64 rows an expert,
+// E = 32, K = 4096, N = 1536, gated); 45, 51, 49 (32 rows, E = 64, K = 2048, N = 1024); 4 x 2, 6: 27, 4 x 2, 2: 17
+// (150 rows, E = 4, K = 4096, N = 512); fp32 83 and, 4 x 2, 2: 33 (151 rows, E = 13, K = 1664, N = 192)
+template <typename T, int P>
+TileChoice choose_tile(const W4Args& p) {
+  TileChoice best{4, 1, 6, tile_cost<T, P>(p, 4, 1, 6)};
+  auto consider = [&](int waves, int shares, int cap) {
+    const double c = tile_cost<T, P>(p, waves, shares, cap);
+    if (c < best.cost) best = TileChoice{waves, shares, cap, c};
+  };
+  for (const int cap : {6, 3, 2, 1}) {
+    consider(4, 1, cap);
+    consider(4, 2, cap);
+  }
+  if (sizeof(T) == 2) consider(12, 1, 6);
+  return best;
+}
+
+template <typename T, int P, bool TAIL>
+hipError_t launch_tiles(const W4Args& p, const TileChoice& c, hipStream_t st) {
+  if constexpr (sizeof(T) == 2) {
+    if (c.waves == 12) return launch_tile<T, P, 12, 1, TAIL>(p, c.cap, st);
+  }
+  if (c.shares == 2) return launch_tile<T, P, 4, 2, TAIL>(p, c.cap, st);
+  return launch_tile<T, P, 4, 1, TAIL>(p, c.cap, st);
 }
 
 // Tiles of a streaming workgroup, and so shares of the reduction (8 / tiles): the number that takes the
@@ -705,19 +752,16 @@ int stream_tiles(const W4Args& p, int span) {
 template <typename T, int P>
 hipError_t launch_w4(const W4Args& p, hipStream_t st) {
   if (p.R == 0) return hipSuccess;
-  const int64_t cus = device_cu_count();
-  const TileWork four = tile_work<P>(p, 4);
-  const bool few = sizeof(T) == 4 && four.tiles < cus;
-  if (p.R > (int64_t)p.E * (few ? kStreamMaxRowsFew : kStreamMaxRows)) {
+  // weights that stream past the rows or tiles of many rows, us: 5 / 8.5 (32 rows, E = 1, K = 2048, N = 1024, gated),
+  // 55 / 64 (4 rows, E = 128, the same), 24.5 / 15.3 (8 rows, E = 8, K = 4096, N = 1536), 8.7 / 7.1 (16 rows, E = 8, K =
+  // 1024, N = 2048, not gated); fp32 6.5 / 14.5 (30 rows, E = 2), 13.4 / 14.9 (12 rows, E = 8), 17.2 / 15.2 (16
+  // rows, E = 8; all three K = 1024, N = 1024 or 2048)
+  const TileChoice tile = choose_tile<T, P>(p);
+  if (tile.cost < stream_cost<T, P>(p)) {
     if constexpr (sizeof(T) == 2) {
-      if (p.K % 128 != 0) return launch_tile<T, P, 4, 1, true>(p, st);
-      // 12 waves read the rows a third as often: 88 -> 67 us at 64 rows an expert (E = 32, K = 4096, N = 1536,
-      // gated; the estimate falls to 0.55), 55.5 -> 52 at 16 (0.79); 45 -> 52 where it does not fall (32
-      // rows, E = 64, K = 2048, N = 1024: 1.02)
-      if (4 * tile_work<P>(p, 12).bytes < 3 * four.bytes) return launch_tile<T, P, 12, 1, false>(p, st);
+      if (p.K % 128 != 0) return launch_tiles<T, P, true>(p, tile, st);
     }
-    if (four.tiles <= cus) return launch_tile<T, P, 4, 2, false>(p, st);
-    return launch_tile<T, P, 4, 1, false>(p, st);
+    return launch_tiles<T, P, false>(p, tile, st);
   }
   const int tiles = stream_tiles(p, sizeof(T) == 2 && p.K % 256 == 0 ? 256 : 128);
   if (p.K % 128 != 0) return launch_stream<T, P, 1, true>(p, tiles, st);

@@ -185,7 +185,9 @@ PRODUCTS = [  # T, d, f, E, k
     (16, 320, 64, 3, 1), (17, 128, 192, 2, 2), (33, 64, 64, 130, 8), (61, 448, 128, 4, 2), (200, 256, 64, 7, 3),
     (515, 192, 64, 2, 1), (300, 64, 64, 1024, 32), (700, 128, 128, 1, 1),
     (512, 128, 1536, 32, 4), (640, 4096, 128, 20, 2),  # tiles of 12 waves: gated, and not
-    (40, 128, 1024, 60, 4), (150, 2048, 192, 96, 3), (9, 1280, 448, 31, 7)]  # eight, four and two tiles a workgroup
+    (40, 128, 1024, 60, 4), (150, 2048, 192, 96, 3), (9, 1280, 448, 31, 7),  # eight, four and two tiles a workgroup
+    (342, 1984, 64, 18, 5), (150, 1152, 192, 2, 2), (257, 576, 320, 3, 1), (120, 1664, 192, 13, 4),  # few tiles
+    (500, 320, 1024, 40, 4), (400, 448, 512, 64, 4)]
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
