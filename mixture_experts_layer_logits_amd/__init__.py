@@ -366,15 +366,16 @@ def _call_checked(name, shape, args, stream=None):
     the current one."""
     dev = None
     raw = [] if shape is None else [shape]
+    put = raw.append
     for a in args:
         if type(a) is not tuple:
-            raw.append(a)
+            put(a)
             continue
         arg, t, dtype, n = a
         if t is None:
-            raw.append(None)
+            put(None)
             if dtype is None:
-                raw.append(0)
+                put(0)
             continue
         at = t.get_device()
         if at != dev:
@@ -383,12 +384,16 @@ def _call_checked(name, shape, args, stream=None):
             if dev is not None:
                 raise ValueError(f"{name}: {arg} lives on GPU {at}, the arguments before it on GPU {dev}")
             dev = at
-        if not t.is_contiguous() or (dtype is not None and (t.dtype is not dtype or t.numel() != n)):
-            raise ValueError(f"{name}: {arg} must be contiguous" + ("" if dtype is None else
-                             f", {dtype}, of {n} elements; got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}"))
-        raw.append(t.data_ptr())
         if dtype is None:
-            raw.append(t.numel() * t.element_size())
+            if not t.is_contiguous():
+                raise ValueError(f"{name}: {arg} must be contiguous")
+            put(t.data_ptr())
+            put(t.numel() * t.element_size())
+            continue
+        if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name}: {arg} must be contiguous, {dtype}, of {n} elements; got {t.dtype}, shape "
+                             f"{tuple(t.shape)}, strides {t.stride()}")
+        put(t.data_ptr())
     lib = _lib or load_library()
     st = _launch(getattr(lib, name), dev, stream, raw)
     if st != 0:

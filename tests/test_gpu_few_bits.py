@@ -187,7 +187,8 @@ PRODUCTS = [  # T, d, f, E, k
     (512, 128, 1536, 32, 4), (640, 4096, 128, 20, 2),  # tiles of 12 waves: gated, and not
     (40, 128, 1024, 60, 4), (150, 2048, 192, 96, 3), (9, 1280, 448, 31, 7),  # eight, four and two tiles a workgroup
     (342, 1984, 64, 18, 5), (150, 1152, 192, 2, 2), (257, 576, 320, 3, 1), (120, 1664, 192, 13, 4),  # few tiles
-    (500, 320, 1024, 40, 4), (400, 448, 512, 64, 4)]
+    (500, 320, 1024, 40, 4), (400, 448, 512, 64, 4), (512, 192, 1536, 32, 4), (640, 4096, 192, 20, 2),
+    (300, 1024, 512, 4, 2), (300, 1088, 512, 4, 2)]
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
