@@ -73,6 +73,7 @@ struct W4Args {
   const uint8_t *q0, *s0;   // [E][N][K/2], [E][N][K/32]
   const uint8_t *q1, *s1;   // the second projection (gated)
   void* out;                // [R][N]
+  int cus;                  // compute units (for the choice of tiles, on the host)
 };
 
 // A scale byte as the widening instructions take it: they read the exponent field alone, 0 as 2^-127
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(64 * NW * KS, NW == 12 ? 3 : 2) w4_tile_kernel
 // rows: of a tile, at most
 unsigned w4_grid(const W4Args& p, int rows, int ntn, int per_cu) {
   const int64_t bound = ((int64_t)p.R / rows + (p.R < p.E ? p.R : p.E)) * ntn;  // tiles of any routing
-  const int64_t most = (int64_t)device_cu_count() * per_cu;
+  const int64_t most = (int64_t)p.cus * per_cu;
   const int64_t g = bound < most ? bound : most;
   return (unsigned)(g < 64 ? g : (g + 63) / 64 * 64);
 }
@@ -681,14 +682,14 @@ double tile_cost(const W4Args& p, int waves, int shares, int cap) {
   const double filled = p.R / (16.0 * cap) + experts / 2, runs = filled > experts ? filled : experts;
   const double tiles = runs * ((p.N + (int)bn - 1) / (int)bn);
   auto work = [&](double r) {
-    const double units = (double)((int64_t)(r + 15) / 16 * 16);
+    const double units = ((int)r + 15) / 16 * 16;
     const double bytes = r * k * sizeof(T) + bn * P * k * 17 / 32, products = (units + 12) * bn * P * k * 2 / 25;
     return (sizeof(T) == 4 && products > bytes ? products : bytes) + 49152 * (shares == 2 ? 1.5 : waves == 12 ? 2 : 1);
   };
-  const double most = (double)((int64_t)(1.6 * rows + 15) / 16 * 16);
-  double one = work(most < 16 * cap ? most : 16 * cap);
+  const double most = 1.6 * rows < 16 * cap ? ((int)(1.6 * rows) + 15) / 16 * 16 : 16 * cap;
+  double one = work(most);
   if (shares == 1 && waves == 4) one *= 1.2;
-  const double all = tiles * work(p.R / runs) / device_cu_count() + one / 4;
+  const double all = tiles * work(p.R / runs) / p.cus + one / 4;
   return (all > one ? all : one) * (waves == 12 ? 1.25 : 1);
 }
 // The same of streaming: the bytes of its tiles, whose 16 weight rows load the routed rows again, and 72 KB; in
@@ -696,7 +697,7 @@ double tile_cost(const W4Args& p, int waves, int shares, int cap) {
 // elements of the reduction
 template <typename T, int P>
 double stream_cost(const W4Args& p) {
-  const double experts = p.R < p.E ? p.R : p.E, cus = device_cu_count();
+  const double experts = p.R < p.E ? p.R : p.E, cus = p.cus;
   if (sizeof(T) == 4) return (p.R / 4.0 + experts / 2) * P * (p.N / kRowsW) * (p.K + 128.0) * 22 / cus;
   const double filled = (double)p.R / kRowsX + experts / 2, runs = filled > experts ? filled : experts;
   return runs * (p.N / kRowsW) * (p.K + 128.0) * (8.5 * P + 2 * p.R / runs) / cus + 73728;
@@ -737,7 +738,7 @@ hipError_t launch_tiles(const W4Args& p, const TileChoice& c, hipStream_t st) {
 // K = 256, N = 2048).
 int stream_tiles(const W4Args& p, int span) {
   const int64_t experts = p.R < p.E ? p.R : p.E, rows = (p.R + experts - 1) / experts;
-  const int64_t all = experts * ((rows + kRowsX - 1) / kRowsX) * (p.N / kRowsW), fit = device_cu_count();
+  const int64_t all = experts * ((rows + kRowsX - 1) / kRowsX) * (p.N / kRowsW), fit = p.cus;
   int best = 1;
   int64_t least = INT64_MAX;
   for (int tiles = 1; tiles <= kStreamWaves; tiles *= 2) {
@@ -788,13 +789,13 @@ hipError_t mx4_quantize_rows(int eb, int rows, int cols, const void* src, uint8_
 
 hipError_t gemm1_fwd_w4(int eb, const GemmShape& g, const int* offsets, const void* X, const uint8_t* W1q,
                         const uint8_t* W1s, const uint8_t* W3q, const uint8_t* W3s, void* h, hipStream_t st) {
-  const W4Args p{g.R, g.d, g.f, g.E, offsets, X, W1q, W1s, W3q, W3s, h};
+  const W4Args p{g.R, g.d, g.f, g.E, offsets, X, W1q, W1s, W3q, W3s, h, device_cu_count()};
   return eb == 2 ? launch_w4<bf16_t, 2>(p, st) : launch_w4<float, 2>(p, st);
 }
 
 hipError_t gemm2_fwd_w4(int eb, const GemmShape& g, const int* offsets, const void* H, const uint8_t* W2q,
                         const uint8_t* W2s, void* Y, hipStream_t st) {
-  const W4Args p{g.R, g.f, g.d, g.E, offsets, H, W2q, W2s, nullptr, nullptr, Y};
+  const W4Args p{g.R, g.f, g.d, g.E, offsets, H, W2q, W2s, nullptr, nullptr, Y, device_cu_count()};
   return eb == 2 ? launch_w4<bf16_t, 1>(p, st) : launch_w4<float, 1>(p, st);
 }
 
