@@ -511,8 +511,8 @@ moe_status moe_mx4_quantize(int32_t rows, int32_t cols, int32_t act, const void*
 /* h = silu(a) b with a = X_e W1_e^T, b = X_e W3_e^T in one kernel (a and b are not stored).
  * x_perm [R, d] act, h [R, f] act written.  The rows are not quantised: the weights widen
  * without a rounding and the sums are float (act MOE_BF16: bf16 products; MOE_F32: float).
- * moe_shape.gemm plays no part.  d and f at most 2^22.  Up to five rows per expert (on average)
- * the weights stream past the rows; for more, tiles of up to 96 rows share each weight. */
+ * moe_shape.gemm plays no part.  d and f at most 2^22.  Few rows per expert stream the weights
+ * past the rows; for more, tiles of up to 96 rows share each weight. */
 moe_status moe_ffn_gemm1_fwd_w4(const moe_shape* s, const void* x_perm, const uint8_t* W1q, const uint8_t* W1s,
                                 const uint8_t* W3q, const uint8_t* W3s, const int32_t* offsets, void* h,
                                 void* stream);

@@ -360,10 +360,10 @@ def moe_ffn_dgrad1_mx(shape, dabq_rows, dabs_rows, W1, W3, offsets, dx_perm, ws,
 # ------------------------------------------------------------------ around the layer
 def _call_checked(name, shape, args, stream=None):
     """Call `name` with shape (None: the call takes none) and args in the C call's order: a tensor as
-    (argument name, tensor or None, dtype, number of elements), anything else as it is.  Tensors have to lie on one GPU, contiguous, of
-    that type and size (dtype None: a workspace of any type, whose size in bytes is passed on
-    behind it).  The call runs on that GPU's current stream if none is given, whichever device is
-    the current one."""
+    (argument name, tensor or None, dtype, number of elements), anything else as it is.  Tensors have to
+    lie on one GPU, contiguous, of that type and size (dtype None: a workspace of any type, whose
+    size in bytes is passed on behind it).  The call runs on that GPU's current stream if none is
+    given, whichever device is the current one."""
     dev = None
     raw = [] if shape is None else [shape]
     put = raw.append

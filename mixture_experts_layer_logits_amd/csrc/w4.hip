@@ -26,7 +26,7 @@ __device__ __forceinline__ int mx4_scale_exp(float amax) {
   return s < -126 ? -126 : s;
 }
 
-// one thread per block of 32
+// one thread per block of 32.  Bound by HBM: 128 x 1024 x 2048 in bf16 takes 117 us (5.8 TB/s read and written)
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_quantize_kernel(int64_t nblk, const T* __restrict__ src,
                                                            uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
@@ -118,10 +118,10 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 
 // The tiles of a launch: an expert's rows in runs of at most kRowsX where UNIT is 8, of even shares of at most
-// `cap` whole 16s where UNIT is 16 (cap_inv: 2^32 / cap, rounded up), its weight rows in ntn tiles; the runs that share a weight tile follow one another.  Every wave finds
-// its tiles by itself, so no barrier stands before the first load: a lane holds two experts of a window
-// of 128, whose run counts are scanned in registers, and as tiles are asked for in ascending order the
-// window only moves forward.
+// `cap` whole 16s where UNIT is 16 (cap_inv: 2^32 / cap, rounded up), its weight rows in ntn tiles; the runs
+// that share a weight tile follow one another.  Every wave finds its tiles by itself, so no barrier stands
+// before the first load: a lane holds two experts of a window of 128, whose run counts are scanned in
+// registers, and as tiles are asked for in ascending order the window only moves forward.
 struct W4Tile {
   int e, m0, m_end, nt;  // e < 0: past the last tile
 };
@@ -192,7 +192,10 @@ __device__ __forceinline__ int first_tile() {
 // `tiles` neighbouring tiles by 8 / tiles shares of the reduction, taken piece by piece; the shares' sums
 // are added through LDS in order.  Each wave loads its next piece, of this tile or the next, before it
 // multiplies the one it has; the routed rows' part comes in whole rows (a load for two of them) and is
-// handed to the lanes through LDS of the wave's own.
+// handed to the lanes through LDS of the wave's own.  What bounds it where most experts have a row or two is
+// HBM: 34 to 40 us for the 183 MB of T = 32, k = 4, E = 128, d = 2048, f = 1024, gated (4.6 to 5.4 TB/s), 19.4 us for
+// the 92 MB of the second product; for one token the launch and two round trips to memory (offsets, then
+// weights), 5.3 us.
 constexpr int kStreamWaves = 8;
 constexpr int kRowsW = 16;          // weight rows of a tile
 constexpr int kRowsX = 8;           // routed rows of a tile
@@ -263,7 +266,8 @@ struct Stream {
   __device__ __forceinline__ void load_rows(u32x4 (&x)[XL], const W4Tile& t, int k) const {
     const uint32_t row = a.K * sizeof(T);
     const uint32_t o = k * sizeof(T) + (lane % LPR) * 16;
-    const auto r = buffer(static_cast<const T*>(a.X) + (int64_t)t.m0 * a.K, t.e >= 0 && k < a.K ? (t.m_end - t.m0) * row : 0);
+    const auto r = buffer(static_cast<const T*>(a.X) + (int64_t)t.m0 * a.K,
+                          t.e >= 0 && k < a.K ? (t.m_end - t.m0) * row : 0);
 #pragma unroll
     for (int i = 0; i < XL; i++)
       x[i] = __builtin_amdgcn_raw_buffer_load_b128(r, !TAIL || o < row ? (i * RPL + lane / LPR) * row + o : kNowhere, 0, 0);
@@ -430,9 +434,11 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
 // A workgroup of NW waves takes 16 NW weight rows of both projections (gated) or 32 NW of one, 2 x 16 a
 // wave, by up to 96 routed rows.  256 bytes of every routed row are staged in LDS (16-byte chunks
 // exchanged by the row's number, so that 16 rows at one place fall on distinct banks) while the 256
-// before are multiplied; rows and weights are loaded into registers two steps ahead.  What bounds it are
+// before are multiplied; rows are loaded into registers two steps ahead, weights three.  What bounds it are
 // the bytes that a compute unit loads, weights or rows, from the L2 or from memory (about 24 a
-// nanosecond, at most): launch_w4 picks the NW that loads fewest.
+// nanosecond, at most), in fp32 the products: choose_tile picks the tile that needs least of both.  66 to 72 us
+// at 64 rows an expert, E = 32, K = 4096, N = 1536, gated, in bf16 (237 MB and 52 GFLOP; 318 MB read from HBM),
+// 13.7 us at 128 rows, E = 8, K = 1024, N = 2048.
 constexpr int kTileRows = 96;
 
 template <typename T>
@@ -622,6 +628,7 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
   }
 }
 
+// KS: shares of the reduction, each NW waves (2 where tiles are few: a compute unit loads for one tile alone)
 template <typename T, int P, int NW, int KS, bool TAIL>
 __global__ void __launch_bounds__(64 * NW * KS, NW == 12 ? 3 : 2) w4_tile_kernel(W4Args a, int cap, uint32_t cap_inv) {
   constexpr int BN = 32 * NW / P;
