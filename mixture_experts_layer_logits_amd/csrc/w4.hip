@@ -221,38 +221,54 @@ struct Stream {
   const W4Args& a;
   int lane, wr, grp;
 
-  __device__ __forceinline__ void load_codes(Piece& c, const W4Tile& t, int col, int k) const {
-    c.live = t.e >= 0 && k < a.K;
-    const int64_t wrow = (int64_t)(t.e >= 0 ? t.e : 0) * a.N + col;
+  // Where a tile's weight rows from `col` on and its routed rows lie (past the last tile: nowhere)
+  struct Source {
+    __amdgpu_buffer_rsrc_t q[P], s[P], x;
+  };
+  __device__ __forceinline__ Source source(const W4Tile& t, int col) const {
     const uint8_t* const qs[2] = {a.q0, a.q1};
-    const uint32_t qb = a.K / 2;  // bytes of a row
+    const uint8_t* const ss[2] = {a.s0, a.s1};
+    const bool in = t.e >= 0;
+    const int64_t wrow = (int64_t)(in ? t.e : 0) * a.N + col;
+    const uint32_t qb = a.K / 2, sb = a.K / kMx4Block, row = a.K * sizeof(T);  // bytes of a row
+    Source r;
 #pragma unroll
     for (int h = 0; h < P; h++) {
-      const auto q = buffer(qs[h] + wrow * qb, c.live ? kRowsW * qb : 0);
-      const uint32_t qo = !TAIL || k + 32 * grp < a.K ? wr * qb + (k + 32 * grp) / 2 : kNowhere;
+      r.q[h] = buffer(qs[h] + wrow * qb, in ? kRowsW * qb : 0);
+      r.s[h] = buffer(ss[h] + wrow * sb, in ? kRowsW * sb : 0);
+    }
+    r.x = buffer(static_cast<const T*>(a.X) + (int64_t)t.m0 * a.K, in ? (t.m_end - t.m0) * row : 0);
+    return r;
+  }
+  // Past the reduction's end an offset is past any buffer: kFar + a lane's own, without a wrap
+  static constexpr uint32_t kFar = 0x80000000u;
+
+  __device__ __forceinline__ void load_codes(Piece& c, const Source& src, bool live, int k) const {
+    c.live = live && k < a.K;
+    const uint32_t at = k < a.K ? k / 2 : kFar;
+    const uint32_t qo = !TAIL || k + 32 * grp < a.K ? wr * (a.K / 2) + 16 * grp + at : kNowhere;
+#pragma unroll
+    for (int h = 0; h < P; h++) {
 #pragma unroll
       for (int b = 0; b < NB; b++) {
-        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(q, qo + 64 * b, 0, 0);
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src.q[h], qo + 64 * b, 0, 0);
         c.q[h][4 * b] = v.x, c.q[h][4 * b + 1] = v.y, c.q[h][4 * b + 2] = v.z, c.q[h][4 * b + 3] = v.w;
       }
     }
   }
-  __device__ __forceinline__ void load_scales(Scales& c, const W4Tile& t, int col, int k) const {
-    const int64_t wrow = (int64_t)(t.e >= 0 ? t.e : 0) * a.N + col;
-    const uint8_t* const ss[2] = {a.s0, a.s1};
+  __device__ __forceinline__ void load_scales(Scales& c, const Source& src, int k) const {
     const uint32_t sb = a.K / kMx4Block, at = k / kMx4Block + SB * grp, so = wr * sb + at;
 #pragma unroll
     for (int h = 0; h < P; h++) {
-      const auto s = buffer(ss[h] + wrow * sb, t.e >= 0 && k < a.K ? kRowsW * sb : 0);
       if constexpr (TAIL) {
         // past the row's end the next row's, which may be NaN
-        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b16(s, at < sb ? so : kNowhere, 0, 0);
-        c.hi[h] = __builtin_amdgcn_raw_buffer_load_b16(s, at + 2 < sb ? so + 2 : kNowhere, 0, 0);
+        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b16(src.s[h], at < sb ? so : kNowhere, 0, 0);
+        c.hi[h] = __builtin_amdgcn_raw_buffer_load_b16(src.s[h], at + 2 < sb ? so + 2 : kNowhere, 0, 0);
       } else if constexpr (NB == 2) {
-        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(s, so, 0, 0);
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(src.s[h], so, 0, 0);
         c.w[h][0] = v.x, c.w[h][1] = v.y;
       } else {
-        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b32(s, so, 0, 0);
+        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b32(src.s[h], so, 0, 0);
       }
     }
   }
@@ -263,14 +279,13 @@ struct Stream {
     return mx4_scale(w >> (8 * grp) & 255);
   }
 
-  __device__ __forceinline__ void load_rows(u32x4 (&x)[XL], const W4Tile& t, int k) const {
-    const uint32_t row = a.K * sizeof(T);
-    const uint32_t o = k * sizeof(T) + (lane % LPR) * 16;
-    const auto r = buffer(static_cast<const T*>(a.X) + (int64_t)t.m0 * a.K,
-                          t.e >= 0 && k < a.K ? (t.m_end - t.m0) * row : 0);
+  __device__ __forceinline__ void load_rows(u32x4 (&x)[XL], const Source& src, int k) const {
+    const uint32_t row = a.K * sizeof(T), o = (lane % LPR) * 16;
+    const uint32_t at = (lane / LPR) * row + o + (k < a.K ? k * sizeof(T) : kFar);
 #pragma unroll
     for (int i = 0; i < XL; i++)
-      x[i] = __builtin_amdgcn_raw_buffer_load_b128(r, !TAIL || o < row ? (i * RPL + lane / LPR) * row + o : kNowhere, 0, 0);
+      x[i] = __builtin_amdgcn_raw_buffer_load_b128(
+          src.x, !TAIL || o + k * sizeof(T) < row ? i * RPL * row + at : kNowhere, 0, 0);
   }
   // 16-byte chunks of a row are exchanged by its number: the 8 rows' at one place are on distinct banks
   __device__ __forceinline__ void hand_over(const u32x4 (&x)[XL], u32x4 (*s)[LPR]) const {
@@ -350,9 +365,10 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
   typename S::Piece even, odd;
   typename S::Scales now, then;  // of the pieces in hand, and of those behind them
   u32x4 x[S::XL];
-  st.load_scales(then, tile, column(tile), first(0));
-  st.load_rows(x, tile, first(0));
-  st.load_codes(even, tile, column(tile), first(0));
+  typename S::Source src = st.source(tile, column(tile));  // of the tile ahead
+  st.load_scales(then, src, first(0));
+  st.load_rows(x, src, first(0));
+  st.load_codes(even, src, true, first(0));
   // multiplies `cur` while the piece behind it loads into `nxt`; false behind the last tile
   auto step = [&](const typename S::Piece& cur, typename S::Piece& nxt) __attribute__((always_inline)) {
     st.hand_over(x, s_x[wave]);
@@ -363,11 +379,12 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
       it = 0;
       t += gridDim.x;
       ahead = finder.find(t);
+      src = st.source(ahead, column(ahead));
     }
     const bool group = it % GROUP == 0;
-    if (group) st.load_scales(then, ahead, column(ahead), first(it));
-    st.load_rows(x, ahead, first(it));
-    st.load_codes(nxt, ahead, column(ahead), first(it));
+    if (group) st.load_scales(then, src, first(it));
+    st.load_rows(x, src, first(it));
+    st.load_codes(nxt, src, ahead.e >= 0, first(it));
     wave_lds_fence();
     if (cur.live) st.multiply(cur, now, at, s_x[wave], tile.m_end - tile.m0, acc);
     wave_lds_fence();
