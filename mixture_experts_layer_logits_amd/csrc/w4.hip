@@ -214,9 +214,10 @@ struct Stream {
     bool live;  // the wave has this piece (the same in all lanes)
   };
   // Scale bytes of four pieces that follow one another: lane l holds those of piece l / 16, row l % 16, so
-  // that a row's come in one load; TAIL: in two, as K / 32 may be an odd number of pairs
+  // that a row's come in one load.  TAIL, where K / 32 is an odd number of pairs: the 8 aligned bytes that hold
+  // the 4 (not past the tile's end), until settle
   struct Scales {
-    uint32_t w[P][NB], hi[TAIL ? P : 1];
+    uint32_t w[P][TAIL ? 2 : NB];
   };
   const W4Args& a;
   int lane, wr, grp;
@@ -256,14 +257,17 @@ struct Stream {
       }
     }
   }
+  static __device__ __forceinline__ uint32_t aligned(uint32_t so, uint32_t sb) {
+    const uint32_t last = kRowsW * sb - 8, down = so & ~3u;
+    return down < last ? down : last;
+  }
   __device__ __forceinline__ void load_scales(Scales& c, const Source& src, int k) const {
     const uint32_t sb = a.K / kMx4Block, at = k / kMx4Block + SB * grp, so = wr * sb + at;
 #pragma unroll
     for (int h = 0; h < P; h++) {
       if constexpr (TAIL) {
-        // past the row's end the next row's, which may be NaN
-        c.w[h][0] = __builtin_amdgcn_raw_buffer_load_b16(src.s[h], at < sb ? so : kNowhere, 0, 0);
-        c.hi[h] = __builtin_amdgcn_raw_buffer_load_b16(src.s[h], at + 2 < sb ? so + 2 : kNowhere, 0, 0);
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(src.s[h], at < sb ? aligned(so, sb) : kNowhere, 0, 0);
+        c.w[h][0] = v.x, c.w[h][1] = v.y;
       } else if constexpr (NB == 2) {
         const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(src.s[h], so, 0, 0);
         c.w[h][0] = v.x, c.w[h][1] = v.y;
@@ -272,10 +276,22 @@ struct Stream {
       }
     }
   }
+  // The loaded scales of the pieces from k on, as `scale` takes them
+  __device__ __forceinline__ void settle(Scales& to, const Scales& c, int k) const {
+    if constexpr (!TAIL) {
+      to = c;
+    } else {
+      const uint32_t sb = a.K / kMx4Block, at = k / kMx4Block + SB * grp, so = wr * sb + at;
+#pragma unroll
+      for (int h = 0; h < P; h++) {
+        const uint32_t w = (uint32_t)(((uint64_t)c.w[h][1] << 32 | c.w[h][0]) >> (8 * (so - aligned(so, sb)) & 63));
+        to.w[h][0] = at + 2 < sb ? w : w & 0xffff;  // past the row's end lies the next row's, which may be NaN
+      }
+    }
+  }
   // The scale of projection h's block b of the p-th of the four pieces, as the widening instructions take it
   __device__ __forceinline__ float scale(const Scales& c, int p, int h, int b) const {
-    const uint32_t w =
-        __builtin_amdgcn_ds_bpermute(4 * (16 * p + wr), TAIL ? c.w[h][0] | c.hi[h] << 16 : c.w[h][b]);
+    const uint32_t w = __builtin_amdgcn_ds_bpermute(4 * (16 * p + wr), c.w[h][b]);
     return mx4_scale(w >> (8 * grp) & 255);
   }
 
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
   auto step = [&](const typename S::Piece& cur, typename S::Piece& nxt) __attribute__((always_inline)) {
     st.hand_over(x, s_x[wave]);
     const int at = it % GROUP;
-    if (at == 0) now = then;  // here, behind the rows, which were loaded after them: the copy waits for nothing else
+    if (at == 0) st.settle(now, then, first(it));  // here, behind the rows, which were loaded after them: the copy waits for nothing else
     const bool last = ++it == iters;
     if (last) {
       it = 0;
@@ -551,7 +567,7 @@ __device__ __forceinline__ void do_tile(const W4Args& a, const W4Tile& tile, u32
       }
     }
   };
-  // a row's scale bytes of four steps come in one load (TAIL: two, see Stream), a step's to each of its four lanes
+  // a row's scale bytes of four steps come in one load (TAIL: two), a step's to each of its four lanes
   auto load_s = [&](int step, int set) __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < 2; h++) {
