@@ -529,9 +529,10 @@ moe_status moe_ffn_gemm2_fwd_w4(const moe_shape* s, const void* h, const uint8_t
  *
  * MXINT8 rows: codes q in [-127, 127] (int8) and one scale byte b per 32 elements along the
  * row: value = q 2^(b - 133).  2^(b - 127) is the smallest power of two with
- * amax <= 127/64 2^(b - 127), not below 2^-120; q is rounded to nearest, ties to even.  255
- * stands for a block of NaN (a block with an infinity or NaN becomes one).  An element is off by
- * at most amax / 127 of its block.  Every buffer is 16-byte aligned.
+ * amax <= 127/64 2^(b - 127), not below 2^-120 and not above 2^127; q is rounded to nearest, ties to
+ * even, and held to [-127, 127] where amax passes 127/64 2^127.  255 stands for a block of NaN (a
+ * block with an infinity or NaN becomes one).  An element is off by at most amax / 127 of its
+ * block, or 2^-127 where that is more (amax < 127 2^-127).  Every buffer is 16-byte aligned.
  * --------------------------------------------------------------------------------------- */
 
 /* rows x cols elements of `act` (MOE_F32 or MOE_BF16) <-> MXINT8 rows, q [rows, cols], scales

@@ -2,11 +2,14 @@
 // 8-bit activation checkpoints (shared by the row kernels and by the GEMM epilogues).
 //
 // Value = q 2^(s - 6) with a whole q in [-127, 127] and one byte s + 127 per block.  2^s is the
-// smallest power of two with amax <= 127/64 2^s (so q never saturates), not below 2^-120 (the
-// factor 2^(6 - s) stays a normal number); q = round(v 2^(6 - s)), ties to even, off by at most
-// amax / 127 from v.  A block that holds an infinity or NaN gets the byte 255 and comes back as
-// NaN in all its elements.  Whole 8-bit steps instead of E4M3's three mantissa bits: a gradient
-// formed from the checkpoint sees 0.6% noise (rms over normal data) instead of 2.6%.
+// smallest power of two with amax <= 127/64 2^s, not below 2^-120 (the factor 2^(6 - s) stays a
+// normal number) and not above 2^127 (the last byte); q = round(v 2^(6 - s)), ties to even, held at
+// 127 in the one case where it would pass it, amax above 127/64 2^127.  A value is off by at most
+// half a step, 2^(s - 7): that is max(amax / 127, 2^-127), since amax > 127/128 2^s above the lowest
+// s, and a held one by less than 2^128 - 127 2^121 = 2^121 < amax / 127.  A block that holds an
+// infinity or NaN gets the byte 255 and comes back as NaN in all its elements.  Whole 8-bit steps
+// instead of E4M3's three mantissa bits: a gradient formed from the checkpoint sees 0.6% noise (rms
+// over normal data) instead of 2.6%.
 #pragma once
 #include "common.h"
 
