@@ -525,8 +525,8 @@ class MoEBlock:
     again.  A layer with the MXFP8 dispatch writes its routed gradient rows in E4M3 from dy, and one
     with 8-bit checkpoints keeps its routed outputs in the combine, so there the combine and the norm
     are separate calls and y is stored.  Over a layer with 4-bit weights the block serves: it has no
-    backward.  The block owns its buffers and holds one
-    forward at a time, like its layer, and its calls run on the current stream."""
+    backward, and no buffers for one.  The block owns its buffers and holds one forward at a time, like
+    its layer, and its calls run on the current stream."""
 
     def __init__(self, layer: MoEExpertLayer, res_scale=1.0, eps=1e-6):
         self.layer, self.res_scale, self.eps = layer, float(res_scale), float(eps)
@@ -535,6 +535,9 @@ class MoEBlock:
         e, T, d, f32 = layer._e, layer.T, layer.d, torch.float32
         self.xn, self.v, self.xn_next = e(T, d), e(T, d), e(T, d)
         self.rstd_pre, self.rstd_post, self.rstd_next = e(T, dtype=f32), e(T, dtype=f32), e(T, dtype=f32)
+        self.dv = self.dh = self.dy = self.dgate = self.dw_pre = self.dw_post = self.dw_next = None
+        if layer.weights4:  # serves: no backward
+            return
         self.dv, self.dh, self.dy = e(T, d), e(T, d), e(T, d)
         self.dgate = e(T, dtype=f32)
         self.dw_pre, self.dw_post, self.dw_next = e(d, dtype=f32), e(d, dtype=f32), e(d, dtype=f32)
