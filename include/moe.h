@@ -44,9 +44,12 @@
  *    and loader waves than the measured defaults.  Each is read from the environment once,
  *    at the first launch that consults it, and kept until moe_tuning_reload.  They
  *    change only how the work is tiled and scheduled: every output element is still one fp32
- *    reduction over the same values in ascending order of the reduction index.  The products
- *    with 4-bit weights and the GEMMs of the 8-bit checkpoints choose their tiles by the sizes
- *    alone.
+ *    reduction over the same values in ascending order of the reduction index.  The GEMMs of the
+ *    8-bit checkpoints choose their tiles by the sizes alone, with the same reduction.
+ *  - The products with 4-bit weights choose tiles by the sizes as well, and with them in how many
+ *    parts (up to eight) and in which order the reduction is summed, in fp32.  A call repeats bit for
+ *    bit; a row's output is not the same to the bit in batches of other sizes (each is as near to the
+ *    exact sum).
  *  - Limits: 1 <= k <= E <= 1024, T*k < 2^31, d and f multiples of 64; with MOE_MXFP8
  *    GEMMs d and f must be multiples of 128.  bf16 buffers need 16-byte alignment.
  */

@@ -64,3 +64,31 @@ def test_each_piece_of_a_row_meets_its_own_weights(T, K, N, E, dtype):
         hw = ref.silu(a) * a
     tol = ((16 + np.abs(a)) * STEP + torch.finfo(dtype).eps / 2) * np.abs(hw) + 2.0 ** -126 * (a * a + 1)
     assert torch.equal(h, h2) and (np.abs(_f64(h) - hw) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("K,N,E", [(2048, 512, 4), (1088, 192, 3), (4096, 256, 16)])
+def test_a_row_in_batches_of_many_sizes(K, N, E, dtype):
+    """The products split the reduction by the sizes of the batch, so a row's output is not the same to the bit
+    in every batch: each lies within its own bound of the exact sum, and a batch repeats bit for bit."""
+    m = _m()
+    g = torch.Generator().manual_seed(K)
+    x = torch.randn(700 * E, K, generator=g).to(dtype).cuda()
+    w = 0.05 * torch.randn(E, N, K, generator=g)
+    q, sc = m.quantize_weights(w.cuda())[0]
+    v = ref.mx4_values(host(q), host(sc))
+    for per in (1, 2, 9, 33, 96, 97, 700):
+        say(f"[gpu] batch rows={per} E={E} K={K} {dtype}")
+        T = per * E
+        rows = x.view(E, 700, K)[:, :per].reshape(T, K).contiguous()
+        off = torch.arange(0, T + 1, per, dtype=torch.int32)
+        s = m.make_shape(T, N, K, E, 1, m.MOE_F32 if dtype == torch.float32 else m.MOE_BF16)
+        y = torch.empty(T, N, dtype=dtype, device="cuda")
+        z = torch.full_like(y, 3)
+        m.moe_ffn_gemm2_fwd_w4(s, rows, q, sc, off.cuda(), y)
+        m.moe_ffn_gemm2_fwd_w4(s, rows, q, sc, off.cuda(), z)
+        assert torch.equal(y, z)
+        xv = _f64(rows)
+        want = ref.grouped(xv, v, off)
+        bound = (K + 16) * STEP * ref.grouped(np.abs(xv), np.abs(v), off) + torch.finfo(dtype).eps / 2 * np.abs(want)
+        assert (np.abs(_f64(y) - want) <= bound + 2.0 ** -133).all()
