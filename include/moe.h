@@ -50,7 +50,7 @@
  *    parts (up to eight) and in which order the reduction is summed, in fp32.  A call repeats bit for
  *    bit; a row's output is not the same to the bit in batches of other sizes (each is as near to the
  *    exact sum).
- *  - Limits: 1 <= k <= E <= 1024, T*k < 2^31, d and f multiples of 64; with MOE_MXFP8
+ *  - Limits: 1 <= k <= 32, k <= E <= 1024, T*k < 2^31, d and f multiples of 64; with MOE_MXFP8
  *    GEMMs d and f must be multiples of 128.  bf16 buffers need 16-byte alignment.
  */
 #ifndef MOE_MI355X_H
