@@ -63,8 +63,9 @@ section "Παραλληλισμός, Ακρίβεια και Τεχνικές Μ
 and writes h again for wgrad2 (moe_ffn_dgrad2_c8); the combine keeps the routed outputs as MXINT8
 (moe_combine_c8) and its backward reads them (moe_combine_bwd_c8); x_perm is gathered again from
 the layer's input before wgrad1.  Next to ``recompute`` this holds less and runs no GEMM twice, at
-the price of the checkpoint's 8 bits in the gradients (the forward is the same, bit for bit).  Where
-GEMM1 or dgrad2 does not run bf16 the rows go through moe_ckpt8_pack and moe_ckpt8_unpack instead.
+the price of the checkpoint's 8 bits in the gradients (the layer's forward is the same, bit for bit; a
+block's carries one rounding more, see MoEBlock).  Where GEMM1 or dgrad2 does not run bf16 the rows go
+through moe_ckpt8_pack and moe_ckpt8_unpack instead.
 
 4-bit weights (``weights4=True``, serving: no backward): W1, W3, W2 are given as the (codes, scales)
 pairs that ``quantize_weights`` makes, and the expert products are moe_ffn_gemm1_fwd_w4 and
@@ -486,7 +487,8 @@ class MoEExpertLayer:
         """Bytes of expert-FFN activations held from the forward to the backward: the
         routed rows (x_perm, or with the MXFP8 dispatch their two E4M3 layouts with
         scales), y_perm, and ab and h unless they are recomputed.  With ckpt8 the 8-bit ab and
-        y_perm in their place (and no bf16 routed rows)."""
+        y_perm in their place (and no bf16 routed rows).  Of the layer alone: a block holds more
+        (MoEBlock)."""
         if self.weights4:
             return 0
         eb = self.y.element_size()
@@ -524,7 +526,8 @@ class MoEBlock:
     y is never stored: the combine's norm takes it from registers and the backward gathers it
     again.  A layer with the MXFP8 dispatch writes its routed gradient rows in E4M3 from dy, and one
     with 8-bit checkpoints keeps its routed outputs in the combine, so there the combine and the norm
-    are separate calls and y is stored.  Over a layer with 4-bit weights the block serves: it has no
+    are separate calls and y is stored: v and xn_next follow from y rounded to the layer's type
+    instead of from the fp32 sum, and y [T, d] is held until the backward.  Over a layer with 4-bit weights the block serves: it has no
     backward, and no buffers for one.  The block owns its buffers and holds one forward at a time, like
     its layer, and its calls run on the current stream."""
 
