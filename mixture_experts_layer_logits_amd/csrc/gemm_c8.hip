@@ -39,11 +39,23 @@ struct ProbDgrad2C8 : ProbDgrad2 {
   }
 };
 
-// Tiles (us below are of the named alternatives, in a graph).  128 x 256 with four loader waves, 64 deep in
-// three stages, where they fill the rounds of one tile a compute unit: 455 against 483 with 128 x 128 for
-// GEMM1 and 275 against 293 for dgrad2 at E = 128, R = 32768, d = 2048, f = 1024.  Where the last round or
-// the last columns stand empty 128 x 128 (8 waves, two workgroups a compute unit) is faster: GEMM1 118 against 127
-// (0.82 filled) but 194 against 197 (0.85), dgrad2 63 against 78 (0.69) but 192 against 176 (0.75).
+// Tiles (us below are medians of graph replays in turn, of the named alternatives).  128 x 256 with four loader
+// waves, 64 deep in three stages, where they fill the rounds of one tile a compute unit: 432 against 454 with
+// 128 x 128 for GEMM1 and 272 against 291 for dgrad2 at E = 128, R = 32768, d = 2048, f = 1024 (the plain calls
+// 399 and 272).  Where the last round or the last columns stand empty 128 x 128 (8 waves, two workgroups a compute
+// unit) is faster: 57 against 65 for GEMM1 (0.69 filled) and 41 against 52 for dgrad2 (0.52) at R = 16384, E = 4, d =
+// 1024, f = 512.  Between the two the thresholds lie on the side of 128 x 128: at E = 8, d = 2048 GEMM1 takes 121
+// with it against 112 (0.84 filled, three rounds of f = 256, just below its threshold) and 118 against 115 (0.86,
+// just above), dgrad2 113 against 100 (0.72, two rounds of f = 256) and 118 against 106 (0.76).  A launch of at
+// most one round takes 128 x 128 at any fill: 128 x 256 measured 1 to 8% less there with E = 1 and from 2% more to 4%
+// less with E = 4 (R = 4352 to 15872, d = 2048).
+//
+// The larger tiles that the plain GEMMs take for 1024 rows an expert and more are not built for these epilogues.
+// 256 x 256 (64 deep, two stages): GEMM1 347 against 334 with 128 x 256 at R = 32768, E = 8, d = 2048, f = 1024 (plain 309),
+// but 2115 against 2183 at R = 65536, E = 32, d = 4096, f = 2048 (plain 2117); dgrad2 290 against 232 and 1421 against
+// 1276.  192 x 256 (32 deep, three stages, loader waves): GEMM1 320 and 2158, dgrad2, which spills 28 registers
+// with the codes, 367 and 2336.  There the coded dgrad2 is slower than the plain one, which has those tiles
+// (190 and 1189).
 //
 // Tiles of a launch for the worst routing, and whether 128 x 256 ones use num / den of their rounds
 static int64_t c8_tiles(const GemmShape& s, int N, int bm, int bn) {
