@@ -466,11 +466,18 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) w4_stream_kernel(W4Args 
 // A workgroup of NW waves takes 16 NW weight rows of both projections (gated) or 32 NW of one, 2 x 16 a
 // wave, by up to 96 routed rows.  256 bytes of every routed row are staged in LDS (16-byte chunks
 // exchanged by the row's number, so that 16 rows at one place fall on distinct banks) while the 256
-// before are multiplied; rows are loaded into registers two steps ahead, weights three.  What bounds it are
-// the bytes that a compute unit loads, weights or rows, from the L2 or from memory (about 24 a
-// nanosecond, at most), in fp32 the products: choose_tile picks the tile that needs least of both.  66 to 72 us
-// at 64 rows an expert, E = 32, K = 4096, N = 1536, gated, in bf16 (237 MB and 52 GFLOP; 318 MB read from HBM),
-// 13.7 us at 128 rows, E = 8, K = 1024, N = 2048.
+// before are multiplied; rows are loaded into registers two steps ahead, weights three.  In bf16 its time goes
+// with the bytes that a compute unit loads, weights or rows, from the L2 or from memory, at some 24 a
+// nanosecond; that is this kernel's rate (rows pass through registers, all waves meet at a barrier each step,
+// and each 16-byte read of LDS feeds two products), not the memory path's: loads straight to LDS take in 39 to
+// 51 from the L2.  In fp32 its products bound it.  choose_tile picks the tile that needs least of both.  61 to
+// 72 us at 64 rows an expert, E = 32, K = 4096, N = 1536, gated, in bf16 (237 MB and 52 GFLOP; 318 MB read from HBM),
+// 13.7 us at 128 rows, E = 8, K = 1024, N = 2048.  fp32: 93 us at 151 rows, E = 8, K = 2048, N = 1024, gated (10 GFLOP),
+// 35 us at 151 rows, E = 13, K = 1664, N = 192.
+//
+// It is made for the rows of decode batches and short prompts.  us against the bf16 GEMM with bf16 weights, E = 128, d =
+// 2048, f = 1024, in (gated) and out: 99 / 224 and 66 / 118 at 64 rows an expert, 172 / 256 and 117 / 132 at 128, 336 /
+// 360 and 224 / 177 at 256, 677 / 597 and 466 / 314 at 512; at 4096 (E = 8) 299 / 261 and 196 / 136.
 constexpr int kTileRows = 96;
 
 template <typename T>
@@ -706,7 +713,7 @@ hipError_t launch_tile(const W4Args& p, int cap, hipStream_t st) {
   return hipGetLastError();
 }
 
-// What the tiles of a launch cost the busiest compute unit, as bytes that it could load in that time (24 a
+// What the tiles of a launch cost the busiest compute unit, as bytes that this kernel loads in that time (24 a
 // nanosecond), for `waves` waves by up to `cap` 16s of rows, `shares` of the reduction: the bytes of its tiles,
 // in fp32 their products where these take longer (25 operations a byte, of 12 rows more than there are), and
 // 48 KB (2 us) a tile for its first loads and its end, more with two shares or 12 waves; a quarter of the

@@ -65,7 +65,9 @@ and writes h again for wgrad2 (moe_ffn_dgrad2_c8); the combine keeps the routed 
 the layer's input before wgrad1.  Next to ``recompute`` this holds less and runs no GEMM twice, at
 the price of the checkpoint's 8 bits in the gradients (the layer's forward is the same, bit for bit; a
 block's carries one rounding more, see MoEBlock).  Where GEMM1 or dgrad2 does not run bf16 the rows go
-through moe_ckpt8_pack and moe_ckpt8_unpack instead.
+through moe_ckpt8_pack and moe_ckpt8_unpack instead, and an epilogue that writes the checkpoint writes no
+MXFP8 operands: a GEMM that takes them quantises them itself (a step at E = 128, T = 8192, d = 2048, f = 1024
+takes 2.23 ms against 2.17 in bf16, 2.51 against 2.43 with the default MXFP8 scope, 3.34 against 3.19 with all).
 
 4-bit weights (``weights4=True``, serving: no backward): W1, W3, W2 are given as the (codes, scales)
 pairs that ``quantize_weights`` makes, and the expert products are moe_ffn_gemm1_fwd_w4 and
