@@ -6,7 +6,7 @@ import torch
 
 import workloads
 from gpu_common import say, to_dev
-from test_gpu_few_bits_layer import CASES, GRADS, _forward, _layer
+from test_gpu_few_bits_layer import CASES, GRADS, _forward, _layer, _values
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +154,30 @@ def test_weights_of_any_rank_quantise_alike():
             m.quantize_weights(bad)
     empty = m.quantize_weights(w[:0])
     assert empty[0][0].shape == (0, 4, 32)
+
+
+@pytest.mark.parametrize("shared_f", [0, 128])
+@pytest.mark.parametrize("scope", [("GEMM1",), ("DGRAD2",), ("GEMM1", "DGRAD2"), ("GEMM2", "DGRAD1", "WGRAD1"),
+                                   ("GEMM1", "DGRAD2", "WGRAD1", "WGRAD2"), ("GEMM1", "GEMM2", "WGRAD2")], ids="_".join)
+def test_any_mxfp8_scope(scope, shared_f):
+    """Whichever GEMMs run MXFP8: the forward is the plain layer's and the backward the plain one on the values
+    that the checkpoint stands for, bit for bit."""
+    m = _m()
+    say(f"[gpu] ckpt8 scope {scope} shared={shared_f}")
+    T, d, f, E, k = 130, 256, 128, 5, 2
+    bits = sum(getattr(m, "MOE_MX_" + n) for n in scope)
+    g = torch.Generator().manual_seed(bits)
+    r = lambda s, *n: (s * torch.randn(*n, generator=g)).to(torch.bfloat16).cuda()  # noqa: E731
+    x, dy, Wr, W = r(1, T, d), r(1, T, d), r(.06, E, d), (r(.06, E, f, d), r(.06, E, f, d), r(.09, E, d, f))
+    sh = (r(.06, 1, f, d), r(.06, 1, f, d), r(.09, 1, d, f)) if shared_f else None
+    kw = dict(gemm=m.MOE_MXFP8, mx_scope=bits, shared_f=shared_f)
+    A, B = m.MoEExpertLayer(T, d, f, E, k, **kw), m.MoEExpertLayer(T, d, f, E, k, ckpt8=True, **kw)
+    assert torch.equal(A.forward(x, *W, Wr=Wr, shared=sh), B.forward(x, *W, Wr=Wr, shared=sh))
+    A.ab, A.h = _values(m, B.ab_bits, A.dtype, h=True)
+    A.y_perm = _values(m, B.y_bits, A.dtype)
+    if sh:
+        A.ab_s, A.h_s = _values(m, B.ab_bits_s, A.dtype, h=True)
+    A.backward(dy)
+    B.backward(dy)
+    for n in GRADS + ("dlogits", "dWr") + (("dW1s", "dW3s", "dW2s") if sh else ()):
+        assert torch.equal(getattr(A, n), getattr(B, n)), n
