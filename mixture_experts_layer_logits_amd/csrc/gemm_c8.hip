@@ -51,8 +51,8 @@ struct ProbDgrad2C8 : ProbDgrad2 {
 // less with E = 4 (R = 4352 to 15872, d = 2048).
 //
 // The larger tiles that the plain GEMMs take for 1024 rows an expert and more are not built for these epilogues.
-// 256 x 256 (64 deep, two stages): GEMM1 347 against 334 with 128 x 256 at R = 32768, E = 8, d = 2048, f = 1024 (plain 309),
-// but 2115 against 2183 at R = 65536, E = 32, d = 4096, f = 2048 (plain 2117); dgrad2 290 against 232 and 1421 against
+// 256 x 256 (64 deep, two stages): GEMM1 347 against 334 with 128 x 256 at R = 32768, E = 8, d = 2048, f = 1024 (plain
+// 309), but 2115 against 2183 at R = 65536, E = 32, d = 4096, f = 2048 (plain 2117); dgrad2 290 against 232 and 1421 against
 // 1276.  192 x 256 (32 deep, three stages, loader waves): GEMM1 320 and 2158, dgrad2, which spills 28 registers
 // with the codes, 367 and 2336.  There the coded dgrad2 is slower than the plain one, which has those tiles
 // (190 and 1189).

@@ -529,9 +529,9 @@ class MoEBlock:
     again.  A layer with the MXFP8 dispatch writes its routed gradient rows in E4M3 from dy, and one
     with 8-bit checkpoints keeps its routed outputs in the combine, so there the combine and the norm
     are separate calls and y is stored: v and xn_next follow from y rounded to the layer's type
-    instead of from the fp32 sum, and y [T, d] is held until the backward.  Over a layer with 4-bit weights the block serves: it has no
-    backward, and no buffers for one.  The block owns its buffers and holds one forward at a time, like
-    its layer, and its calls run on the current stream."""
+    instead of from the fp32 sum, and y [T, d] is held until the backward.  Over a layer with 4-bit
+    weights the block serves: it has no backward, and no buffers for one.  The block owns its buffers
+    and holds one forward at a time, like its layer, and its calls run on the current stream."""
 
     def __init__(self, layer: MoEExpertLayer, res_scale=1.0, eps=1e-6):
         self.layer, self.res_scale, self.eps = layer, float(res_scale), float(eps)
